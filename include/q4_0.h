@@ -61,7 +61,8 @@ typedef enum {
     Q4_0_ERR_UNSUPPORTED = -2,    /* valid Q4_0 call outside what this build runs */
     Q4_0_ERR_CUDA = -3,           /* a CUDA runtime call or a launch failed */
     Q4_0_ERR_DEVICE_TIMEOUT = -4, /* a kernel gave up on a bounded wait */
-    Q4_0_ERR_WORKSPACE = -5       /* workspace missing or too small */
+    Q4_0_ERR_WORKSPACE = -5,      /* workspace missing or too small */
+    Q4_0_ERR_DEVICE_INDEX = -6    /* a kernel met an index out of range in device memory */
 } q4_0_status;
 
 /* Library version (Q4_0_VERSION). */
@@ -338,11 +339,149 @@ int q4_0_gemm_plan(int64_t M, int64_t N, int64_t K, int *tile_rows, int *splits,
 int q4_0_gemm_noalloc(const uint16_t *x, const uint8_t *wq, float *y,
                       int64_t M, int64_t N, int64_t K, void *stream);
 
+/* ------------------------------------------------------------------------
+ * What a served decoder layer runs between the QKV and the O matmul, and
+ * after the vocabulary matmul: q4_0_kv_append, q4_0_attention and
+ * q4_0_token_logprobs.  They take what q4_0_matmul_ex writes (fp32 or
+ * bfloat16 rows) and give what it reads (bfloat16 rows).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * q4_0_kv_cache -- a paged key and value cache and the batch that extends or
+ * reads it.  Host struct, read during the call only; its pointers are device
+ * memory.
+ *   k, v       : bfloat16, one [kv_heads][page_size][head_dim] block per
+ *                page in any order of the three outer dimensions: element
+ *                (page, head, token, i) is at page * page_stride +
+ *                head * head_stride + token * token_stride + i.  Strides in
+ *                elements, positive multiples of 8 (ignored for a dimension
+ *                of size 1); base addresses 16-byte aligned.
+ *   page_table : int32 [sequences][table_width], rows table_stride apart:
+ *                token j of sequence b is in page
+ *                page_table[b][j / page_size], at j % page_size.  Only
+ *                entries of tokens that a call writes or reads need to hold
+ *                a page.
+ *   q_start    : int32 [sequences + 1], non-decreasing: the new tokens of
+ *                sequence b are rows q_start[b] .. q_start[b + 1] - 1 of the
+ *                batch.  A sequence may have none.  Rows outside
+ *                q_start[0] .. q_start[sequences] - 1 belong to no sequence;
+ *                their outputs are not written.
+ *   kv_len     : int32 [sequences]: tokens of the sequence in the cache,
+ *                the new ones included, at most table_width * page_size.
+ *                Row q_start[b] + i is at position
+ *                kv_len[b] - (q_start[b + 1] - q_start[b]) + i.
+ * Sizes (else UNSUPPORTED): pages <= 2^30, page_size <= 2^20, kv_heads and
+ * head_dim <= 1024, sequences <= 2^20, table_width * page_size <= 2^30.
+ * A page, length or position out of range in device memory is skipped (never
+ * dereferenced) and reported by q4_0_device_error.
+ */
+typedef struct {
+    uint16_t *k, *v;
+    int64_t k_page_stride, k_head_stride, k_token_stride;
+    int64_t v_page_stride, v_head_stride, v_token_stride;
+    int64_t pages, page_size, kv_heads, head_dim;
+    const int32_t *page_table;
+    int64_t table_stride, table_width;
+    const int32_t *q_start, *kv_len;
+    int64_t sequences;
+} q4_0_kv_cache;
+
+/*
+ * q4_0_kv_append -- rotate queries and keys by position; append keys and
+ * values to the cache.
+ *   qkv        : [rows][(q_heads + 2 * kv_heads) * head_dim] of `qkv_type`
+ *                (Q4_0_Y_F32 or Q4_0_Y_BF16), rows qkv_stride elements
+ *                apart: query heads, key heads, value heads.
+ *   cos_sin    : float [positions][rot]: rot / 2 cosines, then rot / 2
+ *                sines.  The first `rot` elements of each query and key head
+ *                are rotated: pair p is elements (p, p + rot / 2), or
+ *                (2p, 2p + 1) when `interleaved`, and becomes
+ *                (a cos - b sin, b cos + a sin).
+ *   row_positions : int32 [rows], the row of cos_sin each row takes; NULL
+ *                for the row's position in its sequence.  The cache slot
+ *                always follows the position in the sequence.
+ *   q_out      : bfloat16 [rows][q_heads][head_dim].
+ * Computed in fp32, rounded once to bfloat16.  head_dim and rot are
+ * multiples of 16 (rot may be 0).  Rows of one call must not share a cache
+ * slot.  Alignment: qkv, its rows, cos_sin and q_out 16 bytes.
+ * Returns Q4_0_OK, Q4_0_ERR_INVALID_ARG, Q4_0_ERR_UNSUPPORTED or
+ * Q4_0_ERR_CUDA.
+ */
+int q4_0_kv_append(const void *qkv, int qkv_type, int64_t qkv_stride, int64_t rows, int64_t q_heads,
+                   const float *cos_sin, int64_t positions, int64_t rot, int interleaved,
+                   const int32_t *row_positions, uint16_t *q_out, const q4_0_kv_cache *cache, void *stream);
+
+/*
+ * q4_0_attention -- causal attention of the batch's rows over the cache (the
+ * rows' own keys and values already appended).
+ *   q          : bfloat16 [rows][q_heads][head_dim], strides in elements,
+ *                multiples of 8; query head h reads key head
+ *                h / (q_heads / kv_heads).
+ *   out        : [rows][q_heads][head_dim] of `out_type`.
+ *   lse        : float [rows][q_heads], natural logarithm of the sum of
+ *                exponentials of the row's scaled scores; or NULL.
+ *   max_q_len  : at least every q_start[b + 1] - q_start[b] (a longer
+ *                sequence is cut to it and reported by q4_0_device_error).
+ *   scale      : > 0, multiplies q . k.
+ *   window     : 0, or the number of latest tokens a row sees, itself
+ *                included; sinks: first tokens it sees all the same.
+ * The row at position t sees the keys j <= t with window == 0 or
+ * j > t - window or j < sinks.  A row that sees none (a position before the
+ * sequence's start) gives 0, and -infinity in lse.  Pages and slots that no
+ * row of the call sees are not read or do not matter, whatever they hold.
+ * A NaN or infinity in a key reaches only the rows that see it; in a value
+ * it can also reach rows less than 256 / (q_heads / kv_heads) tokens earlier
+ * in the same call.
+ * head_dim 64 or 128, q_heads / kv_heads <= 128, page_size a multiple of 8
+ * (else UNSUPPORTED).
+ * Accuracy: scores, softmax statistics and sums in fp32; the exponentials are
+ * rounded to bfloat16 for their product with the values.
+ * Workspace: q4_0_attention_workspace_bytes(...) bytes on the current
+ * device, 256-byte aligned, in use until the work on `stream` completes.
+ * Alignment: q and out 16 bytes.
+ * Returns Q4_0_OK, Q4_0_ERR_INVALID_ARG, Q4_0_ERR_UNSUPPORTED,
+ * Q4_0_ERR_WORKSPACE or Q4_0_ERR_CUDA.
+ */
+size_t q4_0_attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                      int64_t max_q_len);
+int q4_0_attention(const uint16_t *q, int64_t q_row_stride, int64_t q_head_stride, void *out, int out_type,
+                   float *lse, int64_t rows, int64_t q_heads, int64_t max_q_len, float scale, int64_t window,
+                   int64_t sinks, const q4_0_kv_cache *cache, void *workspace, size_t workspace_bytes,
+                   void *stream);
+
+/*
+ * q4_0_token_logprobs -- per row of logits: log probability of a given
+ * token, entropy of the distribution, and the top alternatives.
+ *   logits     : [rows][vocab] of `logits_type` (Q4_0_Y_F32 or Q4_0_Y_BF16),
+ *                rows row_stride elements apart, element-aligned.
+ *   tokens     : int64 [rows], or NULL (logprob is then not written).  A
+ *                negative token means none: logprob 0.
+ *   top        : 0 .. Q4_0_MAX_TOP alternatives, at most vocab.
+ *   logprob    : float [rows]; entropy: float [rows], in nats.
+ *   top_logprob, top_ids : float and int64 [rows][top], largest first, equal
+ *                logits by lowest id (may be NULL when top is 0).
+ * Statistics in fp32.  Logits of -infinity have probability 0 and add
+ * nothing to the entropy.  A row of nothing but -infinity gives -infinity
+ * log probabilities and entropy 0; a NaN or +infinity in a row makes its
+ * logprob, entropy and top_logprob NaN (NaN ranks first).
+ * Workspace: q4_0_token_logprobs_workspace_bytes(rows, vocab, top) bytes on
+ * the current device, 256-byte aligned (may be NULL when that is 0).
+ * Returns Q4_0_OK, Q4_0_ERR_INVALID_ARG, Q4_0_ERR_UNSUPPORTED,
+ * Q4_0_ERR_WORKSPACE or Q4_0_ERR_CUDA.
+ */
+#define Q4_0_MAX_TOP 32
+size_t q4_0_token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int top);
+int q4_0_token_logprobs(const void *logits, int logits_type, int64_t row_stride, int64_t rows, int64_t vocab,
+                        const int64_t *tokens, int top, float *logprob, float *entropy, float *top_logprob,
+                        int64_t *top_ids, void *workspace, size_t workspace_bytes, void *stream);
+
 /*
  * q4_0_device_error -- read and clear the device error word of the current
- * device.  Synchronises the device.  *code receives Q4_0_OK or
+ * device.  Synchronises the device.  *code receives Q4_0_OK,
  * Q4_0_ERR_DEVICE_TIMEOUT (a kernel gave up on a bounded wait and left its
- * output incomplete).  Returns Q4_0_OK or Q4_0_ERR_CUDA.
+ * output incomplete) or Q4_0_ERR_DEVICE_INDEX (a page, length, position or
+ * token that q4_0_kv_append, q4_0_attention or q4_0_token_logprobs read from
+ * device memory is out of range).  Returns Q4_0_OK or Q4_0_ERR_CUDA.
  */
 int q4_0_device_error(int *code);
 

@@ -21,13 +21,14 @@ ERR_UNSUPPORTED = -2
 ERR_CUDA = -3
 ERR_DEVICE_TIMEOUT = -4
 ERR_WORKSPACE = -5
+ERR_DEVICE_INDEX = -6
 
 # Output element types of q4_0_matmul_ex (include/q4_0.h).
 Y_F32 = 0
 Y_BF16 = 1
 
 # Every entry point the header declares, with its ctypes signature.
-_P, _I64, _SZ, _INT = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+_P, _I64, _SZ, _INT, _F32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
 SIGNATURES = {
     "q4_0_version": ([], _INT),
     "q4_0_status_string": ([_INT], ctypes.c_char_p),
@@ -48,6 +49,11 @@ SIGNATURES = {
     "q4_0_gemm": ([_P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P], _INT),
     "q4_0_gemm_noalloc": ([_P, _P, _P, _I64, _I64, _I64, _P], _INT),
     "q4_0_gemm_plan": ([_I64, _I64, _I64, _P, _P, _P], _INT),
+    "q4_0_kv_append": ([_P, _INT, _I64, _I64, _I64, _P, _I64, _I64, _INT, _P, _P, _P, _P], _INT),
+    "q4_0_attention_workspace_bytes": ([_I64, _I64, _I64, _I64, _I64], _SZ),
+    "q4_0_attention": ([_P, _I64, _I64, _P, _INT, _P, _I64, _I64, _I64, _F32, _I64, _I64, _P, _P, _SZ, _P], _INT),
+    "q4_0_token_logprobs_workspace_bytes": ([_I64, _I64, _INT], _SZ),
+    "q4_0_token_logprobs": ([_P, _INT, _I64, _I64, _I64, _P, _INT, _P, _P, _P, _P, _P, _SZ, _P], _INT),
     "q4_0_selftest_wait_timeout": ([_I64, _P], _INT),
     "q4_0_device_error": ([ctypes.POINTER(_INT)], _INT),
 }

@@ -1,6 +1,6 @@
 """Build libq4_0.so in-tree with nvcc for sm_103a.
 
-The four translation units compile in parallel; the shared library links the
+The translation units compile in parallel; the shared library links the
 CUDA runtime statically, so it loads on a machine without a GPU (the driver
 is reached at run time through cudaGetDriverEntryPointByVersion).  ptxas
 register/spill reports go to ``_build/ptxas.log``.
@@ -15,7 +15,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "lib", "libq4_0.so")
-SOURCES = ["api.cu", "quantize.cu", "gemv.cu", "gemv_tc.cu", "gemm.cu", "noalloc.cu", "pad.cu"]
+SOURCES = ["api.cu", "quantize.cu", "gemv.cu", "gemv_tc.cu", "gemm.cu", "noalloc.cu", "pad.cu", "kv_append.cu", "attention.cu",
+           "logprobs.cu"]
 HEADERS = ["q4_0_internal.h", "q4_0_ptx.cuh"]
 PUBLIC_HEADER = os.path.join(os.path.dirname(HERE), "include", "q4_0.h")
 

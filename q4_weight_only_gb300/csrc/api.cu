@@ -157,6 +157,7 @@ const char *q4_0_status_string(int status) {
         case Q4_0_ERR_CUDA: return "CUDA error";
         case Q4_0_ERR_DEVICE_TIMEOUT: return "device wait timed out";
         case Q4_0_ERR_WORKSPACE: return "workspace missing or too small";
+        case Q4_0_ERR_DEVICE_INDEX: return "an index in device memory was out of range";
         default: return "unknown status";
     }
 }
@@ -432,6 +433,155 @@ int q4_0_matmul_host(const uint16_t *x_host, const uint8_t *wq, void *y_host, in
     return from_cuda(cudaMemcpyAsync(y_host, yd, ybytes, cudaMemcpyDeviceToHost, s));
 }
 
+namespace {
+bool y_type_ok(int t) { return t == Q4_0_Y_F32 || t == Q4_0_Y_BF16; }
+
+// A q4_0_kv_cache as the kernels take it; a status code.
+int cache_view(const q4_0_kv_cache *c, KvCacheView *v) {
+    if (!c || !c->k || !c->v || !c->page_table || !c->q_start || !c->kv_len) return Q4_0_ERR_INVALID_ARG;
+    if (c->pages < 1 || c->page_size < 1 || c->kv_heads < 1 || c->head_dim < 1 || c->sequences < 0 ||
+        c->table_width < 1 || c->table_stride < c->table_width)
+        return Q4_0_ERR_INVALID_ARG;
+    if (!aligned16(c->k) || !aligned16(c->v) || (reinterpret_cast<uintptr_t>(c->page_table) & 3u) ||
+        (reinterpret_cast<uintptr_t>(c->q_start) & 3u) || (reinterpret_cast<uintptr_t>(c->kv_len) & 3u))
+        return Q4_0_ERR_INVALID_ARG;
+    if (c->pages > (1ll << 30) || c->page_size > (1ll << 20) || c->kv_heads > 1024 || c->head_dim > 1024 ||
+        c->sequences > (1ll << 20) || c->table_width > (1ll << 30) / c->page_size)
+        return Q4_0_ERR_UNSUPPORTED;
+    const int64_t size[3] = {c->pages, c->kv_heads, c->page_size};
+    const int64_t ks[3] = {c->k_page_stride, c->k_head_stride, c->k_token_stride};
+    const int64_t vs[3] = {c->v_page_stride, c->v_head_stride, c->v_token_stride};
+    for (int i = 0; i < 3; ++i) {
+        // the stride of a dimension of one element is never used
+        v->k_stride[i] = size[i] == 1 ? 8 : ks[i];
+        v->v_stride[i] = size[i] == 1 ? 8 : vs[i];
+        if (v->k_stride[i] < 1 || v->v_stride[i] < 1 || v->k_stride[i] % 8 || v->v_stride[i] % 8)
+            return Q4_0_ERR_INVALID_ARG;
+        if (v->k_stride[i] >= (1ll << 38) || v->v_stride[i] >= (1ll << 38)) return Q4_0_ERR_UNSUPPORTED;
+    }
+    v->k = reinterpret_cast<__nv_bfloat16 *>(c->k);
+    v->v = reinterpret_cast<__nv_bfloat16 *>(c->v);
+    v->page_table = c->page_table, v->q_start = c->q_start, v->kv_len = c->kv_len;
+    v->table_stride = c->table_stride;
+    v->pages = (int)c->pages, v->page_size = (int)c->page_size, v->kv_heads = (int)c->kv_heads;
+    v->head_dim = (int)c->head_dim, v->table_width = (int)c->table_width, v->sequences = (int)c->sequences;
+    return Q4_0_OK;
+}
+}  // namespace
+
+int q4_0_kv_append(const void *qkv, int qkv_type, int64_t qkv_stride, int64_t rows, int64_t q_heads,
+                   const float *cos_sin, int64_t positions, int64_t rot, int interleaved,
+                   const int32_t *row_positions, uint16_t *q_out, const q4_0_kv_cache *cache, void *stream) {
+    KvCacheView c;
+    const int st = cache_view(cache, &c);
+    if (st != Q4_0_OK) return st;
+    if (!qkv || !cos_sin || !q_out || !y_type_ok(qkv_type) || rows < 0 || q_heads < 1 || positions < 1)
+        return Q4_0_ERR_INVALID_ARG;
+    if (rot < 0 || rot > c.head_dim || rot % 16 || c.head_dim % 16) return Q4_0_ERR_INVALID_ARG;
+    if (rows > (1ll << 30) || q_heads > 4096 || positions > (1ll << 30) || qkv_stride > (1ll << 32))
+        return Q4_0_ERR_UNSUPPORTED;
+    const int64_t vec = qkv_type == Q4_0_Y_BF16 ? 8 : 4;  // elements of 16 bytes
+    if (qkv_stride < (q_heads + 2 * c.kv_heads) * c.head_dim || qkv_stride % vec) return Q4_0_ERR_INVALID_ARG;
+    if (!aligned16(qkv) || !aligned16(cos_sin) || !aligned16(q_out) ||
+        (reinterpret_cast<uintptr_t>(row_positions) & 3u))
+        return Q4_0_ERR_INVALID_ARG;
+    if (rows == 0 || c.sequences == 0) return Q4_0_OK;
+    unsigned int *err = device_error_word();
+    if (!err) return Q4_0_ERR_CUDA;
+    const KvAppendArgs a{qkv,           qkv_stride, cos_sin, row_positions, reinterpret_cast<__nv_bfloat16 *>(q_out),
+                         (int)q_heads, (int)positions, (int)rot, interleaved != 0};
+    return from_cuda(launch_kv_append(a, c, rows, qkv_type == Q4_0_Y_BF16, static_cast<cudaStream_t>(stream), err));
+}
+
+namespace {
+// Head layouts and lengths the attention kernel runs; a status code.
+int attention_sizes(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_q_len) {
+    if (rows < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads || max_q_len < 1) return Q4_0_ERR_INVALID_ARG;
+    if ((head_dim != 64 && head_dim != 128) || q_heads / kv_heads > 128 || q_heads > 4096 || rows > (1ll << 30) ||
+        max_q_len > (1ll << 30))
+        return Q4_0_ERR_UNSUPPORTED;
+    return Q4_0_OK;
+}
+}  // namespace
+
+size_t q4_0_attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                      int64_t max_q_len) {
+    if (rows < 1 || attention_sizes(rows, q_heads, kv_heads, head_dim, max_q_len) != Q4_0_OK) return 0;
+    return attention_workspace_bytes((int)q_heads, (int)kv_heads, (int)head_dim,
+                                     (int)(max_q_len < rows ? max_q_len : rows));
+}
+
+int q4_0_attention(const uint16_t *q, int64_t q_row_stride, int64_t q_head_stride, void *out, int out_type,
+                   float *lse, int64_t rows, int64_t q_heads, int64_t max_q_len, float scale, int64_t window,
+                   int64_t sinks, const q4_0_kv_cache *cache, void *workspace, size_t workspace_bytes,
+                   void *stream) {
+    KvCacheView c;
+    int st = cache_view(cache, &c);
+    if (st != Q4_0_OK) return st;
+    if (!q || !out || !y_type_ok(out_type) || window < 0 || sinks < 0 || !(scale > 0.f) || scale > 1e30f)
+        return Q4_0_ERR_INVALID_ARG;
+    st = attention_sizes(rows, q_heads, c.kv_heads, c.head_dim, max_q_len);
+    if (st != Q4_0_OK) return st;
+    if (c.page_size % 8) return Q4_0_ERR_UNSUPPORTED;
+    const int64_t hs = q_heads == 1 ? 8 : q_head_stride, rs = rows <= 1 ? 8 : q_row_stride;
+    if (hs < 1 || rs < 1 || hs % 8 || rs % 8) return Q4_0_ERR_INVALID_ARG;
+    if (hs >= (1ll << 30) || rs >= (1ll << 38)) return Q4_0_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return Q4_0_ERR_INVALID_ARG;
+    if (rows == 0 || c.sequences == 0) return Q4_0_OK;
+    const size_t need = q4_0_attention_workspace_bytes(rows, q_heads, c.kv_heads, c.head_dim, max_q_len);
+    if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return Q4_0_ERR_WORKSPACE;
+    unsigned int *err = device_error_word();
+    if (!err) return Q4_0_ERR_CUDA;
+    const int64_t most = 1ll << 30;
+    AttentionArgs a{};
+    a.q = reinterpret_cast<const __nv_bfloat16 *>(q);
+    a.q_row_stride = rs, a.q_head_stride = hs;
+    a.out = out, a.out_bf16 = out_type == Q4_0_Y_BF16, a.lse = lse;
+    a.rows = (int)rows, a.q_heads = (int)q_heads, a.max_q_len = (int)(max_q_len < rows ? max_q_len : rows);
+    a.window = (int)(window < most ? window : most), a.sinks = (int)(sinks < most ? sinks : most);
+    a.scale = scale;
+    return from_cuda(launch_attention(a, c, workspace, static_cast<cudaStream_t>(stream), err));
+}
+
+namespace {
+int logprobs_sizes(int64_t rows, int64_t vocab, int top) {
+    if (rows < 0 || vocab < 1 || top < 0 || top > vocab) return Q4_0_ERR_INVALID_ARG;
+    if (top > Q4_0_MAX_TOP || rows > (1ll << 30) || vocab > (1ll << 30)) return Q4_0_ERR_UNSUPPORTED;
+    return Q4_0_OK;
+}
+}  // namespace
+
+size_t q4_0_token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int top) {
+    if (rows < 1 || logprobs_sizes(rows, vocab, top) != Q4_0_OK) return 0;
+    return token_logprobs_workspace_bytes((int)rows, (int)vocab, top);
+}
+
+int q4_0_token_logprobs(const void *logits, int logits_type, int64_t row_stride, int64_t rows, int64_t vocab,
+                        const int64_t *tokens, int top, float *logprob, float *entropy, float *top_logprob,
+                        int64_t *top_ids, void *workspace, size_t workspace_bytes, void *stream) {
+    const int st = logprobs_sizes(rows, vocab, top);
+    if (st != Q4_0_OK) return st;
+    if (!logits || !y_type_ok(logits_type) || !entropy || (tokens && !logprob) || (top && (!top_logprob || !top_ids)))
+        return Q4_0_ERR_INVALID_ARG;
+    if (rows > 1 && row_stride < vocab) return Q4_0_ERR_INVALID_ARG;
+    const uintptr_t element = logits_type == Q4_0_Y_BF16 ? 2 : 4;
+    if (reinterpret_cast<uintptr_t>(logits) % element || (reinterpret_cast<uintptr_t>(tokens) & 7u) ||
+        (reinterpret_cast<uintptr_t>(top_ids) & 7u) || (reinterpret_cast<uintptr_t>(logprob) & 3u) ||
+        (reinterpret_cast<uintptr_t>(entropy) & 3u) || (reinterpret_cast<uintptr_t>(top_logprob) & 3u))
+        return Q4_0_ERR_INVALID_ARG;
+    if (rows == 0) return Q4_0_OK;
+    const size_t need = q4_0_token_logprobs_workspace_bytes(rows, vocab, top);
+    if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+        return Q4_0_ERR_WORKSPACE;
+    unsigned int *err = device_error_word();
+    if (!err) return Q4_0_ERR_CUDA;
+    const LogprobArgs a{logits,      row_stride, tokens,    logprob,    entropy,
+                        top_logprob, top_ids,    (int)rows, (int)vocab, top};
+    return from_cuda(
+        launch_token_logprobs(a, logits_type == Q4_0_Y_BF16, workspace, static_cast<cudaStream_t>(stream), err));
+}
+
 int q4_0_selftest_wait_timeout(int64_t limit_us, void *stream) {
     if (limit_us < 1 || limit_us > 1000000) return Q4_0_ERR_INVALID_ARG;
     unsigned int *err = device_error_word();
@@ -449,7 +599,7 @@ int q4_0_device_error(int *code) {
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(g_device_error_word, &zero, sizeof zero) != cudaSuccess)
         return Q4_0_ERR_CUDA;
-    *code = v ? Q4_0_ERR_DEVICE_TIMEOUT : Q4_0_OK;
+    *code = v == kErrBadIndex ? Q4_0_ERR_DEVICE_INDEX : v ? Q4_0_ERR_DEVICE_TIMEOUT : Q4_0_OK;
     return Q4_0_OK;
 }
 

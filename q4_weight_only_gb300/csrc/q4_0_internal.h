@@ -2,6 +2,7 @@
 // libq4_0.so (not part of the public ABI).
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -104,5 +105,55 @@ bool gemm_shape_supported(int64_t M, int64_t N, int64_t K);
 size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int splits);
 cudaError_t launch_gemm(const uint16_t *x, const uint8_t *wq, float *y, bool ybf16, int64_t M, int64_t N,
                         int64_t K, void *workspace, int splits, cudaStream_t s, unsigned int *err);
+
+// The paged cache and the batch that reads or extends it, as the kernels see
+// them (q4_0_kv_cache of include/q4_0.h, checked): strides in elements for
+// {page, head, token}.
+struct KvCacheView {
+    __nv_bfloat16 *k, *v;
+    int64_t k_stride[3], v_stride[3];
+    const int32_t *page_table, *q_start, *kv_len;
+    int64_t table_stride;
+    int pages, page_size, kv_heads, head_dim, table_width, sequences;
+};
+
+struct KvAppendArgs {
+    const void *qkv;  // fp32 or bfloat16 rows, qkv_stride elements apart
+    int64_t qkv_stride;
+    const float *cos_sin;  // [positions][rot]: cosines, then sines
+    const int32_t *row_positions;
+    __nv_bfloat16 *q_out;
+    int q_heads, positions, rot, interleaved;
+};
+
+cudaError_t launch_kv_append(const KvAppendArgs &a, const KvCacheView &c, int64_t rows, bool bf16, cudaStream_t s,
+                             unsigned int *err);
+
+struct AttentionArgs {
+    const __nv_bfloat16 *q;
+    int64_t q_row_stride, q_head_stride;  // elements
+    void *out;                            // fp32 or bfloat16 [rows][q_heads][head_dim]
+    float *lse;                           // [rows][q_heads], or null
+    int rows, q_heads, max_q_len, window, sinks, out_bf16;
+    float scale;
+};
+
+// attention_workspace_bytes depends on the device's SM count.
+size_t attention_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q_len);
+cudaError_t launch_attention(const AttentionArgs &a, const KvCacheView &c, void *workspace, cudaStream_t s,
+                             unsigned int *err);
+
+struct LogprobArgs {
+    const void *logits;  // fp32 or bfloat16 rows, row_stride elements apart
+    int64_t row_stride;
+    const int64_t *tokens;
+    float *logprob, *entropy, *top_logprob;
+    int64_t *top_ids;
+    int rows, vocab, top;
+};
+
+size_t token_logprobs_workspace_bytes(int rows, int vocab, int top);
+cudaError_t launch_token_logprobs(const LogprobArgs &a, bool bf16, void *workspace, cudaStream_t s,
+                                  unsigned int *err);
 
 }  // namespace q4_0

@@ -13,6 +13,7 @@ namespace q4_0 {
 // Reason a kernel stores in the device error word (passed to every kernel
 // as a pointer; read back by q4_0_device_error()) when it gives up.
 constexpr unsigned int kErrWaitTimeout = 1;
+constexpr unsigned int kErrBadIndex = 2;  // a page, position or token read from device memory is out of range
 
 // A wait that has not finished after this many nanoseconds is abandoned.
 // Every legitimate wait in these kernels lasts microseconds.
@@ -176,6 +177,16 @@ __device__ __forceinline__ void tma_load_2d_hint(void *dst, const CUtensorMap *m
         : "memory");
 }
 
+// 4-D tiled tensor copy.  Out-of-range coordinates read zeros.
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int32_t c0, int32_t c1, int32_t c2,
+                                            int32_t c3, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+        : "memory");
+}
+
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -188,6 +199,21 @@ __device__ __forceinline__ void store_y(float *y, int64_t i, float v, bool bf16)
         reinterpret_cast<__nv_bfloat16 *>(y)[i] = __float2bfloat16_rn(v);
     else
         y[i] = v;
+}
+
+// Two fp32 values as a bfloat16 pair, rounded to nearest even, `lo` in the
+// low half.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// 2^x (approximate, subnormal results flushed to zero).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // ------------------------------------------------- nibble unpack helper
@@ -241,6 +267,17 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, kind::f16.
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -358,6 +395,26 @@ __device__ __forceinline__ uint64_t smem_desc_k128(const void *tile) {
     d |= (uint64_t)1 << 46;                 // descriptor version
     d |= (uint64_t)2 << 61;                 // 128-byte swizzle
     return d;
+}
+
+// The same tile read as an MN-major operand: the 128-byte rows are steps of
+// k, 8-row groups 1024 bytes apart, and the next 64 elements of the M or N
+// extent start `block` bytes further.
+__device__ __forceinline__ uint64_t smem_desc_mn128(const void *tile, uint32_t block) {
+    const uint64_t addr = smem_u32(tile);
+    uint64_t d = 0;
+    d |= (addr & 0x3FFFFull) >> 4;
+    d |= (uint64_t)(block >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// Instruction descriptor, kind::f16 with bfloat16 A and B, fp32 D; B is
+// K-major, or MN-major when `b_mn`.
+__host__ __device__ constexpr uint32_t idesc_bf16_f32(uint32_t M, uint32_t N, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
 // Instruction descriptor, kind::f16: fp16 A and B (both K-major), fp32 D,
