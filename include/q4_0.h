@@ -438,7 +438,7 @@ int q4_0_kv_append(const void *qkv, int qkv_type, int64_t qkv_stride, int64_t ro
  * rounded to bfloat16 for their product with the values.
  * Workspace: q4_0_attention_workspace_bytes(...) bytes on the current
  * device, 256-byte aligned, in use until the work on `stream` completes.
- * Alignment: q and out 16 bytes.
+ * Alignment: q 16 bytes, out 32 bytes.
  * Returns Q4_0_OK, Q4_0_ERR_INVALID_ARG, Q4_0_ERR_UNSUPPORTED,
  * Q4_0_ERR_WORKSPACE or Q4_0_ERR_CUDA.
  */

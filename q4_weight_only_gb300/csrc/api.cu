@@ -526,7 +526,8 @@ int q4_0_attention(const uint16_t *q, int64_t q_row_stride, int64_t q_head_strid
     const int64_t hs = q_heads == 1 ? 8 : q_head_stride, rs = rows <= 1 ? 8 : q_row_stride;
     if (hs < 1 || rs < 1 || hs % 8 || rs % 8) return Q4_0_ERR_INVALID_ARG;
     if (hs >= (1ll << 30) || rs >= (1ll << 38)) return Q4_0_ERR_UNSUPPORTED;
-    if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return Q4_0_ERR_INVALID_ARG;
+    if (!aligned16(q) || (reinterpret_cast<uintptr_t>(out) & 31u) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+        return Q4_0_ERR_INVALID_ARG;
     if (rows == 0 || c.sequences == 0) return Q4_0_OK;
     const size_t need = q4_0_attention_workspace_bytes(rows, q_heads, c.kv_heads, c.head_dim, max_q_len);
     if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))

@@ -22,15 +22,19 @@
 // like; an item that a share's boundary cuts leaves partial results that
 // attention_join_kernel adds in share order, so results are deterministic.
 //
-// Warps: 0 copies Q and the ring of K and V tiles (TMA; page boxes that no
-// query sees are not read: an out-of-range page coordinate fills zeros),
-// 1 issues the MMAs, 2-5 and 6-9 do the softmax of tile A and of tile B, one
-// thread per row, S and P in tensor memory.  While one tile is in softmax
-// the tensor cores work on the other.
+// Warps: 0 copies Q and K tiles and 2 V tiles into a ring (TMA; page boxes
+// that no query sees are not read: an out-of-range page coordinate fills
+// zeros), 1 issues the MMAs, 3 hands out the items, 4-7 and 8-11 do the softmax of group A
+// and of group B, one thread per row, S and P in tensor memory.  While one
+// group is in softmax the tensor cores work on the other.  In an item of two
+// tiles a group has one tile each; in a narrow item (one tile: single tokens,
+// drafts, a chunk's end) the groups take the key tiles in turn, and group A
+// adds B's O to its own at the end.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "q4_0_internal.h"
 #include "q4_0_ptx.cuh"
@@ -40,8 +44,10 @@ namespace q4_0 {
 namespace {
 
 constexpr int kTile = 128;      // rows of a tile, and tokens of a key tile
-constexpr int kThreads = 320;
-constexpr int kStages = 5;      // K or V tiles in the ring
+constexpr int kThreads = 384;
+// registers a thread: the launch gives 168 each; the copy and MMA warps give
+// theirs up to the softmax warps (128 * 56 + 256 * 224 = 384 * 168)
+constexpr int kRoleRegs = 56, kSoftmaxRegs = 224;
 constexpr int kStatBytes = 2048;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -70,6 +76,11 @@ struct Params {
 constexpr int kHeadPiece = 1;     // its first piece continues an item of an earlier CTA
 constexpr int kHeadGoesOn = 2;    // ... which also goes on in the next CTA
 constexpr int kTailPiece = 4;     // its last piece starts an item that goes on in the next CTA
+
+// Bits 0 .. n - 1.
+__device__ __forceinline__ uint32_t below(int n) {
+    return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1;
+}
 
 // One sequence of the batch, clamped to what the arrays can hold.
 struct Sequence {
@@ -119,115 +130,137 @@ __device__ __forceinline__ Range item_range(const Params &p, const Sequence &s, 
     return r;
 }
 
-__device__ __forceinline__ int key_tile(const Range &r, int t) { return t < r.sink_tiles ? t : r.wtile + t - r.sink_tiles; }
-
-// A CTA's share of the key tiles, item by item; every warp walks it alike.
-struct Cursor {
-    int head, b, item;   // the current item
-    int t0, t1;          // its key tiles in this share
-    int64_t left;        // key tiles of the share from t0 on
-    Sequence s;
-    Range r;
-
-    __device__ __forceinline__ void enter(const Params &p) {
-        r = item_range(p, s, item);
-        t1 = (int)min((int64_t)r.n, t0 + left);
-    }
-    // Next item with work; false at the end of the share.
-    __device__ __forceinline__ bool next(const Params &p) {
-        left -= t1 - t0;
-        if (left <= 0) return false;
-        t0 = 0;
-        if (++item >= items_of(p, s)) {
-            item = 0;
-            int scanned = 0;
-            do {
-                if (++b >= p.sequences) {
-                    b = 0;
-                    ++head;
-                }
-                s = sequence(p, b);
-            } while (s.len == 0 && ++scanned <= p.sequences);
-            if (s.len == 0) return false;
-        }
-        enter(p);
-        return true;
-    }
+// A CTA's part of an item, as warp 3 hands it to the others.
+struct Item {
+    int t0, t1, n;       // its key tiles [t0, t1) of the item's n; t0 == t1: the share has ended
+    int head, b;         // key head and sequence
+    int row0, tokens;    // first row of q, and tokens
+    int pos0;            // position of the first
+    int lo, hi, sink_end, sink_tiles, wtile;  // as in Range
+    __device__ __forceinline__ int key_tile(int t) const { return t < sink_tiles ? t : wtile + t - sink_tiles; }
 };
 
 struct Start {
     int64_t left;
     int head, b, item, t0;
+    Sequence s;
     int64_t warp_sum[kThreads / 32];
 };
 
-// Key tiles of a sequence (one key head).
-__device__ __forceinline__ int64_t sequence_tiles(const Params &p, const Sequence &s) {
+__device__ __forceinline__ Sequence shuffle(const Sequence &s, int lane) {
+    return Sequence{__shfl_sync(0xffffffffu, s.row0, lane), __shfl_sync(0xffffffffu, s.len, lane),
+                    __shfl_sync(0xffffffffu, s.kv, lane)};
+}
+
+// Key tiles (of one key head) of each lane's sequence; the warp takes the
+// items of a long one together.
+__device__ __forceinline__ int64_t sequence_tiles(const Params &p, const Sequence &s, int lane) {
     const int n = items_of(p, s);
-    int64_t sum = 0;
-    for (int i = 0; i < n; ++i) sum += item_range(p, s, i).n;
-    return sum;
+    int64_t mine = n == 1 ? item_range(p, s, 0).n : 0;
+    for (uint32_t many = __ballot_sync(0xffffffffu, n > 1); many; many &= many - 1) {
+        const int src = __ffs(many) - 1;
+        const Sequence t = shuffle(s, src);
+        const int nt = items_of(p, t);
+        int64_t sum = 0;
+        for (int i = lane; i < nt; i += 32) sum += item_range(p, t, i).n;
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane == src) mine = sum;
+    }
+    return mine;
+}
+
+template <typename T>
+__device__ __forceinline__ T warp_inclusive(T v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const T o = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
+// floor(all * i / n) without a product past 64 bits.
+template <typename T>
+__device__ __forceinline__ T share_start(T all, T n, T i) {
+    const T each = all / n;
+    return each * i + (all - each * n) * i / n;
 }
 
 // Where this CTA's share begins.  Called by all threads; the result is in
 // `st` after the call.
 __device__ __forceinline__ void locate(const Params &p, Start &st, int cta, int ctas) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int64_t goal = -1;  // the share's first tile within its key head, from the second pass on
-    int64_t left = 0;
-    int head = 0;
-    for (int pass = 0; pass < 2; ++pass) {
-        int64_t before = 0;  // tiles of the sequences ahead of this round's
-        for (int b0 = 0; b0 < p.sequences; b0 += kThreads) {
-            const int b = b0 + tid;
-            Sequence s{0, 0, 0};
-            if (b < p.sequences) {
-                s = sequence(p, b);
-                if (pass == 0 && cta == 0 && !sequence_fits(p, s, b)) atomicExch(p.err, kErrBadIndex);
-            }
-            const int64_t mine = sequence_tiles(p, s);
-            int64_t incl = mine;
+    Sequence s;
+    int64_t mine, first;  // key tiles of this thread's sequence, and of the ones before it
+    int64_t before = 0;   // key tiles of earlier rounds' sequences
+    // a round: one sequence a thread
+    auto round = [&](int b0) {
+        const int b = b0 + tid;
+        s = Sequence{0, 0, 0};
+        if (b < p.sequences) s = sequence(p, b);
+        mine = sequence_tiles(p, s, lane);
+        const int64_t incl = warp_inclusive(mine, lane);
+        if (lane == 31) st.warp_sum[warp] = incl;
+        __syncthreads();
+        int64_t sum = 0, ahead = 0;
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
-                if (lane >= d) incl += o;
-            }
-            if (lane == 31) st.warp_sum[warp] = incl;
-            __syncthreads();
-            int64_t sum = 0, ahead = 0;
-#pragma unroll
-            for (int w = 0; w < kThreads / 32; ++w) {
-                const int64_t v = st.warp_sum[w];
-                if (w < warp) ahead += v;
-                sum += v;
-            }
-            __syncthreads();
-            const int64_t first = before + ahead + incl - mine;
-            if (pass == 1 && goal >= first && goal < first + mine) {
-                int64_t rest = goal - first;
-                int it = 0;
-                for (;; ++it) {
-                    const int n = item_range(p, s, it).n;
-                    if (rest < n) break;
-                    rest -= n;
-                }
-                st.head = head, st.b = b, st.item = it, st.t0 = (int)rest, st.left = left;
-            }
-            before += sum;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            const int64_t v = st.warp_sum[w];
+            if (w < warp) ahead += v;
+            sum += v;
         }
-        if (pass == 0) {
-            const int64_t all = before * p.kv_heads;
-            // no share is empty before the last one that is not: an item's
-            // pieces are in consecutive CTAs
-            const int64_t n = min(all, (int64_t)ctas);
-            if (cta >= n) {
-                if (tid == 0) st.left = 0;
-                break;
+        __syncthreads();
+        first = before + ahead + incl - mine;
+        before += sum;
+        return b;
+    };
+    for (int b0 = 0; b0 < p.sequences; b0 += kThreads) {
+        const int b = round(b0);
+        if (cta == 0 && b < p.sequences && !sequence_fits(p, s, b)) atomicExch(p.err, kErrBadIndex);
+    }
+    const int64_t each = before, all = each * p.kv_heads;
+    // no share is empty before the last one that is not: an item's pieces are
+    // in consecutive CTAs
+    const int64_t n = min(all, (int64_t)ctas);
+    if (cta >= n) {
+        if (tid == 0) st.left = 0;
+        __syncthreads();
+        return;
+    }
+    int64_t u0, u1;
+    int head;
+    if (all < (1ll << 31)) {
+        u0 = share_start<uint32_t>((uint32_t)all, (uint32_t)n, cta);
+        u1 = share_start<uint32_t>((uint32_t)all, (uint32_t)n, cta + 1);
+        head = (int)((uint32_t)u0 / (uint32_t)each);
+    } else {
+        u0 = share_start<int64_t>(all, n, cta);
+        u1 = share_start<int64_t>(all, n, cta + 1);
+        head = (int)(u0 / each);
+    }
+    const int64_t goal = u0 - head * each;  // the share's first tile within its key head
+    const bool again = p.sequences > kThreads;
+    before = 0;
+    for (int b0 = 0; b0 < p.sequences; b0 += kThreads) {
+        if (again) round(b0);
+        const uint32_t hit = __ballot_sync(0xffffffffu, goal >= first && goal < first + mine);
+        if (!hit) continue;
+        // the warp that has the sequence looks through its items
+        const int src = __ffs(hit) - 1;
+        const Sequence t = shuffle(s, src);
+        const int nt = items_of(p, t);
+        int64_t rest = goal - __shfl_sync(0xffffffffu, first, src);
+        for (int i0 = 0; i0 < nt; i0 += 32) {
+            const int k = i0 + lane < nt ? item_range(p, t, i0 + lane).n : 0;
+            const int64_t incl = warp_inclusive((int64_t)k, lane);
+            if (rest >= incl - k && rest < incl) {
+                st.head = head, st.b = b0 + warp * 32 + src, st.item = i0 + lane, st.t0 = (int)(rest - (incl - k));
+                st.left = u1 - u0, st.s = t;
             }
-            const int64_t u0 = all / n * cta + all % n * cta / n;
-            left = all / n * (cta + 1) + all % n * (cta + 1) / n - u0;
-            head = (int)(u0 / before);
-            goal = u0 - head * before;
+            const int64_t sum = __shfl_sync(0xffffffffu, incl, 31);
+            if (rest < sum) break;
+            rest -= sum;
         }
     }
     __syncthreads();
@@ -238,22 +271,32 @@ struct Layout {
     static constexpr int kHalves = D / 64;                 // 64-element column blocks
     static constexpr int kTileBytes = kTile * D * 2;
     static constexpr int kBlock = kTile * 128;             // bytes of one column block
+    static constexpr int kStages = D == 128 ? 5 : 10;      // K or V tiles in the ring
     static constexpr int kQ = 0;
     static constexpr int kRing = 2 * kTileBytes;
     static constexpr int kBars = kRing + kStages * kTileBytes;
     static constexpr int kSmem = kBars + kStatBytes + 1024;  // + alignment
 };
 
+constexpr int kItems = 4;     // items handed out ahead
+constexpr int kReaders = 11;  // warps that read them
+
+template <int kStages>
 struct Bars {
     uint64_t full[kStages], empty[kStages];
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t b_done, merged;  // narrow items: B's O and (m, l) are ready; A has read them
+    uint64_t item_full[kItems], item_empty[kItems];
     uint64_t drain;
+    Item item[kItems];
+    float2 ml[kTile];
     uint32_t tmem;
+    uint32_t fills[2], q_fills;  // copies made: past the last K and V tile's ring position, and of Q
     int abort;
     Start start;
 };
-static_assert(sizeof(Bars) <= kStatBytes, "");
+static_assert(sizeof(Bars<10>) <= kStatBytes, "");
 
 // Tensor memory columns.
 constexpr uint32_t kTmemCols = 512;
@@ -269,7 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
     uint8_t *ring = smem + L::kRing;
-    Bars &bar = *reinterpret_cast<Bars *>(smem + L::kBars);
+    constexpr int kStages = L::kStages;
+    Bars<kStages> &bar = *reinterpret_cast<Bars<kStages> *>(smem + L::kBars);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int *abort_flag = &bar.abort;
 
@@ -286,6 +330,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bar.p_full[g], 4);
             mbar_init(&bar.o_full[g], 1);
         }
+        mbar_init(&bar.b_done, 4);
+        mbar_init(&bar.merged, 4);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&bar.item_full[i], 1);
+            mbar_init(&bar.item_empty[i], kReaders);
+        }
         mbar_init(&bar.drain, 1);
         bar.abort = 0;
         mbar_fence_init();
@@ -301,94 +351,146 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
 
-    Cursor cur;
-    cur.left = bar.start.left;
-    bool work = cur.left > 0;
-    if (work) {
-        cur.head = bar.start.head, cur.b = bar.start.b, cur.item = bar.start.item, cur.t0 = bar.start.t0;
-        cur.s = sequence(p, cur.b);
-        cur.enter(p);
-    }
+    // The next item of the share, or false at its end or when a wait was
+    // abandoned; done_item() hands its record back.
+    uint32_t items = 0;
+    Item cur;
+    auto next_item = [&]() {
+        const int i = items % kItems;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bar.item_full[i], items / kItems & 1, abort_flag, p.err))) return false;
+        cur = bar.item[i];
+        return cur.t0 < cur.t1;
+    };
+    auto done_item = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.item_empty[items % kItems]);
+        ++items;
+    };
 
-    if (warp == 0) {
-        // ---------------------------------------------------- copies
-        uint32_t fills = 0;  // K and V tiles copied so far
-        uint32_t items = 0;
-        bool ok = true;
-        const int boxes = kTile / p.box;
-        for (; work && ok; work = cur.next(p), ++items) {
-            // Q: one copy per 64-element block and tile
-            if (!__all_sync(0xffffffffu, mbar_wait(&bar.q_empty, (items & 1) ^ 1, abort_flag, p.err))) break;
-            const int tiles = cur.r.tokens > p.tokens ? 2 : 1;
-            const uint32_t qbytes = (uint32_t)(p.tokens * p.group * 128);
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&bar.q_full, tiles * L::kHalves * qbytes);
-                for (int g = 0; g < tiles; ++g)
-                    for (int h = 0; h < L::kHalves; ++h)
-                        tma_load_4d(smem + L::kQ + g * L::kTileBytes + h * L::kBlock, &qmap, h * 64, 0, cur.head,
-                                    cur.s.row0 + cur.item * 2 * p.tokens + g * p.tokens, &bar.q_full);
-            }
-            for (int t = cur.t0; t < cur.t1 && ok; ++t) {
-                // lane i: box i of the tile; a box no query sees (or of a bad
-                // page) takes the page coordinate past the end, which reads zeros
-                const int tok = key_tile(cur.r, t) * kTile + lane * p.box;
-                int page = p.pages, off = 0;
-                if (lane < boxes &&
-                    (tok < cur.r.sink_end || (tok < cur.r.hi && tok + p.box > cur.r.lo))) {
-                    const int index = tok / p.page_size;
-                    page = p.page_table[(int64_t)cur.b * p.table_stride + index];
-                    off = tok - index * p.page_size;
-                    if (page < 0 || page >= p.pages) {
-                        atomicExch(p.err, kErrBadIndex);
-                        page = p.pages;
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
+        if (warp == 0 || warp == 2) {
+            // ------------------------------------------------ copies
+            const int kv = warp >> 1;  // warp 0: Q and K, warp 2: V
+            const CUtensorMap *map = kv ? &vmap : &kmap;
+            uint32_t fill = kv;        // ring position of the next tile; K and V alternate
+            bool ok = true;
+            const int boxes = kTile / p.box;
+            for (; ok && next_item(); done_item()) {
+                if (kv == 0) {
+                    // one copy per 64-element block and tile
+                    if (!__all_sync(0xffffffffu, mbar_wait(&bar.q_empty, (items & 1) ^ 1, abort_flag, p.err))) break;
+                    const int tiles = cur.tokens > p.tokens ? 2 : 1;
+                    const uint32_t qbytes = (uint32_t)(p.tokens * p.group * 128);
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&bar.q_full, tiles * L::kHalves * qbytes);
+                        for (int g = 0; g < tiles; ++g)
+                            for (int h = 0; h < L::kHalves; ++h)
+                                tma_load_4d(smem + L::kQ + g * L::kTileBytes + h * L::kBlock, &qmap, h * 64, 0,
+                                            cur.head, cur.row0 + g * p.tokens, &bar.q_full);
                     }
+                    __syncwarp();
                 }
-#pragma unroll
-                for (int kv = 0; kv < 2 && ok; ++kv, ++fills) {
-                    const int slot = fills % kStages;
+                for (int t = cur.t0; t < cur.t1 && ok; ++t, fill += 2) {
+                    // lane i: box i of the tile; a box no query sees (or of a bad
+                    // page) takes the page coordinate past the end, which reads zeros
+                    const int tok = cur.key_tile(t) * kTile + lane * p.box;
+                    int page = p.pages, off = 0;
+                    if (lane < boxes && (tok < cur.sink_end || (tok < cur.hi && tok + p.box > cur.lo))) {
+                        const int index = tok / p.page_size;
+                        page = p.page_table[(int64_t)cur.b * p.table_stride + index];
+                        off = tok - index * p.page_size;
+                        if (page < 0 || page >= p.pages) {
+                            atomicExch(p.err, kErrBadIndex);
+                            page = p.pages;
+                        }
+                    }
+                    const int slot = fill % kStages;
                     ok = __all_sync(0xffffffffu,
-                                    mbar_wait(&bar.empty[slot], (fills / kStages & 1) ^ 1, abort_flag, p.err));
+                                    mbar_wait(&bar.empty[slot], (fill / kStages & 1) ^ 1, abort_flag, p.err));
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&bar.full[slot], L::kTileBytes);
-                    __syncwarp();
-                    if (lane < boxes) {
-                        uint8_t *dst = ring + slot * L::kTileBytes + lane * p.box * 128;
+                    const bool issue = elect_one();
+                    uint8_t *dst = ring + slot * L::kTileBytes;
+                    if (issue) mbar_arrive_expect_tx(&bar.full[slot], L::kTileBytes);
+                    for (int i = 0; i < boxes; ++i, dst += p.box * 128) {
+                        const int page_i = __shfl_sync(0xffffffffu, page, i), off_i = __shfl_sync(0xffffffffu, off, i);
+                        if (issue) {
 #pragma unroll
-                        for (int h = 0; h < L::kHalves; ++h)
-                            tma_load_4d(dst + h * L::kBlock, kv ? &vmap : &kmap, h * 64, off, cur.head, page,
-                                        &bar.full[slot]);
+                            for (int h = 0; h < L::kHalves; ++h)
+                                tma_load_4d(dst + h * L::kBlock, map, h * 64, off_i, cur.head, page_i,
+                                            &bar.full[slot]);
+                        }
                     }
                     __syncwarp();
                 }
             }
-        }
-        // every copy has landed before the CTA may exit (at once unless a
-        // wait was abandoned)
-        for (uint32_t i = 0; i < kStages; ++i) {
-            if (i >= fills) break;
-            const uint32_t last = (fills - 1 - i) / kStages * kStages + i;  // last fill of slot i
-            mbar_drain(&bar.full[i], last / kStages & 1);
-        }
-        if (items && *abort_flag) mbar_drain(&bar.q_full, (items - 1) & 1);
-    } else if (warp == 1) {
+            if (lane == 0) {
+                bar.fills[kv] = fill;
+                if (kv == 0) bar.q_fills = items;
+            }
+        } else if (warp == 3) {
+            // ------------------------------------------------- items
+            int flags = 0;
+            int4 tail = make_int4(0, 0, 0, 0);
+            int64_t left = bar.start.left;
+            int head = bar.start.head, b = bar.start.b, it = bar.start.item, t0 = bar.start.t0;
+            Sequence s = bar.start.s;
+            int n_items = items_of(p, s);
+            for (;; ++items) {
+                Item o{};
+                if (left > 0) {
+                    const Range r = item_range(p, s, it);
+                    o.t0 = t0, o.t1 = (int)min((int64_t)r.n, t0 + left), o.n = r.n;
+                    o.head = head, o.b = b, o.row0 = s.row0 + it * 2 * p.tokens, o.tokens = r.tokens, o.pos0 = r.pos0;
+                    o.lo = r.lo, o.hi = r.hi, o.sink_end = r.sink_end, o.sink_tiles = r.sink_tiles, o.wtile = r.wtile;
+                    if (o.t0 > 0) flags |= kHeadPiece | (o.t1 < o.n ? kHeadGoesOn : 0);
+                    if (o.t0 == 0 && o.t1 < o.n) flags |= kTailPiece, tail = make_int4(0, b, it, head);
+                }
+                const int i = items % kItems;
+                if (!__all_sync(0xffffffffu,
+                                mbar_wait(&bar.item_empty[i], (items / kItems & 1) ^ 1, abort_flag, p.err)))
+                    break;
+                if (lane == 0) {
+                    bar.item[i] = o;
+                    mbar_arrive(&bar.item_full[i]);
+                }
+                __syncwarp();
+                left -= o.t1 - o.t0;
+                if (o.t0 == o.t1) break;
+                t0 = 0;
+                if (left > 0 && ++it >= n_items) {
+                    it = 0;
+                    int scanned = 0;
+                    do {
+                        if (++b >= p.sequences) {
+                            b = 0;
+                            ++head;
+                        }
+                        s = sequence(p, b);
+                    } while (s.len == 0 && ++scanned <= p.sequences);
+                    n_items = items_of(p, s);
+                }
+            }
+            tail.x = flags;
+            if (lane == 0) p.record[blockIdx.x] = tail;
+        } else if (warp == 1) {
         // ------------------------------------------------------ MMAs
         constexpr uint32_t idesc_qk = idesc_bf16_f32(kTile, kTile, false);
         constexpr uint32_t idesc_pv = idesc_bf16_f32(kTile, D, true);
         uint32_t fills = 0;  // ring position of the next K tile
-        uint32_t items = 0;
         uint32_t p_phase[2] = {0, 0};
         bool ok = true;
         auto wait = [&](uint64_t *b, uint32_t parity) {
             ok = __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag, p.err));
             return ok;
         };
-        // S_g = Q_g K^T
-        auto scores = [&](int g, int slot) {
+        // S_g = Q K^T with tile `q` of Q
+        auto scores = [&](int g, int q, int slot) {
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t a = smem_desc_k128(smem + L::kQ + g * L::kTileBytes + (k >> 2) * L::kBlock);
+                    const uint64_t a = smem_desc_k128(smem + L::kQ + q * L::kTileBytes + (k >> 2) * L::kBlock);
                     const uint64_t b = smem_desc_k128(ring + slot * L::kTileBytes + (k >> 2) * L::kBlock);
                     mma_f16_ss(tmem + col_s(g), a + 2 * (k & 3), b + 2 * (k & 3), idesc_qk, k != 0);
                 }
@@ -413,51 +515,73 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_one()) mma_commit(b);
             __syncwarp();
         };
-        for (; work && ok; work = cur.next(p), ++items) {
-            const int tiles = cur.r.tokens > p.tokens ? 2 : 1;
-            if (!wait(&bar.q_full, items & 1)) break;
-            if (!wait(&bar.full[fills % kStages], fills / kStages & 1)) break;
-            for (int g = 0; g < tiles; ++g) scores(g, fills % kStages);
-            release(&bar.empty[fills % kStages]);
-            for (int t = cur.t0; t < cur.t1; ++t, fills += 2) {
-                const uint32_t v = fills + 1, k = fills + 2;
-                const bool more = t + 1 < cur.t1;
-                if (!more) release(&bar.q_empty);
-                if (!wait(&bar.full[v % kStages], v / kStages & 1)) break;
-                // values of tokens that no query of the item sees may be
-                // anything (0 * NaN): clear those rows of the tile
-                const int tok0 = key_tile(cur.r, t) * kTile;
-                if (tok0 + kTile > cur.r.hi || (tok0 < cur.r.lo && tok0 + kTile > cur.r.sink_end)) {
-                    for (int i = lane; i < kTile * 8; i += 32) {
-                        const int tok = tok0 + (i >> 3);
-                        if (tok < cur.r.sink_end || (tok >= cur.r.lo && tok < cur.r.hi)) continue;
+        auto full = [&](uint32_t fill) { return wait(&bar.full[fill % kStages], fill / kStages & 1); };
+        // Values of tokens that no query of the item sees may be anything
+        // (0 * NaN): clear the rows of the tile in [from, to).
+        auto clear_rows = [&](int slot, int from, int to) {
+            uint8_t *tile = ring + slot * L::kTileBytes;
+            for (int i = from * 8 + lane; i < to * 8; i += 32)
 #pragma unroll
-                        for (int h = 0; h < L::kHalves; ++h)
-                            *reinterpret_cast<uint4 *>(ring + v % kStages * L::kTileBytes + h * L::kBlock + i * 16) =
-                                make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                if (more && !wait(&bar.full[k % kStages], k / kStages & 1)) break;
-                for (int g = 0; g < tiles; ++g) {
+                for (int h = 0; h < L::kHalves; ++h)
+                    *reinterpret_cast<uint4 *>(tile + h * L::kBlock + i * 16) = make_uint4(0, 0, 0, 0);
+        };
+        // Boxes that no query sees were filled with zeros; what remains are
+        // the unseen ends of the boxes that hold the ends of the seen ranges.
+        auto clear_unseen = [&](int t, int slot) {
+            const int tok0 = cur.key_tile(t) * kTile;
+            const int sink = cur.sink_end - tok0, lo = cur.lo - tok0, hi = cur.hi - tok0;
+            if (hi >= kTile && (lo <= 0 || sink >= kTile)) return;
+            const int mask = ~(p.box - 1);  // a power of two
+            if (sink > 0 && sink < kTile) clear_rows(slot, sink, min((sink - 1 & mask) + p.box, max(lo, sink)));
+            if (lo > 0 && lo < kTile) clear_rows(slot, max(lo & mask, max(sink, 0)), lo);
+            if (hi > 0 && hi < kTile) clear_rows(slot, hi, (hi - 1 & mask) + p.box);
+            fence_proxy_async_smem();
+            __syncwarp();
+        };
+        for (; ok && next_item(); done_item()) {
+            const bool wide = cur.tokens > p.tokens;
+            const int n = cur.t1 - cur.t0;
+            if (!wait(&bar.q_full, items & 1)) break;
+            // the first scores: of one key tile for both groups, or of a key
+            // tile for each
+            for (int g = 0; g < 2; ++g) {
+                const uint32_t k = fills + (wide ? 0 : 2 * g);
+                if (!wide && g >= n) break;
+                if ((!wide || g == 0) && !full(k)) break;
+                scores(g, wide ? g : 0, k % kStages);
+                if (!wide || g == 1) release(&bar.empty[k % kStages]);
+            }
+            if (!ok) break;
+            // tile t's second product, then the group's next scores
+            for (int t = 0; t < n; ++t) {
+                const uint32_t v = fills + 2 * t + 1, k = v + (wide ? 1 : 3);
+                const bool more = t + (wide ? 1 : 2) < n;
+                if (t == max(n - (wide ? 1 : 2), 0)) release(&bar.q_empty);  // every score of the item is issued
+                if (!full(v)) break;
+                clear_unseen(cur.t0 + t, v % kStages);
+                for (int g = wide ? 0 : t & 1; g <= (wide ? 1 : t & 1); ++g) {
                     if (!wait(&bar.p_full[g], p_phase[g])) break;
                     p_phase[g] ^= 1;
-                    values(g, v % kStages, t == cur.t0);
-                    if (more) scores(g, k % kStages);
+                    values(g, v % kStages, t < (wide ? 1 : 2));
+                    if (g == 1 || !wide) release(&bar.empty[v % kStages]);
+                    if (!more) continue;
+                    if ((g == 0 || !wide) && !full(k)) break;
+                    scores(g, wide ? g : 0, k % kStages);
+                    if (g == 1 || !wide) release(&bar.empty[k % kStages]);
                 }
                 if (!ok) break;
-                release(&bar.empty[v % kStages]);
-                if (more) release(&bar.empty[k % kStages]);
             }
+            fills += 2 * n;
         }
         // every MMA has finished before tensor memory is released
         if (elect_one()) mma_commit(&bar.drain);
         __syncwarp();
         mbar_drain(&bar.drain, 0);
+        }
     } else {
         // --------------------------------------------------- softmax
-        const int g = (warp - 2) >> 2;                 // tile
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        const int g = (warp - 4) >> 2;                 // group
         const int quad = warp & 3;                     // its tensor-memory lanes
         const int row = quad * 32 + lane;              // row of the tile
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
@@ -470,154 +594,204 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag, p.err));
             return ok;
         };
-        int flags = 0;
-        for (; work && ok; work = cur.next(p)) {
-            if (g == 1 && cur.r.tokens <= p.tokens) {
-                // no tile B; only the record needs the piece
-            } else {
-                const int i = g * p.tokens + my_token;  // token within the item
-                const bool valid = my_token < p.tokens && i < cur.r.tokens;
-                const bool busy = __any_sync(0xffffffffu, valid);
-                const int pos = cur.r.pos0 + i;
-                // positions of the tile's first and last query
-                const int pos_a = cur.r.pos0 + g * p.tokens;
-                const int pos_z = cur.r.pos0 + min((g + 1) * p.tokens, cur.r.tokens) - 1;
-                float m = -INFINITY, l = 0.f;
-                for (int t = cur.t0; t < cur.t1; ++t) {
-                    if (!wait(&bar.s_full[g], s_phase)) break;
-                    s_phase ^= 1;
-                    tc_fence_after();
-                    if (busy) {
-                        uint32_t s[4][32];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) tmem_ld32(ts + q * 32, s[q]);
-                        tmem_wait_ld();
-                        const int tok0 = key_tile(cur.r, t) * kTile;
-                        if (tok0 + kTile - 1 > pos_a ||
-                            (p.window && tok0 <= pos_z - p.window && tok0 + kTile > p.sinks)) {
-                            const int last = pos - tok0;
-                            const int first = p.window ? pos - p.window + 1 - tok0 : -1;
-                            const int sink = p.sinks - tok0;
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) {
-                                    const int j = q * 32 + e;
-                                    if (j > last || (j < first && j >= sink)) s[q][e] = 0xFF800000u;
-                                }
-                        }
-                        float top = -INFINITY;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2)
-                                top = fmaxf(fmaxf(top, __uint_as_float(s[q][e])), __uint_as_float(s[q][e + 1]));
-                        const bool grew = top > m && (m == -INFINITY || (top - m) * c > kGrow);
-                        if (__any_sync(0xffffffffu, grew)) {
-                            const float m_new = fmaxf(m, top);
-                            const float f = m == -INFINITY ? 0.f : ex2((m - m_new) * c);
-                            l *= f;
-                            m = m_new;
-                            if (t > cur.t0) {
-                                // O of the earlier tiles is complete: scale it
-                                if (!wait(&bar.o_full[g], o_phase ^ 1)) break;
-                                tc_fence_after();
-#pragma unroll
-                                for (int d = 0; d < D; d += 32) {
-                                    uint32_t o[32];
-                                    tmem_ld32(to + d, o);
-                                    tmem_wait_ld();
-#pragma unroll
-                                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                    tmem_st32(to + d, o);
-                                }
-                            }
-                        }
-                        const float mc = m == -INFINITY ? 0.f : m * c;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t w[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const float a = ex2(fmaf(__uint_as_float(s[q][2 * e]), c, -mc));
-                                const float b = ex2(fmaf(__uint_as_float(s[q][2 * e + 1]), c, -mc));
-                                l += a + b;
-                                w[e] = pack_bf16(a, b);
-                            }
-                            tmem_st16(ts + q * 16, w);
-                        }
-                        tmem_wait_st();
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.p_full[g]);
-                    o_phase ^= 1;
-                }
-                if (!ok) break;
-                // o_phase counts the tiles' second products: wait for the last
-                if (!wait(&bar.o_full[g], o_phase ^ 1)) break;
+        uint32_t merge_phase = 0;
+        bool unmerged = false;  // group B: A may not have read O of the last item yet
+        for (; ok && next_item(); done_item()) {
+            const bool wide = cur.tokens > p.tokens;
+            const int half = wide ? g : 0;                  // the tile of the item
+            const int i = half * p.tokens + my_token;       // token within the item
+            const bool valid = my_token < p.tokens && i < cur.tokens;
+            const bool busy = __any_sync(0xffffffffu, valid);
+            const int pos = cur.pos0 + i;
+            // positions of the tile's first and last query
+            const int pos_a = cur.pos0 + half * p.tokens;
+            const int pos_z = cur.pos0 + min((half + 1) * p.tokens, cur.tokens) - 1;
+            const int step = wide ? 1 : 2;
+            float m = -INFINITY, l = 0.f;
+            bool started = false;
+            for (int t = cur.t0 + (wide ? 0 : g); t < cur.t1; t += step) {
+                if (!wait(&bar.s_full[g], s_phase)) break;
+                s_phase ^= 1;
                 tc_fence_after();
                 if (busy) {
-                    const bool whole = cur.t0 == 0 && cur.t1 == cur.r.n;
-                    const float mc = m == -INFINITY ? -INFINITY : m * c;
-                    const int64_t at =
-                        ((int64_t)cur.s.row0 + cur.item * 2 * p.tokens + i) * p.q_heads + cur.head * p.group + my_head;
+                    uint32_t s[4][32];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld32(ts + q * 32, s[q]);
+                    tmem_wait_ld();
+                    const int tok0 = cur.key_tile(t) * kTile;
+                    if (tok0 + kTile - 1 > pos_a || (p.window && tok0 <= pos_z - p.window && tok0 + kTile > p.sinks)) {
+                        const int end = pos + 1 - tok0;
+                        const int first = p.window ? end - p.window : 0;
+                        const int sink = p.sinks - tok0;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t seen = below(end - q * 32) & (~below(first - q * 32) | below(sink - q * 32));
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(seen >> e & 1)) s[q][e] = 0xFF800000u;
+                        }
+                    }
+                    // four chains each for the maximum and the sum: one
+                    // would bind the loop by its latency
+                    float top4[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) top4[q] = fmaxf(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
+#pragma unroll
+                    for (int e = 2; e < 32; e += 2)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            top4[q] = max3(top4[q], __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
+                    const float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
+                    const bool grew = top > m && (m == -INFINITY || (top - m) * c > kGrow);
+                    if (__any_sync(0xffffffffu, grew)) {
+                        const float m_new = fmaxf(m, top);
+                        const float f = m == -INFINITY ? 0.f : ex2((m - m_new) * c);
+                        l *= f;
+                        m = m_new;
+                        if (started) {
+                            // O of the earlier tiles is complete: scale it
+                            if (!wait(&bar.o_full[g], o_phase ^ 1)) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int d = 0; d < D; d += 32) {
+                                uint32_t o[32];
+                                tmem_ld32(to + d, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st32(to + d, o);
+                            }
+                        }
+                    }
+                    const float mc = m == -INFINITY ? 0.f : m * c;
+                    const uint64_t c2 = pack2(c, c), mc2 = pack2(-mc, -mc);
+                    uint64_t sum[4] = {pack2(l, 0.f), 0, 0, 0};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float a, b;
+                            unpack2(fma2(pack2(__uint_as_float(s[q][2 * e]), __uint_as_float(s[q][2 * e + 1])), c2, mc2),
+                                    a, b);
+                            a = ex2(a), b = ex2(b);
+                            sum[e & 3] = add2(sum[e & 3], pack2(a, b));
+                            w[e] = pack_bf16(a, b);
+                        }
+                        tmem_st16(ts + q * 16, w);
+                    }
+                    float la, lb;
+                    unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), la, lb);
+                    l = la + lb;
+                    tmem_wait_st();
+                }
+                if (unmerged) {
+                    if (!wait(&bar.merged, merge_phase ^ 1)) break;
+                    unmerged = false;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.p_full[g]);
+                o_phase ^= 1;
+                started = true;
+            }
+            if (!ok) break;
+            // o_phase counts the group's second products: wait for the last
+            if (started && !wait(&bar.o_full[g], o_phase ^ 1)) break;
+            tc_fence_after();
+            const float mc = m == -INFINITY ? -INFINITY : m * c;
+            if (!wide && g == 1) {
+                if (unmerged && !wait(&bar.merged, merge_phase ^ 1)) break;
+                bar.ml[row] = make_float2(mc, l);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.b_done);
+                unmerged = true;
+                merge_phase ^= 1;
+            } else {
+                float fa = 1.f, fb = 0.f, top = mc;
+                if (!wide) {
+                    if (!wait(&bar.b_done, merge_phase)) break;
+                    merge_phase ^= 1;
+                    tc_fence_after();
+                    const float2 other = bar.ml[row];
+                    top = fmaxf(mc, other.x);
+                    const float base = top == -INFINITY ? 0.f : top;
+                    fa = ex2(mc - base), fb = ex2(other.x - base);
+                    l = l * fa + other.y * fb;
+                }
+                const bool both = !wide && cur.t1 - cur.t0 > 1;
+                if (busy) {
+                    const bool whole = cur.t0 == 0 && cur.t1 == cur.n;
+                    const int64_t at = ((int64_t)cur.row0 + i) * p.q_heads + cur.head * p.group + my_head;
                     const int piece = blockIdx.x * 2 + (cur.t0 == 0 ? 1 : 0);
-                    const int prow = piece * p.piece_rows + g * kTile + row;
+                    const int prow = piece * p.piece_rows + half * kTile + row;
                     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+                    if (whole) fa *= inv, fb *= inv;
 #pragma unroll
                     for (int d = 0; d < D; d += 32) {
                         uint32_t o[32];
                         tmem_ld32(to + d, o);
                         tmem_wait_ld();
-                        if (!valid) {
-                        } else if (!whole) {
-                            float4 *dst = reinterpret_cast<float4 *>(p.part + (int64_t)prow * D + d);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                                     __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
-                        } else if (p.out_bf16) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at * D + d);
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fa);
+                        if (both) {
+                            uint32_t ob[32];
+                            tmem_ld32(to + (col_o(1) - col_o(0)) + d, ob);
+                            tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                uint32_t w[4];
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(fmaf(__uint_as_float(ob[e]), fb, __uint_as_float(o[e])));
+                        }
+                        if (valid) {
+                            // 32 bytes a store: a thread's row is its own
+                            // lines, so a warp's store is one line per lane
+                            if (whole && p.out_bf16) {
+                                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + at * D + d;
+                                uint32_t w[16];
 #pragma unroll
-                                for (int f = 0; f < 4; ++f)
-                                    w[f] = pack_bf16(__uint_as_float(o[8 * e + 2 * f]) * inv,
-                                                     __uint_as_float(o[8 * e + 2 * f + 1]) * inv);
-                                dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                                for (int e = 0; e < 16; ++e)
+                                    w[e] = pack_bf16(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+                                store32(dst, w);
+                                store32(dst + 16, w + 8);
+                            } else {
+                                float *dst = whole ? static_cast<float *>(p.out) + at * D + d
+                                                   : p.part + (int64_t)prow * D + d;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) store32(dst + 8 * e, o + 8 * e);
                             }
-                        } else {
-                            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at * D + d);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
-                                                     __uint_as_float(o[4 * e + 2]) * inv,
-                                                     __uint_as_float(o[4 * e + 3]) * inv);
                         }
                         __syncwarp();
                     }
                     if (valid) {
                         if (!whole)
-                            p.part_ml[prow] = make_float2(mc, l);
+                            p.part_ml[prow] = make_float2(top, l);
                         else if (p.lse)
-                            p.lse[at] = (mc + __log2f(l)) * kLn2;
+                            p.lse[at] = (top + __log2f(l)) * kLn2;
                     }
                 }
                 tc_fence_before();
-            }
-            if (cur.t0 > 0) flags |= kHeadPiece | (cur.t1 < cur.r.n ? kHeadGoesOn : 0);
-            if (cur.t0 == 0 && cur.t1 < cur.r.n) {
-                flags |= kTailPiece;
-                if (warp == 2 && lane == 0) p.record[blockIdx.x] = make_int4(flags, cur.b, cur.item, cur.head);
+                if (!wide) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.merged);
+                }
             }
         }
-        if (warp == 2 && lane == 0 && !(flags & kTailPiece)) p.record[blockIdx.x] = make_int4(flags, 0, 0, 0);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (bar.abort && tid == 0) {
+        // a wait was abandoned: copies in flight land before the CTA exits
+        // (otherwise every copy was waited for by its reader)
+        for (uint32_t i = 0; i < kStages; ++i) {
+            int last = -1;
+            for (uint32_t f = i; f < max(bar.fills[0], bar.fills[1]); f += kStages)
+                if (f < bar.fills[f & 1]) last = f;
+            if (last >= 0) mbar_drain(&bar.full[i], last / kStages & 1);
+        }
+        if (bar.q_fills) mbar_drain(&bar.q_full, (bar.q_fills - 1) & 1);
+    }
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
@@ -638,11 +812,18 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
     if (row >= p.piece_rows || in_tile >= p.tokens * p.group || token >= r.tokens) return;
     // pieces: this CTA's tail, then the heads of the next ones
     int n = 1;
-    for (int e = blockIdx.x + 1; e < ctas; ++e) {
-        const int f = p.record[e].x;
-        if (!(f & kHeadPiece)) break;
-        ++n;
-        if (!(f & kHeadGoesOn)) break;
+    for (bool more = true; more; n += 32) {
+        const int e = blockIdx.x + n + lane;
+        const int f = e < ctas ? p.record[e].x : 0;
+        // the first CTA whose piece is not of the item, or is its last
+        const uint32_t none = __ballot_sync(0xffffffffu, !(f & kHeadPiece));
+        const uint32_t last = __ballot_sync(0xffffffffu, (f & kHeadPiece) && !(f & kHeadGoesOn));
+        const int end_none = none ? __ffs(none) - 1 : 32, end_last = last ? __ffs(last) : 33;
+        const int end = min(end_none, end_last);
+        if (end <= 32 && (none | last)) {
+            n += end - 32;
+            more = false;
+        }
     }
     auto place = [&](int i) { return ((blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * p.piece_rows + row; };
     float m = -INFINITY;
@@ -652,11 +833,14 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
     const float base = m == -INFINITY ? 0.f : m;
     constexpr int kOwn = D / 32;
     float acc[kOwn] = {}, l = 0.f;
+    using Own = typename std::conditional<kOwn == 4, float4, float2>::type;
+#pragma unroll 4
     for (int i = 0; i < n; ++i) {
         const float2 ml = p.part_ml[place(i)];
+        const Own v = *reinterpret_cast<const Own *>(p.part + (int64_t)place(i) * D + lane * kOwn);
+        const float *o = reinterpret_cast<const float *>(&v);
         const float f = ex2(ml.x - base);
         l += ml.y * f;
-        const float *o = p.part + (int64_t)place(i) * D + lane * kOwn;
 #pragma unroll
         for (int e = 0; e < kOwn; ++e) acc[e] += o[e] * f;
     }
@@ -737,7 +921,9 @@ cudaError_t launch_d(const AttentionArgs &a, const KvCacheView &c, void *workspa
     p.rows = a.rows, p.q_heads = a.q_heads, p.kv_heads = c.kv_heads, p.group = a.q_heads / c.kv_heads;
     p.window = a.window, p.sinks = a.sinks;
     p.tokens = kTile / p.group;
-    p.box = gcd(c.page_size, kTile);
+    // whole pages, or their largest power of two; at most 64 rows, so that
+    // little of a tile is left to clear by hand
+    p.box = gcd(c.page_size, 64);
     p.scale_log2 = a.scale * kLog2e;
     p.out = a.out, p.lse = a.lse, p.out_bf16 = a.out_bf16;
     p.max_q_len = a.max_q_len;
