@@ -484,32 +484,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag, p.err));
             return ok;
         };
-        // S_g = Q K^T with tile `q` of Q
-        auto scores = [&](int g, int q, int slot) {
-            tc_fence_after();
-            if (elect_one()) {
+        // The instruction rate of this warp bounds the loop unless the
+        // descriptors are one addition each: 32-bit sums on the low word (the
+        // start address), which no offset carries out of.
+        const uint64_t q_desc = smem_desc_k128(smem + L::kQ), k_desc = smem_desc_k128(ring);
+        const uint64_t v_desc = smem_desc_mn128(ring, L::kBlock);
+        constexpr uint32_t kTileStep = L::kTileBytes >> 4, kBlockStep = L::kBlock >> 4;
+        // S_g = Q K^T with tile `q` of Q (one elected thread)
+        auto scores = [&](int g, int q, uint32_t slot) {
+            const uint64_t a = q_desc + q * kTileStep, b = k_desc + slot * kTileStep;
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t a = smem_desc_k128(smem + L::kQ + q * L::kTileBytes + (k >> 2) * L::kBlock);
-                    const uint64_t b = smem_desc_k128(ring + slot * L::kTileBytes + (k >> 2) * L::kBlock);
-                    mma_f16_ss(tmem + col_s(g), a + 2 * (k & 3), b + 2 * (k & 3), idesc_qk, k != 0);
-                }
-                mma_commit(&bar.s_full[g]);
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t step = (k >> 2) * kBlockStep + 2 * (k & 3);
+                mma_f16_ss(tmem + col_s(g), a + step, b + step, idesc_qk, k != 0);
             }
-            __syncwarp();
+            mma_commit(&bar.s_full[g]);
         };
-        // O_g (+)= P_g V
-        auto values = [&](int g, int slot, bool first) {
-            tc_fence_after();
-            if (elect_one()) {
+        // O_g (+)= P_g V (one elected thread)
+        auto values = [&](int g, uint32_t slot, bool first) {
+            const uint64_t b = v_desc + slot * kTileStep;
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                    mma_f16_ts(tmem + col_o(g), tmem + col_s(g) + 8 * k,
-                               smem_desc_mn128(ring + slot * L::kTileBytes + k * 16 * 128, L::kBlock), idesc_pv,
-                               !first || k != 0);
-                mma_commit(&bar.o_full[g]);
-            }
-            __syncwarp();
+            for (int k = 0; k < kTile / 16; ++k)
+                mma_f16_ts(tmem + col_o(g), tmem + col_s(g) + 8 * k, b + (uint32_t)(k * (16 * 128 >> 4)), idesc_pv,
+                           !first || k != 0);
+            mma_commit(&bar.o_full[g]);
         };
         auto release = [&](uint64_t *b) {
             if (elect_one()) mma_commit(b);
@@ -542,35 +540,82 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool wide = cur.tokens > p.tokens;
             const int n = cur.t1 - cur.t0;
             if (!wait(&bar.q_full, items & 1)) break;
-            // the first scores: of one key tile for both groups, or of a key
-            // tile for each
-            for (int g = 0; g < 2; ++g) {
-                const uint32_t k = fills + (wide ? 0 : 2 * g);
-                if (!wide && g >= n) break;
-                if ((!wide || g == 0) && !full(k)) break;
-                scores(g, wide ? g : 0, k % kStages);
-                if (!wide || g == 1) release(&bar.empty[k % kStages]);
-            }
-            if (!ok) break;
-            // tile t's second product, then the group's next scores
-            for (int t = 0; t < n; ++t) {
-                const uint32_t v = fills + 2 * t + 1, k = v + (wide ? 1 : 3);
-                const bool more = t + (wide ? 1 : 2) < n;
-                if (t == max(n - (wide ? 1 : 2), 0)) release(&bar.q_empty);  // every score of the item is issued
-                if (!full(v)) break;
-                clear_unseen(cur.t0 + t, v % kStages);
-                for (int g = wide ? 0 : t & 1; g <= (wide ? 1 : t & 1); ++g) {
+            if (wide) {
+                uint32_t slot_k = fills % kStages, slot_v = (fills + 1) % kStages;
+                if (!full(fills)) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    scores(0, 0, slot_k);
+                    scores(1, 1, slot_k);
+                    mma_commit(&bar.empty[slot_k]);
+                }
+                __syncwarp();
+                for (int t = 0; t < n; ++t) {
+                    const uint32_t v = fills + 2 * t + 1;
+                    const bool more = t + 1 < n;
+                    slot_v = v % kStages, slot_k = (v + 1) % kStages;
+                    if (!full(v)) break;
+                    clear_unseen(cur.t0 + t, slot_v);
+                    if (more && !full(v + 1)) break;
+                    if (!wait(&bar.p_full[0], p_phase[0])) break;
+                    p_phase[0] ^= 1;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        values(0, slot_v, t == 0);
+                        if (more) scores(0, 0, slot_k);
+                    }
+                    __syncwarp();
+                    if (!wait(&bar.p_full[1], p_phase[1])) break;
+                    p_phase[1] ^= 1;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        values(1, slot_v, t == 0);
+                        mma_commit(&bar.empty[slot_v]);
+                        if (more) {
+                            scores(1, 1, slot_k);
+                            mma_commit(&bar.empty[slot_k]);
+                        }
+                    }
+                    __syncwarp();
+                }
+            } else {
+                // the first scores of both groups, then tile t's values and
+                // the scores of tile t + 2
+                for (int t = 0; ok && t < min(n, 2); ++t) {
+                    const uint32_t k = fills + 2 * t;
+                    if (!full(k)) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        scores(t, 0, k % kStages);
+                        mma_commit(&bar.empty[k % kStages]);
+                    }
+                    __syncwarp();
+                }
+                for (int t = 0; ok && t < n; ++t) {
+                    const uint32_t v = fills + 2 * t + 1, k = v + 3;
+                    const int g = t & 1;
+                    if (!full(v)) break;
+                    clear_unseen(cur.t0 + t, v % kStages);
                     if (!wait(&bar.p_full[g], p_phase[g])) break;
                     p_phase[g] ^= 1;
-                    values(g, v % kStages, t < (wide ? 1 : 2));
-                    if (g == 1 || !wide) release(&bar.empty[v % kStages]);
-                    if (!more) continue;
-                    if ((g == 0 || !wide) && !full(k)) break;
-                    scores(g, wide ? g : 0, k % kStages);
-                    if (g == 1 || !wide) release(&bar.empty[k % kStages]);
+                    tc_fence_after();
+                    if (elect_one()) {
+                        values(g, v % kStages, t < 2);
+                        mma_commit(&bar.empty[v % kStages]);
+                    }
+                    __syncwarp();
+                    if (t + 2 >= n) continue;
+                    if (!full(k)) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        scores(g, 0, k % kStages);
+                        mma_commit(&bar.empty[k % kStages]);
+                    }
+                    __syncwarp();
                 }
-                if (!ok) break;
             }
+            if (!ok) break;
+            release(&bar.q_empty);  // every score of the item is done
             fills += 2 * n;
         }
         // every MMA has finished before tensor memory is released
