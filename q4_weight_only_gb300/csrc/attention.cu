@@ -371,62 +371,103 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
         if (warp == 0 || warp == 2) {
             // ------------------------------------------------ copies
+            // K and V tiles alternate in one ring; each warp fills its own.
+            // A warp may not be two uses of a slot ahead (its wait would take
+            // the older phase for the newer): the MMA warp frees tiles in an
+            // order in which the slot of fill f - 7, waited for at fill
+            // f - 2, is freed after that of f - 10.
             const int kv = warp >> 1;  // warp 0: Q and K, warp 2: V
             const CUtensorMap *map = kv ? &vmap : &kmap;
-            uint32_t fill = kv;        // ring position of the next tile; K and V alternate
+            uint32_t fill = kv;        // ring position of the next tile
+            uint32_t slot = kv, phase = 1;
             bool ok = true;
-            const int boxes = kTile / p.box;
-            for (; ok && next_item(); done_item()) {
-                if (kv == 0) {
-                    // one copy per 64-element block and tile
-                    if (!__all_sync(0xffffffffu, mbar_wait(&bar.q_empty, (items & 1) ^ 1, abort_flag, p.err))) break;
-                    const int tiles = cur.tokens > p.tokens ? 2 : 1;
+            const int boxes = kTile / p.box, per_load = 32 / boxes;
+            // Page numbers are loaded for 32 boxes at a time (lane i: box
+            // i % boxes of tile i / boxes) and one load ahead of the copies,
+            // across items: a load a tile, waited for, bound the stream.
+            struct Group {
+                int tiles;                 // 0: the share has ended
+                int page, off;             // off < 0: a box that no query sees
+                int head, row0, tokens;    // tokens 0: not the item's first group
+            };
+            int t = 0, q_items = 0;
+            bool open = false;  // `cur` holds an item with tiles from t on
+            auto fetch = [&]() {
+                Group o{};
+                if (!open) {
+                    if (!next_item()) return o;
+                    open = true;
+                    t = cur.t0;
+                    o.row0 = cur.row0, o.tokens = cur.tokens;
+                }
+                o.head = cur.head;
+                o.tiles = min(per_load, cur.t1 - t);
+                o.off = -1;
+                const int mine = lane / boxes;
+                if (mine < o.tiles) {
+                    const int tok = cur.key_tile(t + mine) * kTile + (lane - mine * boxes) * p.box;
+                    // only boxes that hold a token some query sees
+                    if (tok < cur.sink_end || (tok < cur.hi && tok + p.box > cur.lo)) {
+                        const int index = tok / p.page_size;
+                        o.page = p.page_table[(int64_t)cur.b * p.table_stride + index];
+                        o.off = tok - index * p.page_size;
+                    }
+                }
+                t += o.tiles;
+                if (t == cur.t1) {
+                    open = false;
+                    done_item();
+                }
+                return o;
+            };
+            Group now = fetch();
+            while (ok && now.tiles) {
+                const Group then = fetch();
+                if (kv == 0 && now.tokens) {
+                    // Q: one copy per 64-element block and tile
+                    if (!__all_sync(0xffffffffu, mbar_wait(&bar.q_empty, (q_items & 1) ^ 1, abort_flag, p.err))) break;
+                    const int tiles = now.tokens > p.tokens ? 2 : 1;
                     const uint32_t qbytes = (uint32_t)(p.tokens * p.group * 128);
                     if (elect_one()) {
                         mbar_arrive_expect_tx(&bar.q_full, tiles * L::kHalves * qbytes);
                         for (int g = 0; g < tiles; ++g)
                             for (int h = 0; h < L::kHalves; ++h)
                                 tma_load_4d(smem + L::kQ + g * L::kTileBytes + h * L::kBlock, &qmap, h * 64, 0,
-                                            cur.head, cur.row0 + g * p.tokens, &bar.q_full);
+                                            now.head, now.row0 + g * p.tokens, &bar.q_full);
                     }
                     __syncwarp();
+                    ++q_items;
                 }
-                for (int t = cur.t0; t < cur.t1 && ok; ++t, fill += 2) {
-                    // lane i: box i of the tile; a box no query sees (or of a bad
-                    // page) takes the page coordinate past the end, which reads zeros
-                    const int tok = cur.key_tile(t) * kTile + lane * p.box;
-                    int page = p.pages, off = 0;
-                    if (lane < boxes && (tok < cur.sink_end || (tok < cur.hi && tok + p.box > cur.lo))) {
-                        const int index = tok / p.page_size;
-                        page = p.page_table[(int64_t)cur.b * p.table_stride + index];
-                        off = tok - index * p.page_size;
-                        if (page < 0 || page >= p.pages) {
-                            atomicExch(p.err, kErrBadIndex);
-                            page = p.pages;
-                        }
-                    }
-                    const int slot = fill % kStages;
-                    ok = __all_sync(0xffffffffu,
-                                    mbar_wait(&bar.empty[slot], (fill / kStages & 1) ^ 1, abort_flag, p.err));
+                if (now.off < 0 || now.page < 0 || now.page >= p.pages) {
+                    // a page coordinate past the end reads zeros
+                    if (now.off >= 0) atomicExch(p.err, kErrBadIndex);
+                    now.page = p.pages, now.off = 0;
+                }
+                for (int j = 0; j < now.tiles; ++j) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bar.empty[slot], phase, abort_flag, p.err));
                     if (!ok) break;
                     const bool issue = elect_one();
                     uint8_t *dst = ring + slot * L::kTileBytes;
                     if (issue) mbar_arrive_expect_tx(&bar.full[slot], L::kTileBytes);
                     for (int i = 0; i < boxes; ++i, dst += p.box * 128) {
-                        const int page_i = __shfl_sync(0xffffffffu, page, i), off_i = __shfl_sync(0xffffffffu, off, i);
+                        const int page = __shfl_sync(0xffffffffu, now.page, j * boxes + i);
+                        const int off = __shfl_sync(0xffffffffu, now.off, j * boxes + i);
                         if (issue) {
 #pragma unroll
                             for (int h = 0; h < L::kHalves; ++h)
-                                tma_load_4d(dst + h * L::kBlock, map, h * 64, off_i, cur.head, page_i,
-                                            &bar.full[slot]);
+                                tma_load_4d(dst + h * L::kBlock, map, h * 64, off, now.head, page, &bar.full[slot]);
                         }
                     }
                     __syncwarp();
+                    fill += 2;
+                    slot += 2;
+                    if (slot >= kStages) slot -= kStages, phase ^= 1;
                 }
+                now = then;
             }
             if (lane == 0) {
                 bar.fills[kv] = fill;
-                if (kv == 0) bar.q_fills = items;
+                if (kv == 0) bar.q_fills = q_items;
             }
         } else if (warp == 3) {
             // ------------------------------------------------- items
