@@ -16,115 +16,124 @@ namespace q4_0 {
 
 namespace {
 
-constexpr int kVec = 16;  // elements of one work item: eight pairs
-constexpr int kMaxThreads = 512;
+constexpr int kVec = 8;  // elements of one work item: four pairs
+constexpr int kThreads = 256;
+constexpr int kPieceBytes = 32 * 1024;  // most of a row that one CTA holds
 
-// Eight consecutive elements as fp32.
-__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+// Four consecutive elements as fp32.
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+    const uint2 a = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xFFFF0000u), __uint_as_float(a.y << 16),
+                       __uint_as_float(a.y & 0xFFFF0000u));
 }
 
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+// (a, b) -> (a cos - b sin, b cos + a sin)
+__device__ __forceinline__ void turn(float &a, float &b, float cosv, float sinv) {
+    const float a0 = a;
+    a = a0 * cosv - b * sinv;
+    b = b * cosv + a0 * sinv;
 }
 
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// One CTA per row of qkv.
+// blockIdx.x: row of qkv, blockIdx.y: piece of `heads` heads of the row.
+// Bound by the read of qkv and the writes.  One bulk copy brings the piece
+// to shared memory while the CTA finds the row's place in the cache
+// (sequence, length, page); several CTAs an SM keep their pieces in flight.
+// (Loads into registers, 64 bytes a thread, reached 0.65 of the measured
+// copy rate on 8191 fp32 rows of 7168.)
 template <typename T>
-__global__ void __launch_bounds__(kMaxThreads) kv_append_kernel(const KvAppendArgs a, const KvCacheView c,
+__global__ void __launch_bounds__(kThreads, 6) kv_append_kernel(const KvAppendArgs a, const KvCacheView c, int heads,
                                                                 unsigned int *err) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t full;
+    __shared__ int abort_flag;
+    const T *piece = reinterpret_cast<const T *>(smem);
+    const int row = blockIdx.x, head0 = blockIdx.y * heads;
+    const int n_heads = min(heads, a.q_heads + 2 * c.kv_heads - head0);
+    if (threadIdx.x == 0) {
+        mbar_init(&full, 1);
+        abort_flag = 0;
+        mbar_fence_init();
+    }
     pdl_launch_dependents();
     pdl_wait();
-    const int row = blockIdx.x;
+    if (threadIdx.x == 0) {
+        const uint32_t bytes = (uint32_t)(n_heads * c.head_dim * sizeof(T));
+        mbar_arrive_expect_tx(&full, bytes);
+        bulk_g2s(smem, static_cast<const T *>(a.qkv) + (int64_t)row * a.qkv_stride + (int64_t)head0 * c.head_dim, bytes,
+                 &full);
+    }
     // the sequence the row belongs to: how many end at or before it
     int ended = 0;
-    for (int base = 0; base < c.sequences; base += blockDim.x) {
+    for (int base = 0; base < c.sequences; base += kThreads) {
         const int b = base + threadIdx.x;
         ended += __syncthreads_count(b < c.sequences && c.q_start[b + 1] <= row);
     }
-    if (ended >= c.sequences || row < c.q_start[0]) return;  // a row of no sequence
-    const int pos = c.kv_len[ended] - c.q_start[ended + 1] + row;
-    const int turn = a.row_positions ? a.row_positions[row] : pos;
-    const int page_index = pos >= 0 ? pos / c.page_size : -1;
-    const int page = page_index >= 0 && page_index < c.table_width
-                         ? c.page_table[(int64_t)ended * c.table_stride + page_index]
-                         : -1;
-    const bool bad_turn = turn < 0 || turn >= a.positions;
-    if (bad_turn || page < 0 || page >= c.pages) {
-        if (threadIdx.x == 0) atomicExch(err, kErrBadIndex);
-        return;
+    bool ok = ended < c.sequences && row >= c.q_start[0];  // else: a row of no sequence
+    int pos = 0, turn_row = 0, page = 0, off = 0;
+    if (ok) {
+        pos = c.kv_len[ended] - c.q_start[ended + 1] + row;
+        turn_row = a.row_positions ? a.row_positions[row] : pos;
+        const int index = pos >= 0 ? pos / c.page_size : -1;
+        page = index >= 0 && index < c.table_width ? c.page_table[(int64_t)ended * c.table_stride + index] : -1;
+        off = pos - index * c.page_size;
+        if (turn_row < 0 || turn_row >= a.positions || page < 0 || page >= c.pages) {
+            if (threadIdx.x == 0) atomicExch(err, kErrBadIndex);
+            ok = false;
+        }
     }
-    const int off = pos - page_index * c.page_size;
-    const int per_head = c.head_dim / kVec;
-    const int items = (a.q_heads + 2 * c.kv_heads) * per_head;
-    const int half = a.rot / 2;
-    const T *src = static_cast<const T *>(a.qkv) + (int64_t)row * a.qkv_stride;
-    const float *cs = a.cos_sin + (int64_t)turn * a.rot;
-    for (int it = threadIdx.x; it < items; it += blockDim.x) {
-        const int head = it / per_head, piece = it - head * per_head;
-        const bool turned = head < a.q_heads + c.kv_heads && piece * kVec < a.rot;
-        // first element of each half of the item
-        int e0 = piece * kVec, e1 = e0 + 8;
-        if (turned && !a.interleaved) e0 = piece * 8, e1 = half + piece * 8;
-        const T *s = src + (int64_t)head * c.head_dim;
-        float u[8], v[8];
-        load8(s + e0, u);
-        load8(s + e1, v);
+    const bool landed = mbar_wait(&full, 0, &abort_flag, err);
+    if (!ok || !landed) return;  // the copy has landed, or a wait of two seconds was reported
+    const float *cs = a.cos_sin + (int64_t)turn_row * a.rot;
+    __nv_bfloat16 *q_row = a.q_out + (int64_t)row * a.q_heads * c.head_dim;
+    __nv_bfloat16 *k_row = c.k + page * c.k_stride[0] + off * c.k_stride[2];
+    __nv_bfloat16 *v_row = c.v + page * c.v_stride[0] + off * c.v_stride[2];
+    const int per_head = c.head_dim / kVec, half = a.rot / 2;
+    for (int it = threadIdx.x; it < n_heads * per_head; it += kThreads) {
+        const int in_piece = it / per_head, i = it - in_piece * per_head, head = head0 + in_piece;
+        const bool turned = head < a.q_heads + c.kv_heads && i * kVec < a.rot;
+        // first elements of the item's two halves
+        int e0 = i * kVec, e1 = e0 + 4;
+        if (turned && !a.interleaved) e0 = i * 4, e1 = half + i * 4;
+        const T *s = piece + in_piece * c.head_dim;
+        float4 u = load4(s + e0), v = load4(s + e1);
         if (turned) {
-            float cosv[8], sinv[8];
-            load8(cs + piece * 8, cosv);
-            load8(cs + half + piece * 8, sinv);
+            const float4 cosv = load4(cs + i * 4), sinv = load4(cs + half + i * 4);
             if (a.interleaved) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float &x = i < 4 ? u[2 * i] : v[2 * i - 8], &y = i < 4 ? u[2 * i + 1] : v[2 * i - 7];
-                    const float x0 = x;
-                    x = x0 * cosv[i] - y * sinv[i];
-                    y = y * cosv[i] + x0 * sinv[i];
-                }
+                turn(u.x, u.y, cosv.x, sinv.x), turn(u.z, u.w, cosv.y, sinv.y);
+                turn(v.x, v.y, cosv.z, sinv.z), turn(v.z, v.w, cosv.w, sinv.w);
             } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float x0 = u[i];
-                    u[i] = x0 * cosv[i] - v[i] * sinv[i];
-                    v[i] = v[i] * cosv[i] + x0 * sinv[i];
-                }
+                turn(u.x, v.x, cosv.x, sinv.x), turn(u.y, v.y, cosv.y, sinv.y);
+                turn(u.z, v.z, cosv.z, sinv.z), turn(u.w, v.w, cosv.w, sinv.w);
             }
         }
         __nv_bfloat16 *dst;
-        if (head < a.q_heads)
-            dst = a.q_out + ((int64_t)row * a.q_heads + head) * c.head_dim;
-        else if (head < a.q_heads + c.kv_heads)
-            dst = c.k + page * c.k_stride[0] + (head - a.q_heads) * c.k_stride[1] + off * c.k_stride[2];
+        const int kv_head = head - a.q_heads;
+        if (kv_head < 0)
+            dst = q_row + (int64_t)head * c.head_dim;
+        else if (kv_head < c.kv_heads)
+            dst = k_row + kv_head * c.k_stride[1];
         else
-            dst = c.v + page * c.v_stride[0] + (head - a.q_heads - c.kv_heads) * c.v_stride[1] + off * c.v_stride[2];
-        store8(dst + e0, u);
-        store8(dst + e1, v);
+            dst = v_row + (kv_head - c.kv_heads) * c.v_stride[1];
+        *reinterpret_cast<uint2 *>(dst + e0) = make_uint2(pack_bf16(u.x, u.y), pack_bf16(u.z, u.w));
+        *reinterpret_cast<uint2 *>(dst + e1) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
     }
+}
+
+template <typename T>
+cudaError_t launch_typed(const KvAppendArgs &a, const KvCacheView &c, int64_t rows, cudaStream_t s, unsigned int *err) {
+    // a head is at most 4 KB (head_dim <= 1024)
+    const int all = a.q_heads + 2 * c.kv_heads, fit = kPieceBytes / (c.head_dim * (int)sizeof(T));
+    const int pieces = (all + fit - 1) / fit, heads = (all + pieces - 1) / pieces;
+    const int smem = heads * c.head_dim * (int)sizeof(T);
+    return launch_pdl(kv_append_kernel<T>, dim3((unsigned)rows, pieces), dim3(kThreads), smem, s, a, c, heads, err);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const KvAppendArgs &a, const KvCacheView &c, int64_t rows, bool bf16, cudaStream_t s,
                              unsigned int *err) {
-    const int items = (a.q_heads + 2 * c.kv_heads) * (c.head_dim / kVec);
-    const int threads = items >= kMaxThreads ? kMaxThreads : (items + 31) / 32 * 32;
-    auto *kernel = bf16 ? kv_append_kernel<__nv_bfloat16> : kv_append_kernel<float>;
-    return launch_pdl(kernel, dim3((unsigned)rows), dim3(threads), 0, s, a, c, err);
+    return bf16 ? launch_typed<__nv_bfloat16>(a, c, rows, s, err) : launch_typed<float>(a, c, rows, s, err);
 }
 
 }  // namespace q4_0

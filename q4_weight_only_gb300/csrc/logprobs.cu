@@ -1,22 +1,34 @@
 // logprobs.cu -- log probability of a given token per row of logits, with
 // the row's entropy and its top alternatives (declared in include/q4_0.h).
 //
-// Mathematics, over one read of a row x: with a running maximum m,
-//   s = sum e^(x - m),   t = sum (x - m) e^(x - m),
+// Mathematics, over one read of a row x in base 2, y = x log2 e - m with a
+// running reference m:
+//   s = sum 2^y,   t = sum y 2^y,
 // both rescaled when m grows (t also shifts: t + (m_old - m_new) s), so
-//   lse = m + ln s,   logprob = x[token] - lse,   entropy = ln s - t / s.
-// All statistics are fp32.  Ranking uses 64-bit keys (order-preserving bits
+//   lse = (m + log2 s) ln 2,  logprob = x[token] - lse,
+//   entropy = (log2 s - t / s) ln 2.
+// All statistics are fp32; m is the rounded product that y uses, so its
+// rounding cancels in lse.  Ranking uses 64-bit keys (order-preserving bits
 // of x, then the complement of the index), so equal logits rank by lowest
 // index whatever order threads meet them in.
 //
-// Top alternatives in the same read: a block keeps a threshold key, known to
-// be at most the row's k-th largest, and appends only larger keys to a
-// buffer.  The threshold starts as the k-th largest of the per-thread best
-// keys of the first chunk (k keys at or above it exist), and is raised the
-// same way, with the buffer cut to its k largest, when the buffer could
-// overflow: at most k threads of a chunk then hold candidates, 16 each, so
-// the buffer never overflows, for any order of the logits.
+// Top alternatives in the same read: every warp keeps a threshold key, below
+// the row's k-th largest, and appends only larger keys to a buffer of its
+// own.  The threshold starts below the k-th largest of the block's per-thread
+// best keys of the first chunk (k keys at or above that one exist); a warp
+// whose buffer is full cuts it to its 32 largest and raises its threshold to
+// the k-th of them, so any order of the logits is handled.  Warps meet only
+// at the first chunk and the end of a row: with a barrier a chunk, each
+// waited for the one warp that had found candidates.  Code that runs for the
+// few candidates is kept short: unrolled over a thread's 16 logits, each of
+// its rare runs waited a microsecond for instructions.
+//
+// Bound by the one read of the logits: chunks of 8192 logits stream through
+// a ring of bulk copies (96 KB in flight a block, two blocks an SM) that
+// runs on over the ends of rows.
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "q4_0_internal.h"
 #include "q4_0_ptx.cuh"
@@ -29,10 +41,12 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPerThread = 16;                     // logits of one thread in a chunk
 constexpr int kChunk = kThreads * kPerThread;
-constexpr int kBuffer = 1024;                      // candidate keys a block holds
-constexpr int kMaxTop = 32;                        // one list of alternatives per warp
+constexpr int kMaxTop = 32;                        // one key a lane
+constexpr int kBuffer = 2 * kMaxTop;               // candidate keys a warp holds
 constexpr float kLog2e = 1.4426950408889634f;
-static_assert(kMaxTop * kPerThread + kMaxTop <= kBuffer, "a raised threshold must leave room for a chunk");
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kFloor = -1000.f;                  // 2^kFloor is 0, and kFloor * 0 is too
+constexpr int kRingBytes = 96 * 1024;
 
 using Key = unsigned long long;  // 0: none
 
@@ -51,11 +65,28 @@ __device__ __forceinline__ float key_value(Key k) {
 
 __device__ __forceinline__ uint32_t key_index(Key k) { return 0xFFFFFFFFu - (uint32_t)k; }
 
-// Largest of a and b; NaN if either is.
+// Largest; NaN if one is.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float r;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// The float at or below which a logit is no candidate: the value of the
+// threshold key, above every number when that is a NaN.
+__device__ __forceinline__ float limit_value(Key limit) {
+    const float x = key_value(limit);
+    return x != x ? INFINITY : x;
 }
 
 // ----------------------------------------------------------- sorted lists
@@ -91,20 +122,24 @@ __device__ __forceinline__ Key warp_top_of_two(Key a, Key reversed, int lane) {
     return warp_merge_desc(a > reversed ? a : reversed, lane);
 }
 
+constexpr int kMaxStages = 6;
+
 struct Shared {
-    Key buffer[kBuffer];
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    int abort;
+    Key buffer[kWarps][kBuffer];
     Key lists[kWarps][kMaxTop];
     float m[kWarps], s[kWarps], t[kWarps];
-    int count;
 };
 
-// The block's 32 largest keys from one descending list per warp; the result
-// is in sh.lists[0] after the call (which starts and ends with a barrier).
-__device__ __forceinline__ void block_top(Shared &sh, Key mine, int warp, int lane) {
+// The block's 32 largest keys from one descending list in each of the first
+// `lists` warps; the result is in sh.lists[0] after the call (which starts
+// and ends with a barrier).
+__device__ __forceinline__ void block_top(Shared &sh, Key mine, int lists, int warp, int lane) {
     __syncthreads();
-    sh.lists[warp][lane] = mine;
-#pragma unroll
+    sh.lists[warp][lane] = warp < lists ? mine : 0;
     for (int step = kWarps / 2; step >= 1; step >>= 1) {
+        if (step >= lists) continue;
         __syncthreads();
         if (warp < step) {
             mine = warp_top_of_two(mine, sh.lists[warp + step][31 - lane], lane);
@@ -114,20 +149,14 @@ __device__ __forceinline__ void block_top(Shared &sh, Key mine, int warp, int la
     __syncthreads();
 }
 
-// One descending list per warp of n buffered keys (n <= kBuffer).
-__device__ __forceinline__ Key warp_list(const Key *buffer, int n, int warp, int lane) {
-    constexpr int kOwn = kBuffer / kWarps;
-    static_assert(kOwn % 32 == 0, "");
-    Key mine = 0;
-    // entries are dealt to the warps 32 at a time
-#pragma unroll
-    for (int j = 0; j < kOwn / 32; ++j) {
-        const int i = (j * kWarps + warp) * 32;
-        if (i >= n) break;
-        const Key k = warp_sort_desc(i + lane < n ? buffer[i + lane] : 0, lane);
-        mine = j == 0 ? k : warp_top_of_two(mine, __shfl_xor_sync(0xffffffffu, k, 31), lane);
+// The 32 largest of a warp's n buffered keys, descending.
+__device__ __forceinline__ Key warp_list(const Key *buffer, int n, int lane) {
+    Key k = warp_sort_desc(lane < n ? buffer[lane] : 0, lane);
+    if (n > 32) {
+        const Key o = warp_sort_desc(lane + 32 < n ? buffer[lane + 32] : 0, lane);
+        k = warp_top_of_two(k, __shfl_xor_sync(0xffffffffu, o, 31), lane);
     }
-    return mine;
+    return k;
 }
 
 // ------------------------------------------------------------- statistics
@@ -142,7 +171,7 @@ __device__ __forceinline__ Stats join(const Stats &a, const Stats &b) {
     const float base = r.m == -INFINITY ? 0.f : r.m;
     // a side without any finite logit has s = t = 0, and its shift is cut off
     const float da = fmaxf(a.m - base, -1e30f), db = fmaxf(b.m - base, -1e30f);
-    const float fa = ex2(da * kLog2e), fb = ex2(db * kLog2e);
+    const float fa = ex2(da), fb = ex2(db);
     r.s = a.s * fa + b.s * fb;
     r.t = (a.t + da * a.s) * fa + (b.t + db * b.s) * fb;
     return r;
@@ -181,8 +210,8 @@ template <typename T>
 __device__ __forceinline__ void finish_row(const LogprobArgs &a, int row, Stats v, Key best, int lane,
                                            unsigned int *err) {
     const bool empty = v.m == -INFINITY && v.s == 0.f;  // every logit is -inf
-    const float ln_s = logf(v.s);
-    const float lse = empty ? -INFINITY : v.m + ln_s;
+    const float log_s = log2f(v.s);
+    const float lse = empty ? -INFINITY : (v.m + log_s) * kLn2;
     if (lane == 0) {
         float lp = 0.f;
         if (a.tokens) {
@@ -196,7 +225,7 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, int row, Stats 
             }
             a.logprob[row] = lp;
         }
-        const float h = ln_s - v.t / v.s;
+        const float h = (log_s - v.t / v.s) * kLn2;
         a.entropy[row] = empty ? 0.f : (h < 0.f ? 0.f : h);
     }
     if (lane < a.top) {
@@ -208,31 +237,32 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, int row, Stats 
 
 // ------------------------------------------------------------------ loads
 
-// kPerThread logits of one thread: 16-byte vectors, kThreads vectors apart.
-// `p` is 16-byte aligned and element 0 of it has index `first`; elements
-// outside [lo, hi) read as -inf.
+// kPerThread logits of one thread from a chunk in shared memory: 16-byte
+// vectors, kThreads vectors apart.  Element 0 of the chunk has index `first`;
+// outside [lo, hi) (`edge`: the chunk has such elements) logits read as -inf.
 template <typename T>
-__device__ __forceinline__ void load_chunk(const T *p, int first, int lo, int hi, int tid, float (&x)[kPerThread]) {
+__device__ __forceinline__ void load_chunk(const T *chunk, bool edge, int first, int lo, int hi, int tid,
+                                           float (&x)[kPerThread]) {
     constexpr int kV = 16 / sizeof(T);
 #pragma unroll
     for (int j = 0; j < kPerThread / kV; ++j) {
-        const int o = (j * kThreads + tid) * kV, i = first + o;
+        const int o = (j * kThreads + tid) * kV;
         float *d = x + j * kV;
-        if (i >= lo && i + kV <= hi) {
-            const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p + o));
-            const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+        const uint4 w = *reinterpret_cast<const uint4 *>(chunk + o);
+        const uint32_t r[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if constexpr (sizeof(T) == 4) {
-                    d[e] = __uint_as_float(r[e]);
-                } else {
-                    d[2 * e] = __uint_as_float(r[e] << 16);
-                    d[2 * e + 1] = __uint_as_float(r[e] & 0xFFFF0000u);
-                }
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (sizeof(T) == 4) {
+                d[e] = __uint_as_float(r[e]);
+            } else {
+                d[2 * e] = __uint_as_float(r[e] << 16);
+                d[2 * e + 1] = __uint_as_float(r[e] & 0xFFFF0000u);
             }
-        } else {
+        }
+        if (edge) {
 #pragma unroll
-            for (int e = 0; e < kV; ++e) d[e] = i + e >= lo && i + e < hi ? to_float(p[o + e]) : -INFINITY;
+            for (int e = 0; e < kV; ++e)
+                if (first + o + e < lo || first + o + e >= hi) d[e] = -INFINITY;
         }
     }
 }
@@ -250,112 +280,198 @@ struct Partial {
     Key keys[kMaxTop];
 };
 
-// blockIdx.y: row, blockIdx.x: split of the row.
+// A split of a row, and the 16-byte granules that hold it: the copies start
+// at the boundary at or before the first logit and end at the one at or
+// after the last; no other memory is touched.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const LogprobArgs a, Partial *part, int span,
-                                                                     unsigned int *err) {
+struct Span {
+    const T *src;
+    int begin, lo, hi, chunks;
+    __device__ __forceinline__ Span(const LogprobArgs &a, int unit, int splits, int span) {
+        const int row = unit / splits;
+        lo = (unit - row * splits) * span, hi = min(a.vocab, lo + span);
+        const T *x = static_cast<const T *>(a.logits) + (int64_t)row * a.row_stride + lo;
+        const int skew = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+        src = x - skew, begin = lo - skew;
+        chunks = (hi - begin + kChunk - 1) / kChunk;
+    }
+    __device__ __forceinline__ uint32_t bytes(int c) const {
+        const int64_t left = ((int64_t)(hi - begin) * sizeof(T) + 15) / 16 * 16 - (int64_t)c * kChunk * sizeof(T);
+        return (uint32_t)min(left, (int64_t)(kChunk * sizeof(T)));
+    }
+};
+
+// Each CTA takes the units (splits of rows) blockIdx.x, + gridDim.x, ...; its
+// ring runs on over their ends, so the next unit's first chunks arrive while
+// the last one is finished.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const LogprobArgs a, Partial *part, int splits,
+                                                                     int span, int units, unsigned int *err) {
+    constexpr int kChunkBytes = kChunk * sizeof(T), kStages = kRingBytes / kChunkBytes;
+    extern __shared__ __align__(128) uint8_t ring[];
     __shared__ Shared sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], kWarps);
+        }
+        sh.abort = 0;
+        mbar_fence_init();
+    }
+    __syncthreads();
     pdl_launch_dependents();
     pdl_wait();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int row = blockIdx.y;
-    const T *x0 = static_cast<const T *>(a.logits) + (int64_t)row * a.row_stride;
-    const int lo = blockIdx.x * span, hi = min(a.vocab, lo + span);
-    // start the vectors on a 16-byte boundary at or before the first logit
-    const int skew = (int)((reinterpret_cast<uintptr_t>(x0 + lo) & 15u) / sizeof(T));
-    if (tid == 0) sh.count = 0;
+    // thread 0: the next chunk to copy
+    int next_unit = blockIdx.x, next_chunk = 0, next_slot = 0;
+    uint32_t copies = 0;
+    auto copy = [&]() {
+        if (next_unit >= units) return;
+        const Span<T> w(a, next_unit, splits, span);
+        const uint32_t bytes = w.bytes(next_chunk);
+        mbar_arrive_expect_tx(&sh.full[next_slot], bytes);
+        bulk_g2s(ring + next_slot * kChunkBytes, w.src + (int64_t)next_chunk * kChunk, bytes, &sh.full[next_slot]);
+        ++copies;
+        if (++next_slot == kStages) next_slot = 0;
+        if (++next_chunk == w.chunks) next_chunk = 0, next_unit += gridDim.x;
+    };
+    if (tid == 0)
+        for (int i = 0; i < kStages; ++i) copy();
+    bool ok = true;
+    int slot = 0, last = -1;  // places of this and of the last chunk
+    uint32_t phase = 0, last_phase = 0;
 
-    Stats st{-INFINITY, 0.f, 0.f};
-    Key limit = 0;                // candidates are keys above it
-    float limit_x = -INFINITY;    // its value
-    bool seeded = false;          // false: everything is a candidate
-    int bound = 0;                // at least sh.count, the same in every thread
-
-    float x[kPerThread], next[kPerThread];
-    load_chunk<T>(x0 + lo - skew, lo - skew, lo, hi, tid, x);
-    for (int first = lo - skew; first < hi; first += kChunk) {
-        if (first + kChunk < hi) load_chunk<T>(x0 + first + kChunk, first + kChunk, lo, hi, tid, next);
-        float top = x[0], top_n = x[0];
+    for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const Span<T> w(a, unit, splits, span);
+        const int lo = w.lo, hi = w.hi;
+        Stats st{-INFINITY, 0.f, 0.f};
+        Key limit = 0;                // candidates are keys above it; the same across the warp
+        float limit_x = -INFINITY;    // its value
+        int count = 0;                // keys in the warp's buffer
+        Key *buffer = sh.buffer[warp];
+        for (int c = 0; c < w.chunks; ++c) {
+            const int first = w.begin + c * kChunk;
+            if (tid == 0 && last >= 0 && ok) {
+                // refill the last chunk's place once every warp has left it
+                ok = mbar_wait(&sh.empty[last], last_phase, &sh.abort, err);
+                if (ok) copy();
+            }
+            ok = mbar_wait(&sh.full[slot], phase, &sh.abort, err) && ok;
+            float x[kPerThread];
+            load_chunk<T>(reinterpret_cast<const T *>(ring + slot * kChunkBytes), first < lo || first + kChunk > hi,
+                          first, lo, hi, tid, x);
+            float top = max_nan(x[0], x[1]);  // NaN if one is
+            float low = fminf(x[0], x[1]);
 #pragma unroll
-        for (int e = 1; e < kPerThread; ++e) top = fmaxf(top, x[e]), top_n = max_nan(top_n, x[e]);
-        if (top > st.m) {
-            const float d = fmaxf(st.m - top, -1e30f), f = ex2(d * kLog2e);
-            st.t = (st.t + d * st.s) * f;
-            st.s *= f;
-            st.m = top;
-        }
-        const float base = st.m == -INFINITY ? 0.f : st.m;
+            for (int e = 2; e < kPerThread; e += 2) {
+                top = max_nan(top, x[e], x[e + 1]);
+                low = min3(low, x[e], x[e + 1]);
+            }
+            // a NaN leaves m as it is and reaches s and t below
+            if (top * kLog2e > st.m) {
+                const float m = top * kLog2e, d = fmaxf(st.m - m, -1e30f), f = ex2(d);
+                st.t = (st.t + d * st.s) * f;
+                st.s *= f;
+                st.m = m;
+            }
+            const float base = st.m == -INFINITY ? 0.f : st.m;
+            const uint64_t c2 = pack2(kLog2e, kLog2e), m2 = pack2(-base, -base);
+            uint64_t s2 = pack2(st.s, 0.f), t2 = pack2(st.t, 0.f);
+            // -inf: 2^y is 0, and y 2^y must be
+            auto add = [&](auto cut) {
 #pragma unroll
-        for (int e = 0; e < kPerThread; ++e) {
-            const float d = max_nan(x[e] - base, -1e30f);  // -inf: cut off, so that d * 0 is 0
-            const float p = ex2(d * kLog2e);
-            st.s += p;
-            st.t = fmaf(d, p, st.t);
-        }
-        if (a.top > 0) {
-            const bool any = !seeded || !(top_n <= limit_x);
-            int hits = __syncthreads_count(any);
-            if (hits && bound + hits * kPerThread > kBuffer) {
-                bound = sh.count;
-                __syncthreads();
-                if (bound + hits * kPerThread > kBuffer) {
-                    // cut the buffer to its 32 largest, then raise the
-                    // threshold to the top-th largest of the threads' best keys
-                    if (bound > kMaxTop) {
-                        block_top(sh, warp_list(sh.buffer, bound, warp, lane), warp, lane);
-                        if (tid < kMaxTop) sh.buffer[tid] = sh.lists[0][tid];
-                        bound = kMaxTop;
-                        if (tid == 0) sh.count = kMaxTop;
-                        const Key k = sh.lists[0][a.top - 1];
-                        if (k > limit) limit = k;
-                    }
+                for (int e = 0; e < kPerThread; e += 2) {
+                    float y0, y1;
+                    unpack2(fma2(pack2(x[e], x[e + 1]), c2, m2), y0, y1);
+                    if (decltype(cut)::value) y0 = max_nan(y0, kFloor), y1 = max_nan(y1, kFloor);
+                    const uint64_t p = pack2(ex2(y0), ex2(y1));
+                    s2 = add2(s2, p);
+                    t2 = fma2(pack2(y0, y1), p, t2);
+                }
+            };
+            if (__any_sync(0xffffffffu, low == -INFINITY))
+                add(std::true_type{});
+            else
+                add(std::false_type{});
+            float u, v;
+            unpack2(s2, u, v);
+            st.s = u + v;
+            unpack2(t2, u, v);
+            st.t = u + v;
+            const T *chunk = reinterpret_cast<const T *>(ring + slot * kChunkBytes);
+            if (a.top > 0) {
+                if (c == 0) {
+                    // this thread's best key
                     Key mine = 0;
+                    if (top == top) {
+                        int at = 0;
 #pragma unroll
-                    for (int e = 0; e < kPerThread; ++e) {
-                        const int i = first + chunk_index<T>(e, tid);
-                        const Key k = make_key(x[e], i);
-                        if (i >= lo && i < hi && k > mine) mine = k;
+                        for (int e = kPerThread - 1; e >= 0; --e) at = x[e] == top ? chunk_index<T>(e, tid) : at;
+                        if (first + at >= lo && first + at < hi) mine = make_key(top, first + at);
                     }
-                    block_top(sh, warp_sort_desc(mine, lane), warp, lane);
-                    const Key k = sh.lists[0][a.top - 1];
-                    // keys equal to the new threshold stay candidates
-                    if (k > 0 && k - 1 > limit) limit = k - 1;
-                    limit_x = limit ? key_value(limit) : -INFINITY;
-                    if (limit && limit_x != limit_x) limit_x = INFINITY;
-                    seeded = limit != 0;
-                    hits = kMaxTop;
-                    __syncthreads();
+                    if (!mine) {  // a NaN, or only logits outside the row and -inf
+#pragma unroll 1
+                        for (int e = 0; e < kPerThread; ++e) {
+                            const int o = chunk_index<T>(e, tid), i = first + o;
+                            if (i < lo || i >= hi) continue;
+                            const Key k = make_key(to_float(chunk[o]), i);
+                            if (k > mine) mine = k;
+                        }
+                    }
+                    block_top(sh, warp_sort_desc(mine, lane), kWarps, warp, lane);
+                    const Key best = sh.lists[0][a.top - 1];
+                    if (best > 0) limit = best - 1;  // equal keys are candidates
+                    limit_x = limit ? limit_value(limit) : -INFINITY;
+                }
+                // Threads that may hold a candidate, 16 lanes to each.  In a
+                // later chunk a logit that equals the threshold's ranks
+                // below it.
+                const bool hit = !limit || !(c == 0 ? top < limit_x : top <= limit_x);
+                for (uint32_t m = __ballot_sync(0xffffffffu, hit); m; m &= m - 1) {
+                    const int o = chunk_index<T>(lane & 15, warp * 32 + __ffs(m) - 1), i = first + o;
+                    Key k = 0;
+                    if (lane < kPerThread && i >= lo && i < hi) k = make_key(to_float(chunk[o]), i);
+                    const bool mine = k > limit;
+                    const uint32_t all = __ballot_sync(0xffffffffu, mine);
+                    if (count + __popc(all) > kBuffer) {
+                        const Key kept = warp_list(buffer, count, lane);
+                        __syncwarp();
+                        buffer[lane] = kept;
+                        count = kMaxTop;
+                        const Key least = __shfl_sync(0xffffffffu, kept, a.top - 1);
+                        if (least > limit) limit = least, limit_x = limit_value(limit);
+                    }
+                    if (mine) buffer[count + __popc(all & ((1u << lane) - 1))] = k;
+                    count += __popc(all);
+                    __syncwarp();
                 }
             }
-            if (any) {
-#pragma unroll
-                for (int e = 0; e < kPerThread; ++e) {
-                    const int i = first + chunk_index<T>(e, tid);
-                    if (seeded && x[e] < limit_x) continue;
-                    const Key k = make_key(x[e], i);
-                    if (i >= lo && i < hi && k > limit) sh.buffer[atomicAdd(&sh.count, 1)] = k;
-                }
-            }
-            bound += hits * kPerThread;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.empty[slot]);
+            last = slot, last_phase = phase;
+            if (++slot == kStages) slot = 0, phase ^= 1;
         }
-#pragma unroll
-        for (int e = 0; e < kPerThread; ++e) x[e] = next[e];
-    }
-    Key best = 0;
-    if (a.top > 0) {
+        if (!__syncthreads_and(ok)) break;  // a wait was abandoned, and reported
+        Key best = 0;
+        if (a.top > 0) {
+            block_top(sh, warp_list(buffer, count, lane), kWarps, warp, lane);
+            if (warp == 0) best = sh.lists[0][lane];
+        }
+        st = block_join(sh, st, warp, lane);
+        if (warp == 0) {
+            if (splits == 1) {
+                finish_row<T>(a, unit, st, best, lane, err);
+            } else {
+                Partial &o = part[unit];
+                if (lane == 0) o.m = st.m, o.s = st.s, o.t = st.t;
+                o.keys[lane] = best;
+            }
+        }
         __syncthreads();
-        block_top(sh, warp_list(sh.buffer, sh.count, warp, lane), warp, lane);
-        if (warp == 0) best = sh.lists[0][lane];
     }
-    st = block_join(sh, st, warp, lane);
-    if (warp != 0) return;
-    if (gridDim.x == 1) {
-        finish_row<T>(a, row, st, best, lane, err);
-    } else {
-        Partial &o = part[(int64_t)row * gridDim.x + blockIdx.x];
-        if (lane == 0) o.m = st.m, o.s = st.s, o.t = st.t;
-        o.keys[lane] = best;
-    }
+    if (!ok && tid == 0)  // the copies in flight land before the CTA exits
+        for (uint32_t c = copies > kStages ? copies - kStages : 0; c < copies; ++c)
+            mbar_drain(&sh.full[c % kStages], c / kStages & 1);
 }
 
 // Joins the splits of a row, in split order.  One CTA per row.
@@ -371,7 +487,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_join_kernel(const LogprobAr
     if (a.top > 0) {
         for (int i = warp; i < splits; i += kWarps)  // descending lists already
             best = warp_top_of_two(best, p[i].keys[31 - lane], lane);
-        block_top(sh, best, warp, lane);
+        block_top(sh, best, min(splits, kWarps), warp, lane);
         best = sh.lists[0][lane];
     }
     Stats st{-INFINITY, 0.f, 0.f};
@@ -398,28 +514,21 @@ int current_sms() {
 
 template <typename T>
 cudaError_t launch_typed(const LogprobArgs &a, void *workspace, cudaStream_t s, unsigned int *err) {
-    int splits = logprob_splits(a.rows, a.vocab, current_sms());
+    const int sms = current_sms();
+    if (sms < 1) return cudaErrorInvalidDevice;
+    int splits = logprob_splits(a.rows, a.vocab, sms);
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(token_logprobs_kernel<T>), kRingBytes);
+    if (e != cudaSuccess) return e;
     // a span of whole 128-byte lines
     const int span = ((a.vocab + splits - 1) / splits + 63) / 64 * 64;
     splits = (a.vocab + span - 1) / span;
     Partial *part = static_cast<Partial *>(workspace);
-    for (int r0 = 0; r0 < a.rows; r0 += 65535) {  // the rows are a grid dimension
-        LogprobArgs b = a;
-        b.rows = a.rows - r0 < 65535 ? a.rows - r0 : 65535;
-        b.logits = static_cast<const T *>(a.logits) + (int64_t)r0 * a.row_stride;
-        if (a.tokens) b.tokens = a.tokens + r0, b.logprob = a.logprob + r0;
-        b.entropy = a.entropy + r0;
-        if (a.top) b.top_logprob = a.top_logprob + (int64_t)r0 * a.top, b.top_ids = a.top_ids + (int64_t)r0 * a.top;
-        cudaError_t e = launch_pdl(token_logprobs_kernel<T>, dim3(splits, b.rows), dim3(kThreads), 0, s, b, part, span,
-                                   err);
-        if (e != cudaSuccess) return e;
-        if (splits > 1) {
-            e = launch_pdl(logprobs_join_kernel<T>, dim3(b.rows), dim3(kThreads), 0, s, b, (const Partial *)part,
-                           splits, err);
-            if (e != cudaSuccess) return e;
-        }
-    }
-    return cudaSuccess;
+    const int units = a.rows * splits, ctas = units < 2 * sms ? units : 2 * sms;
+    e = launch_pdl(token_logprobs_kernel<T>, dim3(ctas), dim3(kThreads), kRingBytes, s, a, part, splits, span, units,
+                   err);
+    if (e != cudaSuccess || splits == 1) return e;
+    return launch_pdl(logprobs_join_kernel<T>, dim3(a.rows), dim3(kThreads), 0, s, a, (const Partial *)part, splits,
+                      err);
 }
 
 }  // namespace

@@ -9,79 +9,109 @@ head_dim] in any memory order whose head_dim elements are adjacent (a
 and kv_len [sequences] (its tokens in the cache, the new ones included).
 They are read on the device only, so a captured CUDA graph follows them.
 """
-import ctypes
+import struct
 
 import torch
 
-from ._lib import Y_BF16, Y_F32, _check, _need, _stream, _workspace, _ws_bytes, lib
+from ._lib import Y_BF16, Y_F32, _check, _need, _ws_bytes, lib
 
 MAX_TOP = 32
 
-_TYPES = {torch.float32: Y_F32, torch.bfloat16: Y_BF16}
+_F32, _BF16, _I32, _I64 = torch.float32, torch.bfloat16, torch.int32, torch.int64
+_TYPES = {_F32: Y_F32, _BF16: Y_BF16}
+
+# q4_0_kv_cache: two pointers, six strides, four sizes, the table and its two
+# sizes, two pointers and a size, all 64 bits
+_KV_CACHE = struct.Struct("=18q")
 
 
-class _KvCache(ctypes.Structure):
-    _fields_ = ([("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
-                + [(n, ctypes.c_int64) for n in ("k_page_stride", "k_head_stride", "k_token_stride", "v_page_stride",
-                                                 "v_head_stride", "v_token_stride", "pages", "page_size", "kv_heads",
-                                                 "head_dim")]
-                + [("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("table_width", ctypes.c_int64),
-                   ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("sequences", ctypes.c_int64)])
+# The checks of a call run on every decode step and cost as much as its
+# launches: each tensor gets one short test, and only a misfit goes on to the
+# function that names what is wrong with it.
 
-
-def _strided(t, name, dtype, ndim):
+def _strided(t, name, dtypes, ndim):
     """As _need, but only the last dimension has to be contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dim() != ndim or (t.shape[-1] > 1 and t.stride(-1) != 1):
         raise ValueError(f"{name} must be a {ndim}-D tensor with adjacent elements in its last dimension")
 
 
-def _same_device(*tensors):
-    """Every tensor on the current device: the library launches there."""
-    current = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != current:
-            raise ValueError(f"every tensor must be on the current device (cuda:{current}), got {t.device}")
+def _misplaced(t, name, device):
+    raise ValueError(f"{name} must be on the current device (cuda:{device}), where the call launches, got {t.device}")
 
 
-def _keep(stream, *tensors):
+def _plain(t, name, dtype, ndim, device):
+    """A contiguous tensor of the current device."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.is_contiguous()
+            and t.get_device() == device):
+        _need(t, name, dtype, ndim)
+        _misplaced(t, name, device)
+
+
+def _rows(t, name, dtypes, ndim, device):
+    """A tensor of the current device with adjacent last elements; its
+    strides."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.dim() == ndim and t.get_device() == device:
+        stride = t.stride()
+        if stride[-1] == 1 or t.shape[-1] <= 1:
+            return stride
+    _strided(t, name, dtypes, ndim)
+    _misplaced(t, name, device)
+
+
+def _stream_of(stream, device):
+    """The raw handle of `stream`, the current one when None."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _keep(stream, device, *tensors):
     """Memory made here for work on another stream than the current one is
     not handed out again before that work is done."""
-    if stream is None:
+    if stream is None or _stream_of(stream, device) == _stream_of(None, device):
         return
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
     for t in tensors:
-        if t is not None and s.cuda_stream != torch.cuda.current_stream().cuda_stream:
+        if t is not None:
             t.record_stream(s)
 
 
-def _cache(k_cache, v_cache, page_table, q_start, kv_len):
-    _strided(k_cache, "k_cache", torch.bfloat16, 4)
-    _strided(v_cache, "v_cache", torch.bfloat16, 4)
-    if k_cache.shape != v_cache.shape:
+def _scratch(nbytes, device, workspace):
+    """The caller's workspace or one made here, or None where none is needed."""
+    if workspace is not None:
+        _plain(workspace, "workspace", torch.uint8, 1, device)
+        if workspace.numel() < nbytes:
+            raise ValueError("workspace too small")
+        return workspace
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _cache(k_cache, v_cache, page_table, q_start, kv_len, device):
+    """The q4_0_kv_cache of these tensors, packed, and its heads and head_dim."""
+    ks = _rows(k_cache, "k_cache", (_BF16,), 4, device)
+    vs = _rows(v_cache, "v_cache", (_BF16,), 4, device)
+    ts = _rows(page_table, "page_table", (_I32,), 2, device)
+    _plain(q_start, "q_start", _I32, 1, device)
+    _plain(kv_len, "kv_len", _I32, 1, device)
+    shape = k_cache.shape
+    if shape != v_cache.shape:
         raise ValueError("k_cache and v_cache must have the same shape")
-    _strided(page_table, "page_table", torch.int32, 2)
-    _need(q_start, "q_start", torch.int32, 1)
-    _need(kv_len, "kv_len", torch.int32, 1)
     n = kv_len.shape[0]
-    if q_start.shape[0] != n + 1 or page_table.shape[0] != n:
+    sequences, width = page_table.shape
+    if q_start.shape[0] != n + 1 or sequences != n:
         raise ValueError("page_table, q_start and kv_len must be of sequences, sequences + 1 and sequences rows")
-    _same_device(k_cache, v_cache, page_table, q_start, kv_len)
-    pages, heads, size, dim = k_cache.shape
-    # a dimension of one row has no stride to speak of
-    stride = page_table.stride(0) if n > 1 else page_table.shape[1]
-    return _KvCache(k_cache.data_ptr(), v_cache.data_ptr(), *k_cache.stride()[:3], *v_cache.stride()[:3], pages, size,
-                    heads, dim, page_table.data_ptr(), stride, page_table.shape[1], q_start.data_ptr(),
-                    kv_len.data_ptr(), n)
-
-
-def _row_stride(t):
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    pages, heads, size, dim = shape
+    packed = _KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], pages,
+                            size, heads, dim, page_table.data_ptr(),
+                            ts[0] if n > 1 else width,  # one row has no stride to speak of
+                            width, q_start.data_ptr(), kv_len.data_ptr(), n)
+    return packed, heads, dim
 
 
 def kv_append(qkv: torch.Tensor, cos_sin: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -97,31 +127,34 @@ def kv_append(qkv: torch.Tensor, cos_sin: torch.Tensor, k_cache: torch.Tensor, v
     (halves of the first rot elements, or neighbours when interleaved).
     positions: int32 [rows], the row of cos_sin to use instead of the
     position in the sequence."""
-    _strided(qkv, "qkv", (torch.float32, torch.bfloat16), 2)
-    _need(cos_sin, "cos_sin", torch.float32, 2)
-    c = _cache(k_cache, v_cache, page_table, q_start, kv_len)
-    rows = qkv.shape[0]
-    if qkv.shape[1] != (q_heads + 2 * c.kv_heads) * c.head_dim:
+    dev = torch.cuda.current_device()
+    qs = _rows(qkv, "qkv", _TYPES, 2, dev)
+    _plain(cos_sin, "cos_sin", _F32, 2, dev)
+    cache, kv_heads, dim = _cache(k_cache, v_cache, page_table, q_start, kv_len, dev)
+    rows, width = qkv.shape
+    if width != (q_heads + 2 * kv_heads) * dim:
         raise ValueError("qkv must be [rows, (q_heads + 2 * kv_heads) * head_dim]")
     if positions is not None:
-        _need(positions, "positions", torch.int32, 1)
+        _plain(positions, "positions", _I32, 1, dev)
         if positions.shape[0] != rows:
             raise ValueError("positions must have one element per row")
-    given = out
+    made = None
     if out is None:
-        out = torch.empty((rows, q_heads, c.head_dim), dtype=torch.bfloat16, device=qkv.device)
-    _need(out, "out", torch.bfloat16, 3)
-    if tuple(out.shape) != (rows, q_heads, c.head_dim):
-        raise ValueError("out must be [rows, q_heads, head_dim]")
-    _same_device(qkv, cos_sin, positions, out)
+        out = made = torch.empty((rows, q_heads, dim), dtype=_BF16, device=dev)
+    else:
+        _plain(out, "out", _BF16, 3, dev)
+        if tuple(out.shape) != (rows, q_heads, dim):
+            raise ValueError("out must be [rows, q_heads, head_dim]")
     if rows == 0:
         return out
-    _check(lib().q4_0_kv_append(qkv.data_ptr(), _TYPES[qkv.dtype], _row_stride(qkv), rows, q_heads,
-                                cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)),
-                                positions.data_ptr() if positions is not None else None, out.data_ptr(),
-                                ctypes.byref(c), _stream(stream)), "q4_0_kv_append")
-    if given is None:
-        _keep(stream, out)
+    turns, rot = cos_sin.shape
+    st = lib().q4_0_kv_append(qkv.data_ptr(), _TYPES[qkv.dtype], qs[0] if rows > 1 else width, rows, q_heads,
+                              cos_sin.data_ptr(), turns, rot, 1 if interleaved else 0,
+                              positions.data_ptr() if positions is not None else None, out.data_ptr(), cache,
+                              _stream_of(stream, dev))
+    if st:
+        _check(st, "q4_0_kv_append")
+    _keep(stream, dev, made)
     return out
 
 
@@ -144,30 +177,34 @@ def attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
     natural logarithms of the softmax sums."""
     if out_dtype not in _TYPES:
         raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
-    _strided(q, "q", torch.bfloat16, 3)
-    c = _cache(k_cache, v_cache, page_table, q_start, kv_len)
-    rows, q_heads, dim = q.shape
-    if dim != c.head_dim:
+    dev = torch.cuda.current_device()
+    qs = _rows(q, "q", (_BF16,), 3, dev)
+    cache, kv_heads, cache_dim = _cache(k_cache, v_cache, page_table, q_start, kv_len, dev)
+    rows, q_heads, dim = shape = q.shape
+    if dim != cache_dim:
         raise ValueError("q and the cache must have the same head_dim")
-    given = out
+    made = None
     if out is None:
-        out = torch.empty((rows, q_heads, dim), dtype=out_dtype, device=q.device)
-    _need(out, "out", out_dtype, 3)
-    if tuple(out.shape) != (rows, q_heads, dim):
-        raise ValueError("out must be [rows, q_heads, head_dim]")
+        out = made = torch.empty(shape, dtype=out_dtype, device=dev)
+    else:
+        _plain(out, "out", out_dtype, 3, dev)
+        if out.shape != shape:
+            raise ValueError("out must be [rows, q_heads, head_dim]")
     if lse is not None:
-        _need(lse, "lse", torch.float32, 2)
+        _plain(lse, "lse", _F32, 2, dev)
         if tuple(lse.shape) != (rows, q_heads):
             raise ValueError("lse must be [rows, q_heads]")
-    _same_device(q, out, lse, workspace)
     if rows == 0:
         return out
-    ws, wsb = _workspace(attention_workspace_bytes(rows, q_heads, c.kv_heads, dim, max_q_len), q.device, workspace)
-    _check(lib().q4_0_attention(q.data_ptr(), q.stride(0), q.stride(1), out.data_ptr(), _TYPES[out_dtype],
-                                lse.data_ptr() if lse is not None else None, rows, q_heads, max_q_len,
-                                dim ** -0.5 if scale is None else scale, window, sinks, ctypes.byref(c),
-                                ws.data_ptr() if ws is not None else None, wsb, _stream(stream)), "q4_0_attention")
-    _keep(stream, out if given is None else None, ws if workspace is None else None)
+    ws = _scratch(attention_workspace_bytes(rows, q_heads, kv_heads, dim, max_q_len), dev, workspace)
+    st = lib().q4_0_attention(q.data_ptr(), qs[0], qs[1], out.data_ptr(), _TYPES[out_dtype],
+                              lse.data_ptr() if lse is not None else None, rows, q_heads, max_q_len,
+                              dim ** -0.5 if scale is None else scale, window, sinks, cache,
+                              ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
+                              _stream_of(stream, dev))
+    if st:
+        _check(st, "q4_0_attention")
+    _keep(stream, dev, made, ws if workspace is None else None)
     return out
 
 
@@ -182,23 +219,25 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, top: int = 0, 
     or bf16): the log probability of tokens[row] (int64; negative: none, 0),
     the row's entropy in nats, and its `top` largest log probabilities with
     their ids ([rows, top], largest first, equal logits by lowest id)."""
-    _strided(logits, "logits", (torch.float32, torch.bfloat16), 2)
-    _need(tokens, "tokens", torch.int64, 1)
+    dev = torch.cuda.current_device()
+    ls = _rows(logits, "logits", _TYPES, 2, dev)
+    _plain(tokens, "tokens", _I64, 1, dev)
     rows, vocab = logits.shape
     if tokens.shape[0] != rows:
         raise ValueError("tokens must have one element per row of logits")
-    _same_device(logits, tokens, workspace)
-    dev = logits.device
-    stats = torch.empty((2, rows), dtype=torch.float32, device=dev)
-    top_logprob = torch.empty((rows, max(top, 0)), dtype=torch.float32, device=dev)
-    top_ids = torch.empty((rows, max(top, 0)), dtype=torch.int64, device=dev)
+    logprob = torch.empty(rows, dtype=_F32, device=dev)
+    entropy = torch.empty(rows, dtype=_F32, device=dev)
+    top_logprob = torch.empty((rows, max(top, 0)), dtype=_F32, device=dev)
+    top_ids = torch.empty((rows, max(top, 0)), dtype=_I64, device=dev)
     if rows == 0:
-        return stats[0], stats[1], top_logprob, top_ids
-    ws, wsb = _workspace(token_logprobs_workspace_bytes(rows, vocab, top), dev, workspace)
-    _check(lib().q4_0_token_logprobs(logits.data_ptr(), _TYPES[logits.dtype], _row_stride(logits), rows, vocab,
-                                     tokens.data_ptr(), top, stats[0].data_ptr(), stats[1].data_ptr(),
-                                     top_logprob.data_ptr() if top else None, top_ids.data_ptr() if top else None,
-                                     ws.data_ptr() if ws is not None else None, wsb, _stream(stream)),
-           "q4_0_token_logprobs")
-    _keep(stream, stats, top_logprob, top_ids, ws if workspace is None else None)
-    return stats[0], stats[1], top_logprob, top_ids
+        return logprob, entropy, top_logprob, top_ids
+    ws = _scratch(token_logprobs_workspace_bytes(rows, vocab, top), dev, workspace)
+    st = lib().q4_0_token_logprobs(logits.data_ptr(), _TYPES[logits.dtype], ls[0] if rows > 1 else vocab, rows, vocab,
+                                   tokens.data_ptr(), top, logprob.data_ptr(), entropy.data_ptr(),
+                                   top_logprob.data_ptr() if top else None, top_ids.data_ptr() if top else None,
+                                   ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
+                                   _stream_of(stream, dev))
+    if st:
+        _check(st, "q4_0_token_logprobs")
+    _keep(stream, dev, logprob, entropy, top_logprob, top_ids, ws if workspace is None else None)
+    return logprob, entropy, top_logprob, top_ids
