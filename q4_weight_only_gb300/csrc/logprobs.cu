@@ -37,7 +37,7 @@ namespace q4_0 {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 512;                       // that take logits; one more warp copies
 constexpr int kWarps = kThreads / 32;
 constexpr int kPerThread = 16;                     // logits of one thread in a chunk
 constexpr int kChunk = kThreads * kPerThread;
@@ -136,17 +136,17 @@ struct Shared {
 // `lists` warps; the result is in sh.lists[0] after the call (which starts
 // and ends with a barrier).
 __device__ __forceinline__ void block_top(Shared &sh, Key mine, int lists, int warp, int lane) {
-    __syncthreads();
+    named_bar_sync(1, kThreads);
     sh.lists[warp][lane] = warp < lists ? mine : 0;
     for (int step = kWarps / 2; step >= 1; step >>= 1) {
         if (step >= lists) continue;
-        __syncthreads();
+        named_bar_sync(1, kThreads);
         if (warp < step) {
             mine = warp_top_of_two(mine, sh.lists[warp + step][31 - lane], lane);
             sh.lists[warp][lane] = mine;
         }
     }
-    __syncthreads();
+    named_bar_sync(1, kThreads);
 }
 
 // The 32 largest of a warp's n buffered keys, descending.
@@ -177,21 +177,33 @@ __device__ __forceinline__ Stats join(const Stats &a, const Stats &b) {
     return r;
 }
 
-// The block's statistics from each thread's, in every thread of warp 0.
-__device__ __forceinline__ Stats block_join(Shared &sh, Stats v, int warp, int lane) {
+// The warp's statistics from its lanes'.
+__device__ __forceinline__ Stats warp_join(Stats v) {
+    float m = v.m;
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1)
-        v = join(v, Stats{__shfl_xor_sync(0xffffffffu, v.m, d), __shfl_xor_sync(0xffffffffu, v.s, d),
-                          __shfl_xor_sync(0xffffffffu, v.t, d)});
+    for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    // a lane without any finite logit has s = t = 0, and its shift is cut off
+    const float base = m == -INFINITY ? 0.f : m, d0 = fmaxf(v.m - base, -1e30f), f = ex2(d0);
+    v.t = (v.t + d0 * v.s) * f;
+    v.s *= f;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) {
+        v.s += __shfl_xor_sync(0xffffffffu, v.s, d);
+        v.t += __shfl_xor_sync(0xffffffffu, v.t, d);
+    }
+    v.m = m;
+    return v;
+}
+
+// The block's statistics from each thread's, in warp 0.
+__device__ __forceinline__ Stats block_join(Shared &sh, Stats v, int warp, int lane) {
+    v = warp_join(v);
     if (lane == 0) sh.m[warp] = v.m, sh.s[warp] = v.s, sh.t[warp] = v.t;
-    __syncthreads();
+    named_bar_sync(1, kThreads);
     if (warp == 0) {
         const int w = lane < kWarps ? lane : 0;
-        v = Stats{lane < kWarps ? sh.m[w] : -INFINITY, lane < kWarps ? sh.s[w] : 0.f, lane < kWarps ? sh.t[w] : 0.f};
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1)
-            v = join(v, Stats{__shfl_xor_sync(0xffffffffu, v.m, d), __shfl_xor_sync(0xffffffffu, v.s, d),
-                              __shfl_xor_sync(0xffffffffu, v.t, d)});
+        v = warp_join(Stats{lane < kWarps ? sh.m[w] : -INFINITY, lane < kWarps ? sh.s[w] : 0.f,
+                            lane < kWarps ? sh.t[w] : 0.f});
     }
     return v;
 }
@@ -205,23 +217,32 @@ __device__ __forceinline__ float to_float(__nv_bfloat16 v) {
     return __bfloat162float(v);
 }
 
-// Results of one row, written by warp 0 (lane l has the l-th largest key).
+// The given token of a row, and its logit where there is one.
+struct Given {
+    int64_t token;
+    float x;
+};
+
 template <typename T>
-__device__ __forceinline__ void finish_row(const LogprobArgs &a, int row, Stats v, Key best, int lane,
+__device__ __forceinline__ float given_logit(const LogprobArgs &a, int row, int64_t token) {
+    if (token < 0 || token >= a.vocab) return 0.f;
+    return to_float(static_cast<const T *>(a.logits)[(int64_t)row * a.row_stride + token]);
+}
+
+// Results of one row, written by warp 0 (lane l has the l-th largest key,
+// lane 0 the given token).
+__device__ __forceinline__ void finish_row(const LogprobArgs &a, int row, const Given &g, Stats v, Key best, int lane,
                                            unsigned int *err) {
     const bool empty = v.m == -INFINITY && v.s == 0.f;  // every logit is -inf
     const float log_s = log2f(v.s);
     const float lse = empty ? -INFINITY : (v.m + log_s) * kLn2;
     if (lane == 0) {
-        float lp = 0.f;
         if (a.tokens) {
-            const int64_t token = a.tokens[row];
-            if (token >= a.vocab) {
+            float lp = empty ? -INFINITY : g.x - lse;
+            if (g.token < 0) lp = 0.f;
+            if (g.token >= a.vocab) {
                 atomicExch(err, kErrBadIndex);
                 lp = __uint_as_float(0x7FC00000u);
-            } else if (token >= 0) {
-                const float x = to_float(static_cast<const T *>(a.logits)[(int64_t)row * a.row_stride + token]);
-                lp = empty ? -INFINITY : x - lse;
             }
             a.logprob[row] = lp;
         }
@@ -305,7 +326,7 @@ struct Span {
 // ring runs on over their ends, so the next unit's first chunks arrive while
 // the last one is finished.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const LogprobArgs a, Partial *part, int splits,
+__global__ void __launch_bounds__(kThreads + 32, 2) token_logprobs_kernel(const LogprobArgs a, Partial *part, int splits,
                                                                      int span, int units, unsigned int *err) {
     constexpr int kChunkBytes = kChunk * sizeof(T), kStages = kRingBytes / kChunkBytes;
     extern __shared__ __align__(128) uint8_t ring[];
@@ -322,28 +343,42 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const Logpr
     __syncthreads();
     pdl_launch_dependents();
     pdl_wait();
-    // thread 0: the next chunk to copy
-    int next_unit = blockIdx.x, next_chunk = 0, next_slot = 0;
-    uint32_t copies = 0;
-    auto copy = [&]() {
-        if (next_unit >= units) return;
-        const Span<T> w(a, next_unit, splits, span);
-        const uint32_t bytes = w.bytes(next_chunk);
-        mbar_arrive_expect_tx(&sh.full[next_slot], bytes);
-        bulk_g2s(ring + next_slot * kChunkBytes, w.src + (int64_t)next_chunk * kChunk, bytes, &sh.full[next_slot]);
-        ++copies;
-        if (++next_slot == kStages) next_slot = 0;
-        if (++next_chunk == w.chunks) next_chunk = 0, next_unit += gridDim.x;
-    };
-    if (tid == 0)
-        for (int i = 0; i < kStages; ++i) copy();
+    if (warp == kWarps) {
+        // copies of all chunks, in order; a warp of its own, because every
+        // delay of it starves the others
+        if (lane != 0) return;
+        uint32_t copies = 0, phase = 1;
+        int slot = 0;
+        bool ok = true;
+        for (int unit = blockIdx.x; unit < units && ok; unit += gridDim.x) {
+            const Span<T> w(a, unit, splits, span);
+            for (int c = 0; c < w.chunks && ok; ++c) {
+                ok = mbar_wait(&sh.empty[slot], phase, &sh.abort, err);
+                if (!ok) break;
+                const uint32_t bytes = w.bytes(c);
+                mbar_arrive_expect_tx(&sh.full[slot], bytes);
+                bulk_g2s(ring + slot * kChunkBytes, w.src + (int64_t)c * kChunk, bytes, &sh.full[slot]);
+                ++copies;
+                if (++slot == kStages) slot = 0, phase ^= 1;
+            }
+        }
+        // the last copies land before the CTA may exit
+        for (uint32_t c = copies > kStages ? copies - kStages : 0; c < copies; ++c)
+            mbar_drain(&sh.full[c % kStages], c / kStages & 1);
+        return;
+    }
     bool ok = true;
-    int slot = 0, last = -1;  // places of this and of the last chunk
-    uint32_t phase = 0, last_phase = 0;
+    int slot = 0;
+    uint32_t phase = 0;
 
     for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
         const Span<T> w(a, unit, splits, span);
         const int lo = w.lo, hi = w.hi;
+        // the token is read at the start of the row and its logit at the last
+        // chunk: waited for where it is used, each would show
+        Given given{-1, 0.f};
+        const bool mine_to_give = tid == 0 && splits == 1 && a.tokens;
+        if (mine_to_give) given.token = a.tokens[unit];
         Stats st{-INFINITY, 0.f, 0.f};
         Key limit = 0;                // candidates are keys above it; the same across the warp
         float limit_x = -INFINITY;    // its value
@@ -351,11 +386,6 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const Logpr
         Key *buffer = sh.buffer[warp];
         for (int c = 0; c < w.chunks; ++c) {
             const int first = w.begin + c * kChunk;
-            if (tid == 0 && last >= 0 && ok) {
-                // refill the last chunk's place once every warp has left it
-                ok = mbar_wait(&sh.empty[last], last_phase, &sh.abort, err);
-                if (ok) copy();
-            }
             ok = mbar_wait(&sh.full[slot], phase, &sh.abort, err) && ok;
             float x[kPerThread];
             load_chunk<T>(reinterpret_cast<const T *>(ring + slot * kChunkBytes), first < lo || first + kChunk > hi,
@@ -398,6 +428,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const Logpr
             st.s = u + v;
             unpack2(t2, u, v);
             st.t = u + v;
+            if (mine_to_give && c + 1 == w.chunks) given.x = given_logit<T>(a, unit, given.token);
             const T *chunk = reinterpret_cast<const T *>(ring + slot * kChunkBytes);
             if (a.top > 0) {
                 if (c == 0) {
@@ -448,10 +479,9 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const Logpr
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.empty[slot]);
-            last = slot, last_phase = phase;
             if (++slot == kStages) slot = 0, phase ^= 1;
         }
-        if (!__syncthreads_and(ok)) break;  // a wait was abandoned, and reported
+        if (named_bar_or(1, kThreads, !ok)) break;  // a wait was abandoned, and reported
         Key best = 0;
         if (a.top > 0) {
             block_top(sh, warp_list(buffer, count, lane), kWarps, warp, lane);
@@ -460,18 +490,16 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const Logpr
         st = block_join(sh, st, warp, lane);
         if (warp == 0) {
             if (splits == 1) {
-                finish_row<T>(a, unit, st, best, lane, err);
+                finish_row(a, unit, given, st, best, lane, err);
             } else {
                 Partial &o = part[unit];
                 if (lane == 0) o.m = st.m, o.s = st.s, o.t = st.t;
                 o.keys[lane] = best;
             }
         }
-        __syncthreads();
+        // the other warps go on: they meet warp 0 before they write what it
+        // still reads
     }
-    if (!ok && tid == 0)  // the copies in flight land before the CTA exits
-        for (uint32_t c = copies > kStages ? copies - kStages : 0; c < copies; ++c)
-            mbar_drain(&sh.full[c % kStages], c / kStages & 1);
 }
 
 // Joins the splits of a row, in split order.  One CTA per row.
@@ -483,6 +511,8 @@ __global__ void __launch_bounds__(kThreads) logprobs_join_kernel(const LogprobAr
     pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = blockIdx.x;
     const Partial *p = part + (int64_t)row * splits;
+    Given given{-1, 0.f};
+    if (tid == 0 && a.tokens) given.token = a.tokens[row];
     Key best = 0;
     if (a.top > 0) {
         for (int i = warp; i < splits; i += kWarps)  // descending lists already
@@ -490,10 +520,11 @@ __global__ void __launch_bounds__(kThreads) logprobs_join_kernel(const LogprobAr
         block_top(sh, best, min(splits, kWarps), warp, lane);
         best = sh.lists[0][lane];
     }
+    if (tid == 0) given.x = given_logit<T>(a, row, given.token);
     Stats st{-INFINITY, 0.f, 0.f};
     for (int i = tid; i < splits; i += kThreads) st = join(st, Stats{p[i].m, p[i].s, p[i].t});
     st = block_join(sh, st, warp, lane);
-    if (warp == 0) finish_row<T>(a, row, st, best, lane, err);
+    if (warp == 0) finish_row(a, row, given, st, best, lane, err);
 }
 
 // Splits of a row: enough CTAs for two per SM, none with less than
@@ -524,7 +555,7 @@ cudaError_t launch_typed(const LogprobArgs &a, void *workspace, cudaStream_t s, 
     splits = (a.vocab + span - 1) / span;
     Partial *part = static_cast<Partial *>(workspace);
     const int units = a.rows * splits, ctas = units < 2 * sms ? units : 2 * sms;
-    e = launch_pdl(token_logprobs_kernel<T>, dim3(ctas), dim3(kThreads), kRingBytes, s, a, part, splits, span, units,
+    e = launch_pdl(token_logprobs_kernel<T>, dim3(ctas), dim3(kThreads + 32), kRingBytes, s, a, part, splits, span, units,
                    err);
     if (e != cudaSuccess || splits == 1) return e;
     return launch_pdl(logprobs_join_kernel<T>, dim3(a.rows), dim3(kThreads), 0, s, a, (const Partial *)part, splits,
