@@ -60,6 +60,7 @@ struct Params {
     int rows, q_heads, kv_heads, group, window, sinks;
     int tokens;  // per tile: 128 / group
     int box;     // token rows of one K or V copy
+    int cost[2];  // of a key tile of a narrow item and of one of two tiles
     int max_q_len;
     int piece_rows;  // rows a piece can have: one tile's when max_q_len fits it
     float scale_log2;
@@ -141,7 +142,7 @@ struct Item {
 };
 
 struct Start {
-    int64_t left;
+    int64_t left;  // cost from the start of the first item to the end of the share
     int head, b, item, t0;
     Sequence s;
     int64_t warp_sum[kThreads / 32];
@@ -152,17 +153,24 @@ __device__ __forceinline__ Sequence shuffle(const Sequence &s, int lane) {
                     __shfl_sync(0xffffffffu, s.kv, lane)};
 }
 
-// Key tiles (of one key head) of each lane's sequence; the warp takes the
-// items of a long one together.
-__device__ __forceinline__ int64_t sequence_tiles(const Params &p, const Sequence &s, int lane) {
+__device__ __forceinline__ int tile_cost(const Params &p, const Range &r) { return p.cost[r.tokens > p.tokens]; }
+
+__device__ __forceinline__ int64_t item_cost(const Params &p, const Sequence &s, int item) {
+    const Range r = item_range(p, s, item);
+    return (int64_t)r.n * tile_cost(p, r);
+}
+
+// Cost (for one key head) of each lane's sequence; the warp takes the items
+// of a long one together.
+__device__ __forceinline__ int64_t sequence_cost(const Params &p, const Sequence &s, int lane) {
     const int n = items_of(p, s);
-    int64_t mine = n == 1 ? item_range(p, s, 0).n : 0;
+    int64_t mine = n == 1 ? item_cost(p, s, 0) : 0;
     for (uint32_t many = __ballot_sync(0xffffffffu, n > 1); many; many &= many - 1) {
         const int src = __ffs(many) - 1;
         const Sequence t = shuffle(s, src);
         const int nt = items_of(p, t);
         int64_t sum = 0;
-        for (int i = lane; i < nt; i += 32) sum += item_range(p, t, i).n;
+        for (int i = lane; i < nt; i += 32) sum += item_cost(p, t, i);
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         if (lane == src) mine = sum;
@@ -192,14 +200,14 @@ __device__ __forceinline__ T share_start(T all, T n, T i) {
 __device__ __forceinline__ void locate(const Params &p, Start &st, int cta, int ctas) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     Sequence s;
-    int64_t mine, first;  // key tiles of this thread's sequence, and of the ones before it
-    int64_t before = 0;   // key tiles of earlier rounds' sequences
+    int64_t mine, first;  // cost of this thread's sequence, and of the ones before it
+    int64_t before = 0;   // cost of earlier rounds' sequences
     // a round: one sequence a thread
     auto round = [&](int b0) {
         const int b = b0 + tid;
         s = Sequence{0, 0, 0};
         if (b < p.sequences) s = sequence(p, b);
-        mine = sequence_tiles(p, s, lane);
+        mine = sequence_cost(p, s, lane);
         const int64_t incl = warp_inclusive(mine, lane);
         if (lane == 31) st.warp_sum[warp] = incl;
         __syncthreads();
@@ -220,9 +228,10 @@ __device__ __forceinline__ void locate(const Params &p, Start &st, int cta, int 
         if (cta == 0 && b < p.sequences && !sequence_fits(p, s, b)) atomicExch(p.err, kErrBadIndex);
     }
     const int64_t each = before, all = each * p.kv_heads;
-    // no share is empty before the last one that is not: an item's pieces are
-    // in consecutive CTAs
-    const int64_t n = min(all, (int64_t)ctas);
+    // A key tile belongs to the share in which it ends.  Every share but the
+    // empty ones at the end has a tile (it is at least one tile's cost long):
+    // an item's pieces are in consecutive CTAs.
+    const int64_t n = min(max(all / p.cost[1], (int64_t)(all > 0)), (int64_t)ctas);
     if (cta >= n) {
         if (tid == 0) st.left = 0;
         __syncthreads();
@@ -239,7 +248,7 @@ __device__ __forceinline__ void locate(const Params &p, Start &st, int cta, int 
         u1 = share_start<int64_t>(all, n, cta + 1);
         head = (int)(u0 / each);
     }
-    const int64_t goal = u0 - head * each;  // the share's first tile within its key head
+    const int64_t goal = u0 - head * each;  // where the share begins within its key head
     const bool again = p.sequences > kThreads;
     before = 0;
     for (int b0 = 0; b0 < p.sequences; b0 += kThreads) {
@@ -252,11 +261,13 @@ __device__ __forceinline__ void locate(const Params &p, Start &st, int cta, int 
         const int nt = items_of(p, t);
         int64_t rest = goal - __shfl_sync(0xffffffffu, first, src);
         for (int i0 = 0; i0 < nt; i0 += 32) {
-            const int k = i0 + lane < nt ? item_range(p, t, i0 + lane).n : 0;
-            const int64_t incl = warp_inclusive((int64_t)k, lane);
+            const int64_t k = i0 + lane < nt ? item_cost(p, t, i0 + lane) : 0;
+            const int64_t incl = warp_inclusive(k, lane);
             if (rest >= incl - k && rest < incl) {
-                st.head = head, st.b = b0 + warp * 32 + src, st.item = i0 + lane, st.t0 = (int)(rest - (incl - k));
-                st.left = u1 - u0, st.s = t;
+                const int64_t in = rest - (incl - k);
+                st.head = head, st.b = b0 + warp * 32 + src, st.item = i0 + lane, st.s = t;
+                st.t0 = (int)(in / tile_cost(p, item_range(p, t, i0 + lane)));
+                st.left = u1 - u0 + in;
             }
             const int64_t sum = __shfl_sync(0xffffffffu, incl, 31);
             if (rest < sum) break;
@@ -264,6 +275,15 @@ __device__ __forceinline__ void locate(const Params &p, Start &st, int cta, int 
         }
     }
     __syncthreads();
+}
+
+// f(0), f(1), ... f(N - 1) with constants as arguments.
+template <int N, typename F>
+__device__ __forceinline__ void each_step(F &&f) {
+    if constexpr (N > 0) {
+        each_step<N - 1>(f);
+        f(std::integral_constant<uint32_t, N - 1>{});
+    }
 }
 
 template <int D>
@@ -479,13 +499,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             int n_items = items_of(p, s);
             for (;; ++items) {
                 Item o{};
+                int64_t cost = 0;
                 if (left > 0) {
                     const Range r = item_range(p, s, it);
-                    o.t0 = t0, o.t1 = (int)min((int64_t)r.n, t0 + left), o.n = r.n;
+                    const int each = tile_cost(p, r);
+                    cost = (int64_t)r.n * each;
+                    o.t0 = t0, o.t1 = left >= cost ? r.n : (int)(left / each), o.n = r.n;
                     o.head = head, o.b = b, o.row0 = s.row0 + it * 2 * p.tokens, o.tokens = r.tokens, o.pos0 = r.pos0;
                     o.lo = r.lo, o.hi = r.hi, o.sink_end = r.sink_end, o.sink_tiles = r.sink_tiles, o.wtile = r.wtile;
                     if (o.t0 > 0) flags |= kHeadPiece | (o.t1 < o.n ? kHeadGoesOn : 0);
-                    if (o.t0 == 0 && o.t1 < o.n) flags |= kTailPiece, tail = make_int4(0, b, it, head);
+                    if (o.t0 == 0 && o.t1 > 0 && o.t1 < o.n) flags |= kTailPiece, tail = make_int4(0, b, it, head);
                 }
                 const int i = items % kItems;
                 if (!__all_sync(0xffffffffu,
@@ -496,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&bar.item_full[i]);
                 }
                 __syncwarp();
-                left -= o.t1 - o.t0;
+                left -= cost;
                 if (o.t0 == o.t1) break;
                 t0 = 0;
                 if (left > 0 && ++it >= n_items) {
@@ -525,29 +548,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag, p.err));
             return ok;
         };
-        // The instruction rate of this warp bounds the loop unless the
-        // descriptors are one addition each: 32-bit sums on the low word (the
-        // start address), which no offset carries out of.
-        const uint64_t q_desc = smem_desc_k128(smem + L::kQ), k_desc = smem_desc_k128(ring);
-        const uint64_t v_desc = smem_desc_mn128(ring, L::kBlock);
+        // The instruction rate of this warp bounds the loop: each descriptor
+        // is one addition to the low word (the start address), which no
+        // offset carries out of.
+        const uint64_t q_desc = smem_desc_k128(smem + L::kQ), v_desc = smem_desc_mn128(ring, L::kBlock);
+        const uint32_t hi = (uint32_t)(q_desc >> 32);  // the same for all three
+        const uint32_t q_lo = (uint32_t)q_desc, k_lo = (uint32_t)smem_desc_k128(ring), v_lo = (uint32_t)v_desc;
         constexpr uint32_t kTileStep = L::kTileBytes >> 4, kBlockStep = L::kBlock >> 4;
-        // S_g = Q K^T with tile `q` of Q (one elected thread)
+        // S_g = Q K^T with tile `q` of Q's buffers (one elected thread)
         auto scores = [&](int g, int q, uint32_t slot) {
-            const uint64_t a = q_desc + q * kTileStep, b = k_desc + slot * kTileStep;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint32_t step = (k >> 2) * kBlockStep + 2 * (k & 3);
-                mma_f16_ss(tmem + col_s(g), a + step, b + step, idesc_qk, k != 0);
-            }
+            const uint32_t a = q_lo + q * kTileStep, b = k_lo + slot * kTileStep, d = tmem + col_s(g);
+            each_step<D / 16>([&](auto step) {
+                constexpr uint32_t k = decltype(step)::value, off = (k >> 2) * kBlockStep + 2 * (k & 3);
+                mma_f16_ss_at<off, off>(d, a, b, hi, idesc_qk, k != 0);
+            });
             mma_commit(&bar.s_full[g]);
         };
         // O_g (+)= P_g V (one elected thread)
         auto values = [&](int g, uint32_t slot, bool first) {
-            const uint64_t b = v_desc + slot * kTileStep;
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-                mma_f16_ts(tmem + col_o(g), tmem + col_s(g) + 8 * k, b + (uint32_t)(k * (16 * 128 >> 4)), idesc_pv,
-                           !first || k != 0);
+            const uint32_t a = tmem + col_s(g), b = v_lo + slot * kTileStep, d = tmem + col_o(g);
+            each_step<kTile / 16>([&](auto step) {
+                constexpr uint32_t k = decltype(step)::value;
+                mma_f16_ts_at<8 * k, k * (16 * 128 >> 4)>(d, a, b, hi, idesc_pv, !first || k != 0);
+            });
             mma_commit(&bar.o_full[g]);
         };
         auto release = [&](uint64_t *b) {
@@ -1013,6 +1036,10 @@ cudaError_t launch_d(const AttentionArgs &a, const KvCacheView &c, void *workspa
     p.scale_log2 = a.scale * kLog2e;
     p.out = a.out, p.lse = a.lse, p.out_bf16 = a.out_bf16;
     p.max_q_len = a.max_q_len;
+    // Where both kinds of item can meet, a key tile of two tiles takes about
+    // 1.7 us and one of a narrow item 1.2.
+    const bool mixed = a.max_q_len > p.tokens;
+    p.cost[0] = mixed ? 2 : 1, p.cost[1] = mixed ? 3 : 1;
     p.piece_rows = item_rows(p.group, a.max_q_len);
     const WorkspaceLayout w(ctas, D, p.piece_rows);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
