@@ -1,16 +1,17 @@
 // logprobs.cu -- log probability of a given token per row of logits, with
 // the row's entropy and its top alternatives (declared in include/q4_0.h).
 //
-// Mathematics, over one read of a row x in base 2, y = x log2 e - m with a
-// running reference m:
+// Mathematics, over one read of a row x: with a running maximum m and, in
+// base 2, y = (x - m) log2 e,
 //   s = sum 2^y,   t = sum y 2^y,
-// both rescaled when m grows (t also shifts: t + (m_old - m_new) s), so
-//   lse = (m + log2 s) ln 2,  logprob = x[token] - lse,
-//   entropy = (log2 s - t / s) ln 2.
-// All statistics are fp32; m is the rounded product that y uses, so its
-// rounding cancels in lse.  Ranking uses 64-bit keys (order-preserving bits
-// of x, then the complement of the index), so equal logits rank by lowest
-// index whatever order threads meet them in.
+// both rescaled when m grows (t also shifts by (m_old - m_new) log2 e s),
+//   logprob = (x[token] - m) - ln s,  entropy = (log2 s - t / s) ln 2.
+// y is one fma, x log2 e - (m log2 e); the rounding of its product is the
+// same for all of a row and is taken out of ln s at the end.  Logits near the
+// ends of fp32's range (the type's lowest value, as a mask) would overflow
+// there, and are subtracted first.  All statistics are fp32.  Ranking uses
+// 64-bit keys (order-preserving bits of x, then the complement of the index),
+// so equal logits rank by lowest index whatever order threads meet them in.
 //
 // Top alternatives in the same read: every warp keeps a threshold key, below
 // the row's k-th largest, and appends only larger keys to a buffer of its
@@ -46,6 +47,7 @@ constexpr int kBuffer = 2 * kMaxTop;               // candidate keys a warp hold
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFloor = -1000.f;                  // 2^kFloor is 0, and kFloor * 0 is too
+constexpr float kFar = 1e37f;                      // beyond it x log2 e may overflow
 constexpr int kRingBytes = 96 * 1024;
 
 using Key = unsigned long long;  // 0: none
@@ -165,12 +167,19 @@ struct Stats {
     float m, s, t;
 };
 
+// The exponent that takes sums with reference m to reference `to`, from the
+// products that y uses; where they overflow, different references are further
+// apart than any sum reaches.
+__device__ __forceinline__ float shift(float m, float to) {
+    return m == to ? 0.f : fmaxf(__fmul_rn(m, kLog2e) - __fmul_rn(to, kLog2e), -1e30f);
+}
+
 __device__ __forceinline__ Stats join(const Stats &a, const Stats &b) {
     Stats r;
     r.m = fmaxf(a.m, b.m);
     const float base = r.m == -INFINITY ? 0.f : r.m;
     // a side without any finite logit has s = t = 0, and its shift is cut off
-    const float da = fmaxf(a.m - base, -1e30f), db = fmaxf(b.m - base, -1e30f);
+    const float da = shift(a.m, base), db = shift(b.m, base);
     const float fa = ex2(da), fb = ex2(db);
     r.s = a.s * fa + b.s * fb;
     r.t = (a.t + da * a.s) * fa + (b.t + db * b.s) * fb;
@@ -183,7 +192,7 @@ __device__ __forceinline__ Stats warp_join(Stats v) {
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     // a lane without any finite logit has s = t = 0, and its shift is cut off
-    const float base = m == -INFINITY ? 0.f : m, d0 = fmaxf(v.m - base, -1e30f), f = ex2(d0);
+    const float base = m == -INFINITY ? 0.f : m, d0 = shift(v.m, base), f = ex2(d0);
     v.t = (v.t + d0 * v.s) * f;
     v.s *= f;
 #pragma unroll
@@ -235,10 +244,12 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, int row, const 
                                            unsigned int *err) {
     const bool empty = v.m == -INFINITY && v.s == 0.f;  // every logit is -inf
     const float log_s = log2f(v.s);
-    const float lse = empty ? -INFINITY : (v.m + log_s) * kLn2;
+    // y was taken from the rounded product m log2 e: the rounding, exactly
+    const float rounding = fabsf(v.m) < kFar ? fmaf(v.m, kLog2e, -__fmul_rn(v.m, kLog2e)) : 0.f;
+    const float ln_s = (log_s - rounding) * kLn2;
     if (lane == 0) {
         if (a.tokens) {
-            float lp = empty ? -INFINITY : g.x - lse;
+            float lp = empty ? -INFINITY : (g.x - v.m) - ln_s;
             if (g.token < 0) lp = 0.f;
             if (g.token >= a.vocab) {
                 atomicExch(err, kErrBadIndex);
@@ -251,7 +262,7 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, int row, const 
     }
     if (lane < a.top) {
         const int64_t o = (int64_t)row * a.top + lane;
-        a.top_logprob[o] = empty ? -INFINITY : key_value(best) - lse;
+        a.top_logprob[o] = empty ? -INFINITY : (key_value(best) - v.m) - ln_s;
         a.top_ids[o] = key_index(best);
     }
 }
@@ -398,28 +409,34 @@ __global__ void __launch_bounds__(kThreads + 32, 2) token_logprobs_kernel(const 
                 low = min3(low, x[e], x[e + 1]);
             }
             // a NaN leaves m as it is and reaches s and t below
-            if (top * kLog2e > st.m) {
-                const float m = top * kLog2e, d = fmaxf(st.m - m, -1e30f), f = ex2(d);
+            if (top > st.m) {
+                const float d = shift(st.m, top), f = ex2(d);
                 st.t = (st.t + d * st.s) * f;
                 st.s *= f;
-                st.m = m;
+                st.m = top;
             }
             const float base = st.m == -INFINITY ? 0.f : st.m;
-            const uint64_t c2 = pack2(kLog2e, kLog2e), m2 = pack2(-base, -base);
+            const float product = __fmul_rn(base, kLog2e);
+            const uint64_t c2 = pack2(kLog2e, kLog2e), m2 = pack2(-product, -product);
             uint64_t s2 = pack2(st.s, 0.f), t2 = pack2(st.t, 0.f);
-            // -inf: 2^y is 0, and y 2^y must be
-            auto add = [&](auto cut) {
+            auto add = [&](auto far) {
 #pragma unroll
                 for (int e = 0; e < kPerThread; e += 2) {
                     float y0, y1;
-                    unpack2(fma2(pack2(x[e], x[e + 1]), c2, m2), y0, y1);
-                    if (decltype(cut)::value) y0 = max_nan(y0, kFloor), y1 = max_nan(y1, kFloor);
+                    if (decltype(far)::value) {
+                        // no product that overflows; -inf: 2^y is 0, and
+                        // y 2^y must be
+                        y0 = max_nan((x[e] - base) * kLog2e, kFloor);
+                        y1 = max_nan((x[e + 1] - base) * kLog2e, kFloor);
+                    } else {
+                        unpack2(fma2(pack2(x[e], x[e + 1]), c2, m2), y0, y1);
+                    }
                     const uint64_t p = pack2(ex2(y0), ex2(y1));
                     s2 = add2(s2, p);
                     t2 = fma2(pack2(y0, y1), p, t2);
                 }
             };
-            if (__any_sync(0xffffffffu, low == -INFINITY))
+            if (__any_sync(0xffffffffu, low < -kFar || st.m > kFar))
                 add(std::true_type{});
             else
                 add(std::false_type{});
