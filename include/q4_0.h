@@ -464,16 +464,13 @@ int q4_0_attention(const uint16_t *q, int64_t q_row_stride, int64_t q_head_strid
  * nothing to the entropy.  A row of nothing but -infinity gives -infinity
  * log probabilities and entropy 0; a NaN or +infinity in a row makes its
  * logprob, entropy and top_logprob NaN (NaN ranks first).
- * Workspace: q4_0_token_logprobs_workspace_bytes(rows, vocab, top) bytes on
- * the current device, 256-byte aligned (may be NULL when that is 0).
- * Returns Q4_0_OK, Q4_0_ERR_INVALID_ARG, Q4_0_ERR_UNSUPPORTED,
- * Q4_0_ERR_WORKSPACE or Q4_0_ERR_CUDA.
+ * Returns Q4_0_OK, Q4_0_ERR_INVALID_ARG, Q4_0_ERR_UNSUPPORTED or
+ * Q4_0_ERR_CUDA.
  */
 #define Q4_0_MAX_TOP 32
-size_t q4_0_token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int top);
 int q4_0_token_logprobs(const void *logits, int logits_type, int64_t row_stride, int64_t rows, int64_t vocab,
                         const int64_t *tokens, int top, float *logprob, float *entropy, float *top_logprob,
-                        int64_t *top_ids, void *workspace, size_t workspace_bytes, void *stream);
+                        int64_t *top_ids, void *stream);
 
 /*
  * q4_0_device_error -- read and clear the device error word of the current

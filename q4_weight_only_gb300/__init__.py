@@ -10,9 +10,9 @@ from ._lib import (ERR_CUDA, ERR_DEVICE_INDEX, ERR_DEVICE_TIMEOUT, ERR_INVALID_A
                    ERR_WORKSPACE, OK, Y_BF16, Y_F32, Q4Error, device_error, gemm, gemm_plan, gemv, gemv_alloc, lib, matmul,
                    matmul_alloc, matmul_grouped, grouped_launches, matmul_host, host_workspace_bytes, quantize, selftest_wait_timeout, status_string, version,
                    weight_bytes)
-from .serving import MAX_TOP, attention, attention_workspace_bytes, kv_append, token_logprobs, token_logprobs_workspace_bytes
+from .serving import MAX_TOP, attention, attention_workspace_bytes, kv_append, token_logprobs
 
 __all__ = ["quantize", "matmul", "matmul_alloc", "matmul_grouped", "grouped_launches", "matmul_host", "host_workspace_bytes", "gemv", "gemv_alloc", "gemm", "gemm_plan", "weight_bytes", "device_error",
            "version", "status_string", "lib", "selftest_wait_timeout", "Q4Error", "OK", "ERR_INVALID_ARG",
            "ERR_UNSUPPORTED", "ERR_CUDA", "ERR_DEVICE_TIMEOUT", "ERR_WORKSPACE", "Y_F32", "Y_BF16", "ERR_DEVICE_INDEX",
-           "kv_append", "attention", "attention_workspace_bytes", "token_logprobs", "token_logprobs_workspace_bytes", "MAX_TOP"]
+           "kv_append", "attention", "attention_workspace_bytes", "token_logprobs", "MAX_TOP"]

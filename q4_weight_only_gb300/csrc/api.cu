@@ -553,14 +553,9 @@ int logprobs_sizes(int64_t rows, int64_t vocab, int top) {
 }
 }  // namespace
 
-size_t q4_0_token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int top) {
-    if (rows < 1 || logprobs_sizes(rows, vocab, top) != Q4_0_OK) return 0;
-    return token_logprobs_workspace_bytes((int)rows, (int)vocab, top);
-}
-
 int q4_0_token_logprobs(const void *logits, int logits_type, int64_t row_stride, int64_t rows, int64_t vocab,
                         const int64_t *tokens, int top, float *logprob, float *entropy, float *top_logprob,
-                        int64_t *top_ids, void *workspace, size_t workspace_bytes, void *stream) {
+                        int64_t *top_ids, void *stream) {
     const int st = logprobs_sizes(rows, vocab, top);
     if (st != Q4_0_OK) return st;
     if (!logits || !y_type_ok(logits_type) || !entropy || (tokens && !logprob) || (top && (!top_logprob || !top_ids)))
@@ -572,15 +567,11 @@ int q4_0_token_logprobs(const void *logits, int logits_type, int64_t row_stride,
         (reinterpret_cast<uintptr_t>(entropy) & 3u) || (reinterpret_cast<uintptr_t>(top_logprob) & 3u))
         return Q4_0_ERR_INVALID_ARG;
     if (rows == 0) return Q4_0_OK;
-    const size_t need = q4_0_token_logprobs_workspace_bytes(rows, vocab, top);
-    if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
-        return Q4_0_ERR_WORKSPACE;
     unsigned int *err = device_error_word();
     if (!err) return Q4_0_ERR_CUDA;
     const LogprobArgs a{logits,      row_stride, tokens,    logprob,    entropy,
                         top_logprob, top_ids,    (int)rows, (int)vocab, top};
-    return from_cuda(
-        launch_token_logprobs(a, logits_type == Q4_0_Y_BF16, workspace, static_cast<cudaStream_t>(stream), err));
+    return from_cuda(launch_token_logprobs(a, logits_type == Q4_0_Y_BF16, static_cast<cudaStream_t>(stream), err));
 }
 
 int q4_0_selftest_wait_timeout(int64_t limit_us, void *stream) {

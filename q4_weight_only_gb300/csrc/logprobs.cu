@@ -21,12 +21,19 @@
 // the k-th of them, so any order of the logits is handled.  Warps meet only
 // at the first chunk and the end of a row: with a barrier a chunk, each
 // waited for the one warp that had found candidates.  Code that runs for the
-// few candidates is kept short: unrolled over a thread's 16 logits, each of
-// its rare runs waited a microsecond for instructions.
+// few candidates is kept short (unrolled over a thread's 16 logits, each of
+// its rare runs waited a microsecond for instructions) and takes the logits
+// of two such threads at a time, a lane each (one at a time: 217 us below).
 //
 // Bound by the one read of the logits: chunks of 8192 logits stream through
 // a ring of bulk copies (96 KB in flight a block, two blocks an SM) that
-// runs on over the ends of rows.
+// runs on over the ends of rows.  Where there are few rows a cluster of up to
+// eight blocks shares one, and the first of them joins what the others leave
+// in its shared memory: a second kernel for that, with its workspace, made
+// one row of 32000 take 12.5 us, for 10.4.  Measured: 2048 fp32 rows of
+// 131072 take 201 us with 20 alternatives (5.3 TB/s) and 155 us with none
+// (6.9 TB/s, what a copy reaches); 16 bf16 rows of 128257 14.6 us, most of it
+// launch, first chunks and the end of the row.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -49,6 +56,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFloor = -1000.f;                  // 2^kFloor is 0, and kFloor * 0 is too
 constexpr float kFar = 1e37f;                      // beyond it x log2 e may overflow
 constexpr int kRingBytes = 96 * 1024;
+constexpr int kMaxCluster = 8;                     // blocks that share a row
 
 using Key = unsigned long long;  // 0: none
 
@@ -126,12 +134,19 @@ __device__ __forceinline__ Key warp_top_of_two(Key a, Key reversed, int lane) {
 
 constexpr int kMaxStages = 6;
 
+// What a block of a cluster leaves with the first one.
+struct Partial {
+    float m, s, t, unused;
+    Key keys[kMaxTop];
+};
+
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages];
     int abort;
     Key buffer[kWarps][kBuffer];
     Key lists[kWarps][kMaxTop];
     float m[kWarps], s[kWarps], t[kWarps];
+    Partial part[kMaxCluster];
 };
 
 // The block's 32 largest keys from one descending list in each of the first
@@ -306,12 +321,6 @@ __device__ __forceinline__ int chunk_index(int e, int tid) {
     return (e / kV * kThreads + tid) * kV + e % kV;
 }
 
-// Partial results of a row's split: statistics, then the keys.
-struct Partial {
-    float m, s, t, unused;
-    Key keys[kMaxTop];
-};
-
 // A split of a row, and the 16-byte granules that hold it: the copies start
 // at the boundary at or before the first logit and end at the one at or
 // after the last; no other memory is touched.
@@ -333,12 +342,13 @@ struct Span {
     }
 };
 
-// Each CTA takes the units (splits of rows) blockIdx.x, + gridDim.x, ...; its
-// ring runs on over their ends, so the next unit's first chunks arrive while
-// the last one is finished.
+// Each CTA takes the units (rows, or one split of one row) blockIdx.x,
+// + gridDim.x, ...; its ring runs on over their ends, so the next unit's
+// first chunks arrive while the last one is finished.  The splits of a row
+// are the CTAs of a cluster, with one unit each.
 template <typename T>
-__global__ void __launch_bounds__(kThreads + 32, 2) token_logprobs_kernel(const LogprobArgs a, Partial *part, int splits,
-                                                                     int span, int units, unsigned int *err) {
+__global__ void __launch_bounds__(kThreads + 32, 2) token_logprobs_kernel(const LogprobArgs a, int splits, int span,
+                                                                          int units, unsigned int *err) {
     constexpr int kChunkBytes = kChunk * sizeof(T), kStages = kRingBytes / kChunkBytes;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ Shared sh;
@@ -352,15 +362,15 @@ __global__ void __launch_bounds__(kThreads + 32, 2) token_logprobs_kernel(const 
         mbar_fence_init();
     }
     __syncthreads();
+    if (splits > 1) cluster_arrive();  // this block's shared memory is there
     pdl_launch_dependents();
     pdl_wait();
     if (warp == kWarps) {
         // copies of all chunks, in order; a warp of its own, because every
         // delay of it starves the others
-        if (lane != 0) return;
         uint32_t copies = 0, phase = 1;
         int slot = 0;
-        bool ok = true;
+        bool ok = lane == 0;
         for (int unit = blockIdx.x; unit < units && ok; unit += gridDim.x) {
             const Span<T> w(a, unit, splits, span);
             for (int c = 0; c < w.chunks && ok; ++c) {
@@ -376,6 +386,12 @@ __global__ void __launch_bounds__(kThreads + 32, 2) token_logprobs_kernel(const 
         // the last copies land before the CTA may exit
         for (uint32_t c = copies > kStages ? copies - kStages : 0; c < copies; ++c)
             mbar_drain(&sh.full[c % kStages], c / kStages & 1);
+        __syncwarp();
+        if (splits > 1) {
+            cluster_wait();
+            cluster_arrive();
+            cluster_wait();
+        }
         return;
     }
     bool ok = true;
@@ -388,8 +404,8 @@ __global__ void __launch_bounds__(kThreads + 32, 2) token_logprobs_kernel(const 
         // the token is read at the start of the row and its logit at the last
         // chunk: waited for where it is used, each would show
         Given given{-1, 0.f};
-        const bool mine_to_give = tid == 0 && splits == 1 && a.tokens;
-        if (mine_to_give) given.token = a.tokens[unit];
+        const bool mine_to_give = tid == 0 && blockIdx.x % splits == 0 && a.tokens;
+        if (mine_to_give) given.token = a.tokens[unit / splits];
         Stats st{-INFINITY, 0.f, 0.f};
         Key limit = 0;                // candidates are keys above it; the same across the warp
         float limit_x = -INFINITY;    // its value
@@ -445,7 +461,7 @@ __global__ void __launch_bounds__(kThreads + 32, 2) token_logprobs_kernel(const 
             st.s = u + v;
             unpack2(t2, u, v);
             st.t = u + v;
-            if (mine_to_give && c + 1 == w.chunks) given.x = given_logit<T>(a, unit, given.token);
+            if (mine_to_give && c + 1 == w.chunks) given.x = given_logit<T>(a, unit / splits, given.token);
             const T *chunk = reinterpret_cast<const T *>(ring + slot * kChunkBytes);
             if (a.top > 0) {
                 if (c == 0) {
@@ -471,14 +487,19 @@ __global__ void __launch_bounds__(kThreads + 32, 2) token_logprobs_kernel(const 
                     if (best > 0) limit = best - 1;  // equal keys are candidates
                     limit_x = limit ? limit_value(limit) : -INFINITY;
                 }
-                // Threads that may hold a candidate, 16 lanes to each.  In a
+                // Threads that may hold a candidate, two of them a step and
+                // 16 lanes to each.  In a
                 // later chunk a logit that equals the threshold's ranks
                 // below it.
                 const bool hit = !limit || !(c == 0 ? top < limit_x : top <= limit_x);
-                for (uint32_t m = __ballot_sync(0xffffffffu, hit); m; m &= m - 1) {
-                    const int o = chunk_index<T>(lane & 15, warp * 32 + __ffs(m) - 1), i = first + o;
+                for (uint32_t m = __ballot_sync(0xffffffffu, hit); m;) {
+                    const int l0 = __ffs(m) - 1;
+                    m &= m - 1;
+                    const int of = lane < kPerThread ? l0 : m ? __ffs(m) - 1 : -1;
+                    m &= m - 1;
+                    const int o = chunk_index<T>(lane & 15, warp * 32 + max(of, 0)), i = first + o;
                     Key k = 0;
-                    if (lane < kPerThread && i >= lo && i < hi) k = make_key(to_float(chunk[o]), i);
+                    if (of >= 0 && i >= lo && i < hi) k = make_key(to_float(chunk[o]), i);
                     const bool mine = k > limit;
                     const uint32_t all = __ballot_sync(0xffffffffu, mine);
                     if (count + __popc(all) > kBuffer) {
@@ -499,60 +520,59 @@ __global__ void __launch_bounds__(kThreads + 32, 2) token_logprobs_kernel(const 
             if (++slot == kStages) slot = 0, phase ^= 1;
         }
         if (named_bar_or(1, kThreads, !ok)) break;  // a wait was abandoned, and reported
-        Key best = 0;
+        Key ranked = 0;
         if (a.top > 0) {
             block_top(sh, warp_list(buffer, count, lane), kWarps, warp, lane);
-            if (warp == 0) best = sh.lists[0][lane];
+            if (warp == 0) ranked = sh.lists[0][lane];
         }
         st = block_join(sh, st, warp, lane);
-        if (warp == 0) {
-            if (splits == 1) {
-                finish_row(a, unit, given, st, best, lane, err);
-            } else {
-                Partial &o = part[unit];
-                if (lane == 0) o.m = st.m, o.s = st.s, o.t = st.t;
-                o.keys[lane] = best;
-            }
+        if (splits == 1) {
+            if (warp == 0) finish_row(a, unit, given, st, ranked, lane, err);
+            // the other warps go on: they meet warp 0 before they write what
+            // it still reads
+            continue;
         }
-        // the other warps go on: they meet warp 0 before they write what it
-        // still reads
+        // the cluster's one unit: every block's results to the first
+        const int rank = blockIdx.x % splits;
+        cluster_wait();
+        if (warp == 0) {
+            const uint32_t to = first_block(&sh.part[rank]);
+            if (lane == 0) store_cluster(to, __float_as_uint(st.m), __float_as_uint(st.s));
+            if (lane == 0) store_cluster(to + 8, __float_as_uint(st.t), 0);
+            store_cluster(to + 16 + 8 * lane, (uint32_t)ranked, (uint32_t)(ranked >> 32));
+            __syncwarp();
+        }
+        cluster_arrive();
+        cluster_wait();
+        if (rank == 0) {
+            const Partial &mine = sh.part[lane < splits ? lane : 0];
+            if (warp == 0)
+                st = warp_join(Stats{lane < splits ? mine.m : -INFINITY, lane < splits ? mine.s : 0.f,
+                                     lane < splits ? mine.t : 0.f});
+            if (a.top > 0) {
+                block_top(sh, warp < splits ? sh.part[warp].keys[lane] : 0, splits, warp, lane);
+                ranked = sh.lists[0][lane];
+            }
+            if (warp == 0) finish_row(a, unit / splits, given, st, ranked, lane, err);
+        }
+        return;
+    }
+    // a wait was abandoned (blocks that share a row still meet)
+    if (splits > 1) {
+        cluster_wait();
+        cluster_arrive();
+        cluster_wait();
     }
 }
 
-// Joins the splits of a row, in split order.  One CTA per row.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) logprobs_join_kernel(const LogprobArgs a, const Partial *part, int splits,
-                                                                 unsigned int *err) {
-    __shared__ Shared sh;
-    pdl_launch_dependents();
-    pdl_wait();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = blockIdx.x;
-    const Partial *p = part + (int64_t)row * splits;
-    Given given{-1, 0.f};
-    if (tid == 0 && a.tokens) given.token = a.tokens[row];
-    Key best = 0;
-    if (a.top > 0) {
-        for (int i = warp; i < splits; i += kWarps)  // descending lists already
-            best = warp_top_of_two(best, p[i].keys[31 - lane], lane);
-        block_top(sh, best, min(splits, kWarps), warp, lane);
-        best = sh.lists[0][lane];
-    }
-    if (tid == 0) given.x = given_logit<T>(a, row, given.token);
-    Stats st{-INFINITY, 0.f, 0.f};
-    for (int i = tid; i < splits; i += kThreads) st = join(st, Stats{p[i].m, p[i].s, p[i].t});
-    st = block_join(sh, st, warp, lane);
-    if (warp == 0) finish_row(a, row, given, st, best, lane, err);
-}
-
-// Splits of a row: enough CTAs for two per SM, none with less than
-// kMinSpan logits.
-constexpr int kMinSpan = 2048;
+// Blocks that share a row: as many as leave no SM with more than two, none
+// with fewer than kMinSpan logits.
+constexpr int kMinSpan = 1024;
 
 int logprob_splits(int rows, int vocab, int sms) {
-    const int64_t want = (2 * (int64_t)sms + rows - 1) / rows;
-    const int64_t most = (vocab + kMinSpan - 1) / kMinSpan;
-    const int64_t s = want < most ? want : most;
-    return rows >= sms || s < 2 ? 1 : (int)s;
+    int n = 1;
+    while (n < kMaxCluster && (int64_t)rows * n * 2 <= 2 * sms && vocab / (n * 2) >= kMinSpan) n *= 2;
+    return n;
 }
 
 int current_sms() {
@@ -561,34 +581,34 @@ int current_sms() {
 }
 
 template <typename T>
-cudaError_t launch_typed(const LogprobArgs &a, void *workspace, cudaStream_t s, unsigned int *err) {
+cudaError_t launch_typed(const LogprobArgs &a, cudaStream_t s, unsigned int *err) {
     const int sms = current_sms();
     if (sms < 1) return cudaErrorInvalidDevice;
-    int splits = logprob_splits(a.rows, a.vocab, sms);
-    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(token_logprobs_kernel<T>), kRingBytes);
+    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(token_logprobs_kernel<T>), kRingBytes);
     if (e != cudaSuccess) return e;
-    // a span of whole 128-byte lines
+    const int splits = logprob_splits(a.rows, a.vocab, sms);
+    // spans of whole 128-byte lines; the last is shorter
     const int span = ((a.vocab + splits - 1) / splits + 63) / 64 * 64;
-    splits = (a.vocab + span - 1) / span;
-    Partial *part = static_cast<Partial *>(workspace);
     const int units = a.rows * splits, ctas = units < 2 * sms ? units : 2 * sms;
-    e = launch_pdl(token_logprobs_kernel<T>, dim3(ctas), dim3(kThreads + 32), kRingBytes, s, a, part, splits, span, units,
-                   err);
-    if (e != cudaSuccess || splits == 1) return e;
-    return launch_pdl(logprobs_join_kernel<T>, dim3(a.rows), dim3(kThreads), 0, s, a, (const Partial *)part, splits,
-                      err);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads + 32);
+    cfg.dynamicSmemBytes = kRingBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = splits, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = splits > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T>, a, splits, span, units, err);
 }
 
 }  // namespace
 
-size_t token_logprobs_workspace_bytes(int rows, int vocab, int /*top*/) {
-    const int splits = logprob_splits(rows, vocab, current_sms());
-    return splits > 1 ? ((size_t)rows * splits * sizeof(Partial) + 255) / 256 * 256 : 0;
-}
-
-cudaError_t launch_token_logprobs(const LogprobArgs &a, bool bf16, void *workspace, cudaStream_t s,
-                                  unsigned int *err) {
-    return bf16 ? launch_typed<__nv_bfloat16>(a, workspace, s, err) : launch_typed<float>(a, workspace, s, err);
+cudaError_t launch_token_logprobs(const LogprobArgs &a, bool bf16, cudaStream_t s, unsigned int *err) {
+    return bf16 ? launch_typed<__nv_bfloat16>(a, s, err) : launch_typed<float>(a, s, err);
 }
 
 }  // namespace q4_0

@@ -152,8 +152,6 @@ struct LogprobArgs {
     int rows, vocab, top;
 };
 
-size_t token_logprobs_workspace_bytes(int rows, int vocab, int top);
-cudaError_t launch_token_logprobs(const LogprobArgs &a, bool bf16, void *workspace, cudaStream_t s,
-                                  unsigned int *err);
+cudaError_t launch_token_logprobs(const LogprobArgs &a, bool bf16, cudaStream_t s, unsigned int *err);
 
 }  // namespace q4_0

@@ -438,6 +438,28 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// ------------------------------------------------------------- clusters
+
+// All threads of the cluster's blocks: arrive (what they wrote is visible to
+// those that wait), and wait for the others.
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The address, for store_cluster, of a variable of the cluster's first block
+// that lies at `p` in this one's shared memory.
+__device__ __forceinline__ uint32_t first_block(const void *p) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+    return r;
+}
+__device__ __forceinline__ void store_cluster(uint32_t to, uint32_t a, uint32_t b) {
+    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(a), "r"(b) : "memory");
+}
+
 // ------------------------------------------------------------- barriers
 
 // Named barrier `id` over `nthreads` threads (whole warps).  The .aligned

@@ -208,13 +208,7 @@ def attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
     return out
 
 
-def token_logprobs_workspace_bytes(rows: int, vocab: int, top: int) -> int:
-    """Scratch of token_logprobs on the current device."""
-    return _ws_bytes("q4_0_token_logprobs_workspace_bytes", rows, vocab, top)
-
-
-def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, top: int = 0, workspace: torch.Tensor = None,
-                   stream=None):
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, top: int = 0, stream=None):
     """(logprob, entropy, top_logprob, top_ids) of logits [rows, vocab] (fp32
     or bf16): the log probability of tokens[row] (int64; negative: none, 0),
     the row's entropy in nats, and its `top` largest log probabilities with
@@ -231,13 +225,11 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, top: int = 0, 
     top_ids = torch.empty((rows, max(top, 0)), dtype=_I64, device=dev)
     if rows == 0:
         return logprob, entropy, top_logprob, top_ids
-    ws = _scratch(token_logprobs_workspace_bytes(rows, vocab, top), dev, workspace)
     st = lib().q4_0_token_logprobs(logits.data_ptr(), _TYPES[logits.dtype], ls[0] if rows > 1 else vocab, rows, vocab,
                                    tokens.data_ptr(), top, logprob.data_ptr(), entropy.data_ptr(),
                                    top_logprob.data_ptr() if top else None, top_ids.data_ptr() if top else None,
-                                   ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
                                    _stream_of(stream, dev))
     if st:
         _check(st, "q4_0_token_logprobs")
-    _keep(stream, dev, logprob, entropy, top_logprob, top_ids, ws if workspace is None else None)
+    _keep(stream, dev, logprob, entropy, top_logprob, top_ids)
     return logprob, entropy, top_logprob, top_ids

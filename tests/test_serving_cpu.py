@@ -45,7 +45,7 @@ def attention(lib, c=None, **change):
 
 def logprobs(lib, **change):
     a = dict(logits=GOOD, type=0, stride=100, rows=4, vocab=100, tokens=GOOD, top=3, logprob=GOOD, entropy=GOOD,
-             top_logprob=GOOD, top_ids=GOOD, workspace=GOOD, bytes=1 << 40, stream=None)
+             top_logprob=GOOD, top_ids=GOOD, stream=None)
     a.update(change)
     return lib.q4_0_token_logprobs(*a.values())
 
@@ -108,8 +108,6 @@ def test_logprobs_arguments(lib):
     for change in (dict(top=33), dict(rows=1 << 31), dict(vocab=1 << 31, stride=1 << 31)):
         assert logprobs(lib, **change) == -2, change
     assert logprobs(lib, rows=0) == 0
-    assert lib.q4_0_token_logprobs_workspace_bytes(0, 100, 1) == 0
-    assert lib.q4_0_token_logprobs_workspace_bytes(1, 100, 101) == 0
 
 
 def test_status_text(lib):
