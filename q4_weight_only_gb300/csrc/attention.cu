@@ -69,7 +69,7 @@ struct Params {
     int out_bf16;
     float *part;      // [CTA][head piece, tail piece][piece_rows][D], unnormalised
     float2 *part_ml;  // the rows' (m * scale_log2, l)
-    int4 *record;     // per CTA: flags, then sequence, first token and key head of the tail piece
+    int4 *record;     // per CTA: flags, then first row of q, tokens and key head of the tail piece's item
     unsigned int *err;
 };
 
@@ -292,8 +292,9 @@ struct Layout {
     static constexpr int kTileBytes = kTile * D * 2;
     static constexpr int kBlock = kTile * 128;             // bytes of one column block
     static constexpr int kStages = D == 128 ? 5 : 10;      // K or V tiles in the ring
+    static constexpr int kQTiles = D == 128 ? 2 : 4;       // Q tiles held
     static constexpr int kQ = 0;
-    static constexpr int kRing = 2 * kTileBytes;
+    static constexpr int kRing = kQTiles * kTileBytes;
     static constexpr int kBars = kRing + kStages * kTileBytes;
     static constexpr int kSmem = kBars + kStatBytes + 1024;  // + alignment
 };
@@ -301,10 +302,12 @@ struct Layout {
 constexpr int kItems = 4;     // items handed out ahead
 constexpr int kReaders = 11;  // warps that read them
 
+constexpr int kMaxQTiles = 4;
+
 template <int kStages>
 struct Bars {
     uint64_t full[kStages], empty[kStages];
-    uint64_t q_full, q_empty;
+    uint64_t q_full[kMaxQTiles], q_empty[kMaxQTiles];
     uint64_t s_full[2], p_full[2], o_full[2];
     uint64_t b_done, merged;  // narrow items: B's O and (m, l) are ready; A has read them
     uint64_t item_full[kItems], item_empty[kItems];
@@ -343,8 +346,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bar.full[i], 1);
             mbar_init(&bar.empty[i], 1);
         }
-        mbar_init(&bar.q_full, 1);
-        mbar_init(&bar.q_empty, 1);
+        for (int i = 0; i < L::kQTiles; ++i) {
+            mbar_init(&bar.q_full[i], 1);
+            mbar_init(&bar.q_empty[i], 1);
+        }
         for (int g = 0; g < 2; ++g) {
             mbar_init(&bar.s_full[g], 1);
             mbar_init(&bar.p_full[g], 4);
@@ -410,7 +415,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int page, off;             // off < 0: a box that no query sees
                 int head, row0, tokens;    // tokens 0: not the item's first group
             };
-            int t = 0, q_items = 0;
+            int t = 0;
+            uint32_t q = 0;  // Q tiles copied
             bool open = false;  // `cur` holds an item with tiles from t on
             auto fetch = [&]() {
                 Group o{};
@@ -443,21 +449,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             Group now = fetch();
             while (ok && now.tiles) {
                 const Group then = fetch();
-                if (kv == 0 && now.tokens) {
-                    // Q: one copy per 64-element block and tile
-                    if (!__all_sync(0xffffffffu, mbar_wait(&bar.q_empty, (q_items & 1) ^ 1, abort_flag, p.err))) break;
-                    const int tiles = now.tokens > p.tokens ? 2 : 1;
-                    const uint32_t qbytes = (uint32_t)(p.tokens * p.group * 128);
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(&bar.q_full, tiles * L::kHalves * qbytes);
-                        for (int g = 0; g < tiles; ++g)
-                            for (int h = 0; h < L::kHalves; ++h)
-                                tma_load_4d(smem + L::kQ + g * L::kTileBytes + h * L::kBlock, &qmap, h * 64, 0,
-                                            now.head, now.row0 + g * p.tokens, &bar.q_full);
-                    }
-                    __syncwarp();
-                    ++q_items;
-                }
                 if (now.off < 0 || now.page < 0 || now.page >= p.pages) {
                     // a page coordinate past the end reads zeros
                     if (now.off >= 0) atomicExch(p.err, kErrBadIndex);
@@ -482,12 +473,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fill += 2;
                     slot += 2;
                     if (slot >= kStages) slot -= kStages, phase ^= 1;
+                    // an item's Q after its first K tile: Q waits for room
+                    for (; kv == 0 && now.tokens > 0; now.tokens -= p.tokens, now.row0 += p.tokens) {
+                        const int at = q % L::kQTiles;
+                        ok = __all_sync(0xffffffffu, mbar_wait(&bar.q_empty[at], (q / L::kQTiles & 1) ^ 1, abort_flag,
+                                                               p.err));
+                        if (!ok) break;
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(&bar.q_full[at], L::kHalves * p.tokens * p.group * 128);
+                            for (int h = 0; h < L::kHalves; ++h)
+                                tma_load_4d(smem + L::kQ + at * L::kTileBytes + h * L::kBlock, &qmap, h * 64, 0,
+                                            now.head, now.row0, &bar.q_full[at]);
+                        }
+                        __syncwarp();
+                        ++q;
+                    }
+                    if (!ok) break;
                 }
                 now = then;
             }
             if (lane == 0) {
                 bar.fills[kv] = fill;
-                if (kv == 0) bar.q_fills = q_items;
+                if (kv == 0) bar.q_fills = q;
             }
         } else if (warp == 3) {
             // ------------------------------------------------- items
@@ -508,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     o.head = head, o.b = b, o.row0 = s.row0 + it * 2 * p.tokens, o.tokens = r.tokens, o.pos0 = r.pos0;
                     o.lo = r.lo, o.hi = r.hi, o.sink_end = r.sink_end, o.sink_tiles = r.sink_tiles, o.wtile = r.wtile;
                     if (o.t0 > 0) flags |= kHeadPiece | (o.t1 < o.n ? kHeadGoesOn : 0);
-                    if (o.t0 == 0 && o.t1 > 0 && o.t1 < o.n) flags |= kTailPiece, tail = make_int4(0, b, it, head);
+                    if (o.t0 == 0 && o.t1 > 0 && o.t1 < o.n) flags |= kTailPiece, tail = make_int4(0, o.row0, o.tokens, head);
                 }
                 const int i = items % kItems;
                 if (!__all_sync(0xffffffffu,
@@ -542,6 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t idesc_qk = idesc_bf16_f32(kTile, kTile, false);
         constexpr uint32_t idesc_pv = idesc_bf16_f32(kTile, D, true);
         uint32_t fills = 0;  // ring position of the next K tile
+        uint32_t q = 0;      // Q tiles of earlier items
         uint32_t p_phase[2] = {0, 0};
         bool ok = true;
         auto wait = [&](uint64_t *b, uint32_t parity) {
@@ -555,15 +563,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t hi = (uint32_t)(q_desc >> 32);  // the same for all three
         const uint32_t q_lo = (uint32_t)q_desc, k_lo = (uint32_t)smem_desc_k128(ring), v_lo = (uint32_t)v_desc;
         constexpr uint32_t kTileStep = L::kTileBytes >> 4, kBlockStep = L::kBlock >> 4;
-        // S_g = Q K^T with tile `q` of Q's buffers (one elected thread)
-        auto scores = [&](int g, int q, uint32_t slot) {
-            const uint32_t a = q_lo + q * kTileStep, b = k_lo + slot * kTileStep, d = tmem + col_s(g);
+        // S_g = Q K^T with Q tile `qt`, for the `last` time (one elected
+        // thread)
+        auto scores = [&](int g, uint32_t qt, uint32_t slot, bool last) {
+            qt %= L::kQTiles;
+            const uint32_t a = q_lo + qt * kTileStep, b = k_lo + slot * kTileStep, d = tmem + col_s(g);
             each_step<D / 16>([&](auto step) {
                 constexpr uint32_t k = decltype(step)::value, off = (k >> 2) * kBlockStep + 2 * (k & 3);
                 mma_f16_ss_at<off, off>(d, a, b, hi, idesc_qk, k != 0);
             });
             mma_commit(&bar.s_full[g]);
+            if (last) mma_commit(&bar.q_empty[qt]);
         };
+        auto q_full = [&](uint32_t qt) { return wait(&bar.q_full[qt % L::kQTiles], qt / L::kQTiles & 1); };
         // O_g (+)= P_g V (one elected thread)
         auto values = [&](int g, uint32_t slot, bool first) {
             const uint32_t a = tmem + col_s(g), b = v_lo + slot * kTileStep, d = tmem + col_o(g);
@@ -572,10 +584,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_f16_ts_at<8 * k, k * (16 * 128 >> 4)>(d, a, b, hi, idesc_pv, !first || k != 0);
             });
             mma_commit(&bar.o_full[g]);
-        };
-        auto release = [&](uint64_t *b) {
-            if (elect_one()) mma_commit(b);
-            __syncwarp();
         };
         auto full = [&](uint32_t fill) { return wait(&bar.full[fill % kStages], fill / kStages & 1); };
         // Values of tokens that no query of the item sees may be anything
@@ -603,14 +611,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (; ok && next_item(); done_item()) {
             const bool wide = cur.tokens > p.tokens;
             const int n = cur.t1 - cur.t0;
-            if (!wait(&bar.q_full, items & 1)) break;
+            if (!q_full(q)) break;
             if (wide) {
                 uint32_t slot_k = fills % kStages, slot_v = (fills + 1) % kStages;
-                if (!full(fills)) break;
+                if (!full(fills) || !q_full(q + 1)) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    scores(0, 0, slot_k);
-                    scores(1, 1, slot_k);
+                    scores(0, q, slot_k, n == 1);
+                    scores(1, q + 1, slot_k, n == 1);
                     mma_commit(&bar.empty[slot_k]);
                 }
                 __syncwarp();
@@ -626,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     if (elect_one()) {
                         values(0, slot_v, t == 0);
-                        if (more) scores(0, 0, slot_k);
+                        if (more) scores(0, q, slot_k, t + 2 == n);
                     }
                     __syncwarp();
                     if (!wait(&bar.p_full[1], p_phase[1])) break;
@@ -636,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         values(1, slot_v, t == 0);
                         mma_commit(&bar.empty[slot_v]);
                         if (more) {
-                            scores(1, 1, slot_k);
+                            scores(1, q + 1, slot_k, t + 2 == n);
                             mma_commit(&bar.empty[slot_k]);
                         }
                     }
@@ -650,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!full(k)) break;
                     tc_fence_after();
                     if (elect_one()) {
-                        scores(t, 0, k % kStages);
+                        scores(t, q, k % kStages, t + 1 == n);
                         mma_commit(&bar.empty[k % kStages]);
                     }
                     __syncwarp();
@@ -672,15 +680,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!full(k)) break;
                     tc_fence_after();
                     if (elect_one()) {
-                        scores(g, 0, k % kStages);
+                        scores(g, q, k % kStages, t + 3 == n);
                         mma_commit(&bar.empty[k % kStages]);
                     }
                     __syncwarp();
                 }
             }
             if (!ok) break;
-            release(&bar.q_empty);  // every score of the item is done
             fills += 2 * n;
+            q += wide ? 2 : 1;
         }
         // every MMA has finished before tensor memory is released
         if (elect_one()) mma_commit(&bar.drain);
@@ -899,26 +907,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (f < bar.fills[f & 1]) last = f;
             if (last >= 0) mbar_drain(&bar.full[i], last / kStages & 1);
         }
-        if (bar.q_fills) mbar_drain(&bar.q_full, (bar.q_fills - 1) & 1);
+        for (uint32_t f = max(bar.q_fills, (uint32_t)L::kQTiles) - L::kQTiles; f < bar.q_fills; ++f)
+            mbar_drain(&bar.q_full[f % L::kQTiles], f / L::kQTiles & 1);
     }
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
 // Adds the pieces of the items that a share's boundary cut.  blockIdx.x: the
-// CTA whose tail piece starts the item; one warp per row of it.
+// CTA whose tail piece starts the item; a warp takes every (gridDim.y * 8)-th
+// of its rows.  Latency bounds it: three reads that wait for one another (the
+// records, the rows' (m, l), O), and blocks enough for one wave.
 template <int D>
 __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ Params p, int ctas) {
     pdl_launch_dependents();
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int4 rec = p.record[blockIdx.x];
-    if (!(rec.x & kTailPiece)) return;
-    const int row = blockIdx.y * 8 + warp;
-    const int g = row / kTile, in_tile = row - g * kTile;
-    const int token = g * p.tokens + in_tile / p.group, head = in_tile % p.group;
-    const Sequence s = sequence(p, rec.y);
-    const Range r = item_range(p, s, rec.z);
-    if (row >= p.piece_rows || in_tile >= p.tokens * p.group || token >= r.tokens) return;
     // pieces: this CTA's tail, then the heads of the next ones
     int n = 1;
     for (bool more = true; more; n += 32) {
@@ -934,38 +938,65 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
             more = false;
         }
     }
-    auto place = [&](int i) { return ((blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * p.piece_rows + row; };
-    float m = -INFINITY;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, p.part_ml[place(i)].x);
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float base = m == -INFINITY ? 0.f : m;
+    if (!(rec.x & kTailPiece)) return;
     constexpr int kOwn = D / 32;
-    float acc[kOwn] = {}, l = 0.f;
     using Own = typename std::conditional<kOwn == 4, float4, float2>::type;
+    const int rows = rec.z <= p.tokens ? min(p.piece_rows, rec.z * p.group) : p.piece_rows, step = gridDim.y * 8;
+    int row = blockIdx.y * 8 + warp;
+    auto place = [&](int i, int r) { return ((blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * p.piece_rows + r; };
+    auto piece = [&](int i, int r) {
+        return *reinterpret_cast<const Own *>(p.part + (int64_t)place(i, r) * D + lane * kOwn);
+    };
+    // an item that was cut has two pieces at least; the next row's are read
+    // ahead
+    Own v0{}, v1{};
+    float2 ml0{};
+    auto read = [&](int r) {
+        if (r >= rows) return;
+        v0 = piece(0, r), v1 = piece(1, r), ml0 = p.part_ml[place(min(lane, n - 1), r)];
+    };
+    read(row);
+    for (; row < rows; row += step) {
+        const int g = row / kTile, in_tile = row - g * kTile;
+        const int in_token = in_tile / p.group, head = in_tile - in_token * p.group, token = g * p.tokens + in_token;
+        const Own w0 = v0, w1 = v1;
+        const float2 ml = ml0;
+        read(row + step);
+        if (in_token >= p.tokens || token >= rec.z) continue;
+        float m = ml.x;
+        for (int i = lane + 32; i < n; i += 32) m = fmaxf(m, p.part_ml[place(i, row)].x);
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const float base = m == -INFINITY ? 0.f : m;
+        float acc[kOwn] = {}, l = 0.f;
+        auto add = [&](const Own &v, float pm, float pl) {
+            const float *o = reinterpret_cast<const float *>(&v);
+            const float f = ex2(pm - base);
+            l += pl * f;
+#pragma unroll
+            for (int e = 0; e < kOwn; ++e) acc[e] += o[e] * f;
+        };
+        add(w0, __shfl_sync(0xffffffffu, ml.x, 0), __shfl_sync(0xffffffffu, ml.y, 0));
+        add(w1, __shfl_sync(0xffffffffu, ml.x, 1), __shfl_sync(0xffffffffu, ml.y, 1));
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-        const float2 ml = p.part_ml[place(i)];
-        const Own v = *reinterpret_cast<const Own *>(p.part + (int64_t)place(i) * D + lane * kOwn);
-        const float *o = reinterpret_cast<const float *>(&v);
-        const float f = ex2(ml.x - base);
-        l += ml.y * f;
+        for (int i = 2; i < n; ++i) {
+            const float2 more_ml = p.part_ml[place(i, row)];
+            add(piece(i, row), more_ml.x, more_ml.y);
+        }
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        const int64_t at = ((int64_t)rec.y + token) * p.q_heads + rec.w * p.group + head;
 #pragma unroll
-        for (int e = 0; e < kOwn; ++e) acc[e] += o[e] * f;
+        for (int e = 0; e < kOwn; e += 2) {
+            const int64_t o = at * D + lane * kOwn + e;
+            if (p.out_bf16)
+                *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.out) + o) =
+                    pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+            else
+                *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + o) =
+                    make_float2(acc[e] * inv, acc[e + 1] * inv);
+        }
+        if (p.lse && lane == 0) p.lse[at] = (m + __log2f(l)) * kLn2;
     }
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    const int64_t at = ((int64_t)s.row0 + rec.z * 2 * p.tokens + token) * p.q_heads + rec.w * p.group + head;
-#pragma unroll
-    for (int e = 0; e < kOwn; e += 2) {
-        const int64_t o = at * D + lane * kOwn + e;
-        if (p.out_bf16)
-            *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.out) + o) =
-                pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-        else
-            *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + o) =
-                make_float2(acc[e] * inv, acc[e + 1] * inv);
-    }
-    if (p.lse && lane == 0) p.lse[at] = (m + __log2f(l)) * kLn2;
 }
 
 // -------------------------------------------------------------------- host
@@ -1062,7 +1093,8 @@ cudaError_t launch_d(const AttentionArgs &a, const KvCacheView &c, void *workspa
     if (e != cudaSuccess) return e;
     e = launch_pdl(attention_kernel<D>, dim3(ctas), dim3(kThreads), Layout<D>::kSmem, s, qmap, kmap, vmap, p);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attention_join_kernel<D>, dim3(ctas, (p.piece_rows + 7) / 8), dim3(256), 0, s, p, ctas);
+    const int blocks = (p.piece_rows + 7) / 8;  // of 8 warps; 8 blocks of each fit an SM
+    return launch_pdl(attention_join_kernel<D>, dim3(ctas, blocks < 8 ? blocks : 8), dim3(256), 0, s, p, ctas);
 }
 
 int current_sms() {
