@@ -402,8 +402,9 @@ typedef struct {
  *                always follows the position in the sequence.
  *   q_out      : bfloat16 [rows][q_heads][head_dim].
  * Computed in fp32, rounded once to bfloat16.  head_dim and rot are
- * multiples of 8 (rot may be 0, cos_sin then NULL).  Rows of one call must not share a cache
- * slot.  Alignment: qkv, its rows, cos_sin and q_out 16 bytes.
+ * multiples of 8 (rot may be 0, cos_sin then NULL).  Rows of one call must
+ * not share a cache slot.  Alignment: qkv, its rows, cos_sin and q_out 16
+ * bytes.
  * Returns Q4_0_OK, Q4_0_ERR_INVALID_ARG, Q4_0_ERR_UNSUPPORTED or
  * Q4_0_ERR_CUDA.
  */
@@ -430,8 +431,8 @@ int q4_0_kv_append(const void *qkv, int qkv_type, int64_t qkv_stride, int64_t ro
  * sequence's start) gives 0, and -infinity in lse.  Pages and slots that no
  * row of the call sees are not read or do not matter, whatever they hold.
  * A NaN or infinity in a key reaches only the rows that see it; in a value
- * it can also reach rows less than 256 / (q_heads / kv_heads) tokens earlier
- * in the same call.
+ * it can also reach rows of the same sequence and call less than
+ * 256 / (q_heads / kv_heads) tokens before or after one that sees it.
  * head_dim 64 or 128, q_heads / kv_heads <= 128, page_size a multiple of 8
  * (else UNSUPPORTED).
  * Accuracy: scores, softmax statistics and sums in fp32; the exponentials are

@@ -17,19 +17,42 @@
 // all query heads that share a key head read each key tile once, and a tile
 // of 128 rows spans few tokens, so little of a causal or windowed tile is
 // masked.  An item is two tiles (A and B) of one sequence and key head; its
-// cost is the number of 128-token key tiles it sees.  One CTA per SM takes
-// an equal share of all key tiles, in item order, whatever the batch looks
-// like; an item that a share's boundary cuts leaves partial results that
-// attention_join_kernel adds in share order, so results are deterministic.
+// cost is the number of 128-token key tiles it sees, each weighted by whether
+// one tile or two share it.  One CTA per SM takes an equal share of all cost,
+// in item order, whatever the batch looks like; an item that a share's
+// boundary cuts leaves partial results that attention_join_kernel adds in
+// share order, so results are deterministic.
 //
-// Warps: 0 copies Q and K tiles and 2 V tiles into a ring (TMA; page boxes
-// that no query sees are not read: an out-of-range page coordinate fills
-// zeros), 1 issues the MMAs, 3 hands out the items, 4-7 and 8-11 do the softmax of group A
-// and of group B, one thread per row, S and P in tensor memory.  While one
-// group is in softmax the tensor cores work on the other.  In an item of two
-// tiles a group has one tile each; in a narrow item (one tile: single tokens,
-// drafts, a chunk's end) the groups take the key tiles in turn, and group A
-// adds B's O to its own at the end.
+// Warps: 0 copies Q and K tiles and 2 V tiles into rings (TMA; boxes of a
+// page that no query sees are not read: an out-of-range page coordinate fills
+// zeros), 1 issues the MMAs, 3 hands out the items, 4-7 and 8-11 do the
+// softmax of group A and of group B, one thread per row, S and P in tensor
+// memory.  While one group is in softmax the tensor cores work on the other.
+// In an item of two tiles a group has one tile each; in a narrow item (one
+// tile: single tokens, drafts, a chunk's end) the groups take the key tiles
+// in turn, and group A adds B's O to its own at the end.
+//
+// Bounds and measurements (bfloat16, 40 query heads on 8 key heads of 128
+// unless stated; device time):
+// * A new token of each of many long sequences reads its cache once and is
+//   bound by that: 64 sequences under a window of 4096, 1.08 GB, 175 us (6.2
+//   TB/s, 0.91 of a copy's rate); 16 of 1 to 8 thousand tokens, 347 MB, 67 us
+//   (5.2 TB/s), of which 16 us are launch, the search for a share's start,
+//   the first reads and the join.
+// * A prompt is bound by the chain softmax -> P V and the next Q K of a group
+//   (1500 + 1800 cycles a pair of tiles at D = 128, of which the tensor cores
+//   are busy 2048): 8192 tokens after 8192 others take 1.34 ms, 1.54 PFLOP/s
+//   (1.42 ms in a long run, at the board's power limit).  TMEM is full (two
+//   S, two O), so a group's next scores cannot start earlier.  A shorter
+//   softmax would show; the exponential units are not what bounds it (a
+//   polynomial on the multiply-add units for 1/8 to 1/2 of the elements made
+//   it 3 to 25 % slower).
+// * Prompts of 2500 to 3500 tokens under a window of 1000 (24 heads on 4, D =
+//   64) take 143 us: 2750 cycles a pair of tiles, and 10000 more an item of
+//   ten, for masks at both ends of the window, both groups' start at once,
+//   the last product and the rows' stores.
+// * One token after 2047 takes 16.7 us against a floor of 1.2: 4.3 launch, 6
+//   join, the rest reads that wait for one another.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -515,7 +538,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     o.head = head, o.b = b, o.row0 = s.row0 + it * 2 * p.tokens, o.tokens = r.tokens, o.pos0 = r.pos0;
                     o.lo = r.lo, o.hi = r.hi, o.sink_end = r.sink_end, o.sink_tiles = r.sink_tiles, o.wtile = r.wtile;
                     if (o.t0 > 0) flags |= kHeadPiece | (o.t1 < o.n ? kHeadGoesOn : 0);
-                    if (o.t0 == 0 && o.t1 > 0 && o.t1 < o.n) flags |= kTailPiece, tail = make_int4(0, o.row0, o.tokens, head);
+                    if (o.t0 == 0 && o.t1 > 0 && o.t1 < o.n)
+                        flags |= kTailPiece, tail = make_int4(0, o.row0, o.tokens, head);
                 }
                 const int i = items % kItems;
                 if (!__all_sync(0xffffffffu,
@@ -789,8 +813,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float a, b;
-                            unpack2(fma2(pack2(__uint_as_float(s[q][2 * e]), __uint_as_float(s[q][2 * e + 1])), c2, mc2),
-                                    a, b);
+                            const uint64_t s2 = pack2(__uint_as_float(s[q][2 * e]), __uint_as_float(s[q][2 * e + 1]));
+                            unpack2(fma2(s2, c2, mc2), a, b);
                             a = ex2(a), b = ex2(b);
                             sum[e & 3] = add2(sum[e & 3], pack2(a, b));
                             w[e] = pack_bf16(a, b);
