@@ -155,6 +155,15 @@ def test_long_context_and_many_sequences():
     check(b, *run(b, 4))
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("window", [0, 90])
+def test_items_of_one_and_two_tiles_in_turn(dim, window):
+    """A CTA's share of some thousand items mixes both kinds at any offset."""
+    new = [(1, 60, 3, 129, 40, 1, 1, 26)[i % 8] + (i % 3 == 0) * 25 for i in range(400)]
+    b = ref.Batch(new, [n + 37 * (i % 11) for i, n in enumerate(new)], 32, 2, dim, seed=20).write_tokens()
+    check(b, *run(b, 10, window=window, sinks=2 if window else 0), window, 2 if window else 0)
+
+
 def test_strided_queries():
     """Queries inside fused rows: row and head strides of their own."""
     b = ref.Batch([1, 30], [100, 200], 16, 2, 64, seed=16).write_tokens()

@@ -149,6 +149,32 @@ def test_tokens_missing_and_out_of_range():
     assert logprob[1].isnan() and torch.isfinite(logprob[[0, 2]]).all()
 
 
+@pytest.mark.parametrize("vocab", [2049, 4100, 8195, 70001])
+@pytest.mark.parametrize("rows", [1, 19, 38, 39, 76, 77, 152, 153])
+def test_rows_shared_by_blocks(rows, vocab):
+    """Row counts and vocabularies at which the blocks of a row change."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = torch.randn(rows, vocab, generator=g, device="cuda")
+    x[:, vocab // 2:] -= 30.0  # some blocks hold none of the top
+    check(x, torch.randint(0, vocab, (rows,), generator=g, device="cuda"), 20)
+
+
+def test_graph_replay_reads_new_logits():
+    q4 = lib()
+    x, t = torch.randn(3, 40000, device="cuda"), torch.tensor([5, -1, 39999], device="cuda")
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        q4.token_logprobs(x, t, top=7)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = q4.token_logprobs(x, t, top=7)
+    x.copy_(torch.randn(3, 40000, device="cuda"))
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(out, q4.token_logprobs(x, t, top=7)))
+    check(x, t, 7)
+
+
 def test_same_bits_twice_and_another_stream():
     q4 = lib()
     x = torch.randn(5, 70001, device="cuda").bfloat16()
