@@ -85,7 +85,11 @@ __global__ void __launch_bounds__(kThreads, 6) kv_append_kernel(const KvAppendAr
         }
     }
     const bool landed = mbar_wait(&full, 0, &abort_flag, err);
-    if (!ok || !landed) return;  // the copy has landed, or a wait of two seconds was reported
+    if (!ok || !landed) {
+        // a wait that was given up has been reported; the copy lands first
+        if (!landed) mbar_drain(&full, 0);
+        return;
+    }
     const float *cs = a.cos_sin + (int64_t)turn_row * a.rot;
     __nv_bfloat16 *q_row = a.q_out + (int64_t)row * a.q_heads * c.head_dim;
     __nv_bfloat16 *k_row = c.k + page * c.k_stride[0] + off * c.k_stride[2];
