@@ -51,7 +51,7 @@
 //   64) take 143 us: 2750 cycles a pair of tiles, and 10000 more an item of
 //   ten, for masks at both ends of the window, both groups' start at once,
 //   the last product and the rows' stores.
-// * One token after 2047 takes 16.7 us against a floor of 1.2: 4.3 launch, 6
+// * One token after 2047 takes 16.7 us against a floor of 1.2: 4.3 launch, 4
 //   join, the rest reads that wait for one another.
 #include <cuda.h>
 #include <cuda_bf16.h>
