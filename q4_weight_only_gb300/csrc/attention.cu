@@ -748,7 +748,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pos_a = cur.pos0 + half * p.tokens;
             const int pos_z = cur.pos0 + min((half + 1) * p.tokens, cur.tokens) - 1;
             const int step = wide ? 1 : 2;
-            float m = -INFINITY, l = 0.f;
+            // A row whose maximum grew moves the references of its warp's
+            // rows (each its own, one by one, took prompts 1 to 4 % longer).
+            // Lanes that are no row of the item must not: they hold other
+            // sequences' rows, or what an earlier kernel left in shared
+            // memory.  Nothing is above their reference.
+            float m = valid ? -INFINITY : INFINITY, l = 0.f;
             bool started = false;
             for (int t = cur.t0 + (wide ? 0 : g); t < cur.t1; t += step) {
                 if (!wait(&bar.s_full[g], s_phase)) break;
