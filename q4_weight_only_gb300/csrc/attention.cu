@@ -5,13 +5,14 @@
 //
 // Mathematics, for a query row at position t and the keys j it sees
 // (j <= t, and j > t - window or j < sinks): with a running reference m,
-//   p_j = 2^(c (s_j - m)),  l = sum p_j,  O = sum p_j v_j,  out = O / l,
-// s_j = q . k_j, c = scale * log2 e, all of s, l, O and m in fp32.  m follows
+//   p_j = 2^(c s_j - c m),  l = sum p_j,  O = sum p_j v_j,  out = O / l,
+// s_j = q . k_j, c = scale * log2 e, all of s, l, O and c m in fp32.  c m is
+// kept rounded, and its rounding is the same in all of a row.  It follows
 // the running maximum only when a row's maximum grew by more than 2^8 in p:
-// the result does not depend on m, p <= 2^8 keeps every sum far inside
-// fp32, and most tiles then skip the correction of O.  p is rounded to
-// bfloat16 for the second product: the MMA takes one operand type, and V is
-// bfloat16; l sums p before the rounding.
+// the result does not depend on m, p <= 2^8 (2^72 where c m is near 2^30)
+// keeps every sum inside fp32, and most tiles then skip the correction of O.
+// p is rounded to bfloat16 for the second product: the MMA takes one operand
+// type, and V is bfloat16; l sums p before the rounding.
 //
 // Layout of work.  The rows of a tile are (token, head of the group) pairs:
 // all query heads that share a key head read each key tile once, and a tile
@@ -56,6 +57,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <cmath>
 #include <mutex>
 #include <type_traits>
 
@@ -75,6 +77,11 @@ constexpr int kStatBytes = 2048;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;    // log2 of the growth of a row's maximum that moves its reference
+// Every p of a row has 2^(the rounding of c m) as a factor.  Where c m is
+// beyond this, that would leave fp32, and fp32 scores that differ are 64
+// apart at least: the next power of two in the place of c gives the same
+// p, 1 or nothing, without a rounding.
+constexpr float kHuge = 1 << 30;
 
 struct Params {
     const int32_t *page_table, *q_start, *kv_len;
@@ -86,7 +93,7 @@ struct Params {
     int cost[2];  // of a key tile of a narrow item and of one of two tiles
     int max_q_len;
     int piece_rows;  // rows a piece can have: one tile's when max_q_len fits it
-    float scale_log2;
+    float scale_log2, scale_pow2, scale_back;  // scale * log2 e, the next power of two, and their ratio
     void *out;
     float *lse;
     int out_bf16;
@@ -753,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Lanes that are no row of the item must not: they hold other
             // sequences' rows, or what an earlier kernel left in shared
             // memory.  Nothing is above their reference.
-            float m = valid ? -INFINITY : INFINITY, l = 0.f;
+            float mc = valid ? -INFINITY : INFINITY, c_row = c, l = 0.f;
             bool started = false;
             for (int t = cur.t0 + (wide ? 0 : g); t < cur.t1; t += step) {
                 if (!wait(&bar.s_full[g], s_phase)) break;
@@ -788,12 +795,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int q = 0; q < 4; ++q)
                             top4[q] = max3(top4[q], __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
                     const float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
-                    const bool grew = top > m && (m == -INFINITY || (top - m) * c > kGrow);
-                    if (__any_sync(0xffffffffu, grew)) {
-                        const float m_new = fmaxf(m, top);
-                        const float f = m == -INFINITY ? 0.f : ex2((m - m_new) * c);
+                    // (nothing is above an infinite reference)
+                    if (__any_sync(0xffffffffu, fmaf(top, c_row, -mc) > kGrow)) {
+                        const float c_top = fabsf(top * c) > kHuge ? p.scale_pow2 : c;
+                        const float mc_new = __fmul_rn(top, c_top);
+                        const bool above = mc_new > mc;
+                        const float f = mc == -INFINITY ? 0.f : above ? ex2(mc - mc_new) : 1.f;
                         l *= f;
-                        m = m_new;
+                        if (above) mc = mc_new, c_row = c_top;
                         if (started) {
                             // O of the earlier tiles is complete: scale it
                             if (!wait(&bar.o_full[g], o_phase ^ 1)) break;
@@ -809,8 +818,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-                    const float mc = m == -INFINITY ? 0.f : m * c;
-                    const uint64_t c2 = pack2(c, c), mc2 = pack2(-mc, -mc);
+                    const float base = mc == -INFINITY ? 0.f : mc;
+                    const uint64_t c2 = pack2(c_row, c_row), mc2 = pack2(-base, -base);
                     uint64_t sum[4] = {pack2(l, 0.f), 0, 0, 0};
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -845,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // o_phase counts the group's second products: wait for the last
             if (started && !wait(&bar.o_full[g], o_phase ^ 1)) break;
             tc_fence_after();
-            const float mc = m == -INFINITY ? -INFINITY : m * c;
+            mc *= c_row == c ? 1.f : p.scale_back;
             if (!wide && g == 1) {
                 if (unmerged && !wait(&bar.merged, merge_phase ^ 1)) break;
                 bar.ml[row] = make_float2(mc, l);
@@ -1095,6 +1104,10 @@ cudaError_t launch_d(const AttentionArgs &a, const KvCacheView &c, void *workspa
     // little of a tile is left to clear by hand
     p.box = gcd(c.page_size, 64);
     p.scale_log2 = a.scale * kLog2e;
+    int exponent;
+    const float mantissa = frexpf(p.scale_log2, &exponent);
+    p.scale_pow2 = mantissa == 0.5f ? p.scale_log2 : ldexpf(1.f, exponent);
+    p.scale_back = p.scale_log2 / p.scale_pow2;
     p.out = a.out, p.lse = a.lse, p.out_bf16 = a.out_bf16;
     p.max_q_len = a.max_q_len;
     // Where both kinds of item can meet, a key tile of two tiles takes about
