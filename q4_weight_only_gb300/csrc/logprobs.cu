@@ -6,12 +6,13 @@
 //   s = sum 2^y,   t = sum y 2^y,
 // both rescaled when m grows (t also shifts by (m_old - m_new) log2 e s),
 //   logprob = (x[token] - m) - ln s,  entropy = (log2 s - t / s) ln 2.
-// y is one fma, x log2 e - (m log2 e); the rounding of its product is the
-// same for all of a row and is taken out of ln s at the end.  Logits near the
-// ends of fp32's range (the type's lowest value, as a mask) would overflow
-// there, and are subtracted first.  All statistics are fp32.  Ranking uses
-// 64-bit keys (order-preserving bits of x, then the complement of the index),
-// so equal logits rank by lowest index whatever order threads meet them in.
+// m is subtracted before the product with log2 e: the largest logit has y = 0
+// exactly, s >= 1, no log probability is above 0, and an error does not grow
+// with an offset of the row.  (x log2 e - (m log2 e) as one fma has the
+// rounding of m's product in every y, whole exponents from 1e9 on; it took 2
+// of the 201 us below less.)  All statistics are fp32.  Ranking uses 64-bit
+// keys (order-preserving bits of x, then the complement of the index), so
+// equal logits rank by lowest index whatever order threads meet them in.
 //
 // Top alternatives in the same read: every warp keeps a threshold key, below
 // the row's k-th largest, and appends only larger keys to a buffer of its
@@ -54,7 +55,7 @@ constexpr int kBuffer = 2 * kMaxTop;               // candidate keys a warp hold
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFloor = -1000.f;                  // 2^kFloor is 0, and kFloor * 0 is too
-constexpr float kFar = 1e37f;                      // beyond it x log2 e may overflow
+constexpr float kFar = 1e37f;                      // beyond it (x - m) log2 e may overflow
 constexpr int kRingBytes = 96 * 1024;
 constexpr int kMaxCluster = 8;                     // blocks that share a row
 
@@ -182,23 +183,10 @@ struct Stats {
     float m, s, t;
 };
 
-// The exponent that takes sums with reference m to reference `to`, from the
-// products that y uses; where they overflow, different references are further
-// apart than any sum reaches.
+// The exponent that takes sums with reference m to reference `to`; cut off
+// further apart than any sum reaches.
 __device__ __forceinline__ float shift(float m, float to) {
-    return m == to ? 0.f : fmaxf(__fmul_rn(m, kLog2e) - __fmul_rn(to, kLog2e), -1e30f);
-}
-
-__device__ __forceinline__ Stats join(const Stats &a, const Stats &b) {
-    Stats r;
-    r.m = fmaxf(a.m, b.m);
-    const float base = r.m == -INFINITY ? 0.f : r.m;
-    // a side without any finite logit has s = t = 0, and its shift is cut off
-    const float da = shift(a.m, base), db = shift(b.m, base);
-    const float fa = ex2(da), fb = ex2(db);
-    r.s = a.s * fa + b.s * fb;
-    r.t = (a.t + da * a.s) * fa + (b.t + db * b.s) * fb;
-    return r;
+    return m == to ? 0.f : fmaxf((m - to) * kLog2e, -1e30f);
 }
 
 // The warp's statistics from its lanes'.
@@ -258,10 +246,7 @@ __device__ __forceinline__ float given_logit(const LogprobArgs &a, int row, int6
 __device__ __forceinline__ void finish_row(const LogprobArgs &a, int row, const Given &g, Stats v, Key best, int lane,
                                            unsigned int *err) {
     const bool empty = v.m == -INFINITY && v.s == 0.f;  // every logit is -inf
-    const float log_s = log2f(v.s);
-    // y was taken from the rounded product m log2 e: the rounding, exactly
-    const float rounding = fabsf(v.m) < kFar ? fmaf(v.m, kLog2e, -__fmul_rn(v.m, kLog2e)) : 0.f;
-    const float ln_s = (log_s - rounding) * kLn2;
+    const float log_s = log2f(v.s), ln_s = log_s * kLn2;
     if (lane == 0) {
         if (a.tokens) {
             float lp = empty ? -INFINITY : (g.x - v.m) - ln_s;
@@ -432,21 +417,16 @@ __global__ void __launch_bounds__(kThreads + 32, 2) token_logprobs_kernel(const 
                 st.m = top;
             }
             const float base = st.m == -INFINITY ? 0.f : st.m;
-            const float product = __fmul_rn(base, kLog2e);
-            const uint64_t c2 = pack2(kLog2e, kLog2e), m2 = pack2(-product, -product);
+            const uint64_t c2 = pack2(kLog2e, kLog2e), m2 = pack2(-base, -base);
             uint64_t s2 = pack2(st.s, 0.f), t2 = pack2(st.t, 0.f);
             auto add = [&](auto far) {
 #pragma unroll
                 for (int e = 0; e < kPerThread; e += 2) {
                     float y0, y1;
-                    if (decltype(far)::value) {
-                        // no product that overflows; -inf: 2^y is 0, and
-                        // y 2^y must be
-                        y0 = max_nan((x[e] - base) * kLog2e, kFloor);
-                        y1 = max_nan((x[e + 1] - base) * kLog2e, kFloor);
-                    } else {
-                        unpack2(fma2(pack2(x[e], x[e + 1]), c2, m2), y0, y1);
-                    }
+                    unpack2(mul2(add2(pack2(x[e], x[e + 1]), m2), c2), y0, y1);
+                    // -inf, or a product that overflowed: 2^y is 0, and y 2^y
+                    // must be
+                    if (decltype(far)::value) y0 = max_nan(y0, kFloor), y1 = max_nan(y1, kFloor);
                     const uint64_t p = pack2(ex2(y0), ex2(y1));
                     s2 = add2(s2, p);
                     t2 = fma2(pack2(y0, y1), p, t2);
