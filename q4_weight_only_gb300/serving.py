@@ -8,6 +8,11 @@ head_dim] in any memory order whose head_dim elements are adjacent (a
 [sequences, max_pages], q_start [sequences + 1] (the rows of each sequence)
 and kv_len [sequences] (its tokens in the cache, the new ones included).
 They are read on the device only, so a captured CUDA graph follows them.
+
+A call with `stream` reads its inputs and writes its results there: that
+stream waits for whoever writes the inputs, and whoever reads the results
+waits for it, both in the caller's hands.  Results and workspaces that are not
+given are that stream's own memory.
 """
 import struct
 
@@ -71,25 +76,35 @@ def _stream_of(stream, device):
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _keep(stream, device, *tensors):
-    """Memory made here for work on another stream than the current one is
-    not handed out again before that work is done."""
+def _other(stream, device):
+    """`stream` as a torch stream where it is not the current one, else None."""
     if stream is None or _stream_of(stream, device) == _stream_of(None, device):
-        return
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-    for t in tensors:
-        if t is not None:
-            t.record_stream(s)
+        return None
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
 
 
-def _scratch(nbytes, device, workspace):
+def _empty(shape, dtype, device, other, result=True):
+    """Memory for a call on the stream `other` (None: the current one).  It
+    comes from that stream's pool: a block of the current stream's may be in
+    use by work that is still queued there.  A result goes back to its pool
+    only after what the current stream does with it."""
+    if other is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(other):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if result:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _scratch(nbytes, device, workspace, other):
     """The caller's workspace or one made here, or None where none is needed."""
     if workspace is not None:
         _plain(workspace, "workspace", torch.uint8, 1, device)
         if workspace.numel() < nbytes:
             raise ValueError("workspace too small")
         return workspace
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    return _empty(nbytes, torch.uint8, device, other, result=False) if nbytes else None
 
 
 def _cache(k_cache, v_cache, page_table, q_start, kv_len, device):
@@ -138,9 +153,8 @@ def kv_append(qkv: torch.Tensor, cos_sin: torch.Tensor, k_cache: torch.Tensor, v
         _plain(positions, "positions", _I32, 1, dev)
         if positions.shape[0] != rows:
             raise ValueError("positions must have one element per row")
-    made = None
     if out is None:
-        out = made = torch.empty((rows, q_heads, dim), dtype=_BF16, device=dev)
+        out = _empty((rows, q_heads, dim), _BF16, dev, _other(stream, dev))
     else:
         _plain(out, "out", _BF16, 3, dev)
         if tuple(out.shape) != (rows, q_heads, dim):
@@ -154,7 +168,6 @@ def kv_append(qkv: torch.Tensor, cos_sin: torch.Tensor, k_cache: torch.Tensor, v
                               _stream_of(stream, dev))
     if st:
         _check(st, "q4_0_kv_append")
-    _keep(stream, dev, made)
     return out
 
 
@@ -183,9 +196,9 @@ def attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
     rows, q_heads, dim = shape = q.shape
     if dim != cache_dim:
         raise ValueError("q and the cache must have the same head_dim")
-    made = None
+    other = _other(stream, dev)
     if out is None:
-        out = made = torch.empty(shape, dtype=out_dtype, device=dev)
+        out = _empty(shape, out_dtype, dev, other)
     else:
         _plain(out, "out", out_dtype, 3, dev)
         if out.shape != shape:
@@ -196,7 +209,7 @@ def attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
             raise ValueError("lse must be [rows, q_heads]")
     if rows == 0:
         return out
-    ws = _scratch(attention_workspace_bytes(rows, q_heads, kv_heads, dim, max_q_len), dev, workspace)
+    ws = _scratch(attention_workspace_bytes(rows, q_heads, kv_heads, dim, max_q_len), dev, workspace, other)
     st = lib().q4_0_attention(q.data_ptr(), qs[0], qs[1], out.data_ptr(), _TYPES[out_dtype],
                               lse.data_ptr() if lse is not None else None, rows, q_heads, max_q_len,
                               dim ** -0.5 if scale is None else scale, window, sinks, cache,
@@ -204,7 +217,6 @@ def attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
                               _stream_of(stream, dev))
     if st:
         _check(st, "q4_0_attention")
-    _keep(stream, dev, made, ws if workspace is None else None)
     return out
 
 
@@ -219,10 +231,11 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, top: int = 0, 
     rows, vocab = logits.shape
     if tokens.shape[0] != rows:
         raise ValueError("tokens must have one element per row of logits")
-    logprob = torch.empty(rows, dtype=_F32, device=dev)
-    entropy = torch.empty(rows, dtype=_F32, device=dev)
-    top_logprob = torch.empty((rows, max(top, 0)), dtype=_F32, device=dev)
-    top_ids = torch.empty((rows, max(top, 0)), dtype=_I64, device=dev)
+    other = _other(stream, dev)
+    logprob = _empty(rows, _F32, dev, other)
+    entropy = _empty(rows, _F32, dev, other)
+    top_logprob = _empty((rows, max(top, 0)), _F32, dev, other)
+    top_ids = _empty((rows, max(top, 0)), _I64, dev, other)
     if rows == 0:
         return logprob, entropy, top_logprob, top_ids
     st = lib().q4_0_token_logprobs(logits.data_ptr(), _TYPES[logits.dtype], ls[0] if rows > 1 else vocab, rows, vocab,
@@ -231,5 +244,4 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, top: int = 0, 
                                    _stream_of(stream, dev))
     if st:
         _check(st, "q4_0_token_logprobs")
-    _keep(stream, dev, logprob, entropy, top_logprob, top_ids)
     return logprob, entropy, top_logprob, top_ids
