@@ -479,7 +479,8 @@ int q4_0_token_logprobs(const void *logits, int logits_type, int64_t row_stride,
  * Q4_0_ERR_DEVICE_TIMEOUT (a kernel gave up on a bounded wait and left its
  * output incomplete) or Q4_0_ERR_DEVICE_INDEX (a page, length, position or
  * token that q4_0_kv_append, q4_0_attention or q4_0_token_logprobs read from
- * device memory is out of range).  Returns Q4_0_OK or Q4_0_ERR_CUDA.
+ * device memory is out of range); Q4_0_ERR_DEVICE_TIMEOUT where both happened.
+ * Returns Q4_0_OK or Q4_0_ERR_CUDA.
  */
 int q4_0_device_error(int *code);
 

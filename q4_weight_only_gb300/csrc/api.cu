@@ -44,7 +44,7 @@ __global__ void wait_timeout_selftest_kernel(unsigned long long limit_ns, unsign
     const unsigned long long t0 = global_ns();
     while (!mbar_try_wait(&bar, 0)) {
         if (global_ns() - t0 > limit_ns) {
-            atomicExch(err, kErrWaitTimeout);
+            report(err, kErrWaitTimeout);
             return;
         }
     }
@@ -591,7 +591,7 @@ int q4_0_device_error(int *code) {
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(g_device_error_word, &zero, sizeof zero) != cudaSuccess)
         return Q4_0_ERR_CUDA;
-    *code = v == kErrBadIndex ? Q4_0_ERR_DEVICE_INDEX : v ? Q4_0_ERR_DEVICE_TIMEOUT : Q4_0_OK;
+    *code = v & kErrWaitTimeout ? Q4_0_ERR_DEVICE_TIMEOUT : v ? Q4_0_ERR_DEVICE_INDEX : Q4_0_OK;
     return Q4_0_OK;
 }
 

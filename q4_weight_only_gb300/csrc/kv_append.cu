@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kThreads, 6) kv_append_kernel(const KvAppendAr
         page = index >= 0 && index < c.table_width ? c.page_table[(int64_t)ended * c.table_stride + index] : -1;
         off = pos - index * c.page_size;
         if (turn_row < 0 || turn_row >= a.positions || page < 0 || page >= c.pages) {
-            if (threadIdx.x == 0) atomicExch(err, kErrBadIndex);
+            if (threadIdx.x == 0) report(err, kErrBadIndex);
             ok = false;
         }
     }

@@ -10,10 +10,13 @@
 
 namespace q4_0 {
 
-// Reason a kernel stores in the device error word (passed to every kernel
-// as a pointer; read back by q4_0_device_error()) when it gives up.
+// Bits that kernels set in the device error word (passed to every kernel as a
+// pointer; read back by q4_0_device_error()): a kernel gave up on a wait ...
 constexpr unsigned int kErrWaitTimeout = 1;
-constexpr unsigned int kErrBadIndex = 2;  // a page, position or token read from device memory is out of range
+// ... or met a page, position or token out of range in device memory.
+constexpr unsigned int kErrBadIndex = 2;
+
+__device__ __forceinline__ void report(unsigned int *err, unsigned int bit) { atomicOr(err, bit); }
 
 // A wait that has not finished after this many nanoseconds is abandoned.
 // Every legitimate wait in these kernels lasts microseconds.
@@ -89,7 +92,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
         if ((it & 7u) == 0) {
             if (*abort) return false;
             if (global_ns() - t0 > kWaitLimitNs) {
-                atomicExch(err, kErrWaitTimeout);
+                report(err, kErrWaitTimeout);
                 *abort = 1;
                 return false;
             }
