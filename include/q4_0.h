@@ -402,8 +402,9 @@ typedef struct {
  *                always follows the position in the sequence.
  *   q_out      : bfloat16 [rows][q_heads][head_dim].
  * Computed in fp32, rounded once to bfloat16.  head_dim and rot are
- * multiples of 8 (rot may be 0, cos_sin then NULL).  Rows of one call must
- * not share a cache slot.  Alignment: qkv, its rows, cos_sin and q_out 16
+ * multiples of 8.  With rot 0 nothing is rotated: cos_sin (then NULL or not),
+ * positions and row_positions are not looked at.  Rows of one call must not
+ * share a cache slot.  Alignment: qkv, its rows, cos_sin and q_out 16
  * bytes.
  * Returns Q4_0_OK, Q4_0_ERR_INVALID_ARG, Q4_0_ERR_UNSUPPORTED or
  * Q4_0_ERR_CUDA.

@@ -475,8 +475,9 @@ int q4_0_kv_append(const void *qkv, int qkv_type, int64_t qkv_stride, int64_t ro
     KvCacheView c;
     const int st = cache_view(cache, &c);
     if (st != Q4_0_OK) return st;
-    if (!qkv || (rot && !cos_sin) || !q_out || !y_type_ok(qkv_type) || rows < 0 || q_heads < 1 || positions < 1)
+    if (!qkv || (rot && !cos_sin) || !q_out || !y_type_ok(qkv_type) || rows < 0 || q_heads < 1 || positions < 0)
         return Q4_0_ERR_INVALID_ARG;
+    if (rot && positions < 1) return Q4_0_ERR_INVALID_ARG;
     if (rot < 0 || rot > c.head_dim || rot % 8 || c.head_dim % 8) return Q4_0_ERR_INVALID_ARG;
     if (rows > (1ll << 30) || q_heads > 4096 || positions > (1ll << 30) || qkv_stride > (1ll << 32))
         return Q4_0_ERR_UNSUPPORTED;

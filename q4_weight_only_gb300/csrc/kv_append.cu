@@ -75,11 +75,12 @@ __global__ void __launch_bounds__(kThreads, 6) kv_append_kernel(const KvAppendAr
     int pos = 0, turn_row = 0, page = 0, off = 0;
     if (ok) {
         pos = c.kv_len[ended] - c.q_start[ended + 1] + row;
-        turn_row = a.row_positions ? a.row_positions[row] : pos;
+        if (a.rot) turn_row = a.row_positions ? a.row_positions[row] : pos;
         const int index = pos >= 0 ? pos / c.page_size : -1;
         page = index >= 0 && index < c.table_width ? c.page_table[(int64_t)ended * c.table_stride + index] : -1;
         off = pos - index * c.page_size;
-        if (turn_row < 0 || turn_row >= a.positions || page < 0 || page >= c.pages) {
+        const bool turns = !a.rot || (turn_row >= 0 && turn_row < a.positions);
+        if (!turns || page < 0 || page >= c.pages) {
             if (threadIdx.x == 0) report(err, kErrBadIndex);
             ok = false;
         }
