@@ -370,6 +370,7 @@ int q4_0_gemm_noalloc(const uint16_t *x, const uint8_t *wq, float *y,
  *                the new ones included, at most table_width * page_size.
  *                Row q_start[b] + i is at position
  *                kv_len[b] - (q_start[b + 1] - q_start[b]) + i.
+ *   sequences  : may be 0 (the three arrays may then be NULL).
  * Sizes (else UNSUPPORTED): pages <= 2^30, page_size <= 2^20, kv_heads and
  * head_dim <= 1024, sequences <= 2^20, table_width * page_size <= 2^30.
  * A page, length or position out of range in device memory is skipped (never

@@ -438,7 +438,9 @@ bool y_type_ok(int t) { return t == Q4_0_Y_F32 || t == Q4_0_Y_BF16; }
 
 // A q4_0_kv_cache as the kernels take it; a status code.
 int cache_view(const q4_0_kv_cache *c, KvCacheView *v) {
-    if (!c || !c->k || !c->v || !c->page_table || !c->q_start || !c->kv_len) return Q4_0_ERR_INVALID_ARG;
+    if (!c || !c->k || !c->v) return Q4_0_ERR_INVALID_ARG;
+    // arrays without an element may have no address
+    if (c->sequences && (!c->page_table || !c->q_start || !c->kv_len)) return Q4_0_ERR_INVALID_ARG;
     if (c->pages < 1 || c->page_size < 1 || c->kv_heads < 1 || c->head_dim < 1 || c->sequences < 0 ||
         c->table_width < 1 || c->table_stride < c->table_width)
         return Q4_0_ERR_INVALID_ARG;
