@@ -7,6 +7,7 @@ All arithmetic happens in the library's CUDA kernels; there is no fallback:
 if the library is not built, the first call raises.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -140,18 +141,17 @@ def _q4_bytes(N: int, K: int) -> int:
     return N * (K // 32) * 18 if N > 0 and K > 0 and K % 32 == 0 else 0
 
 
-_ws_cache = {}
+@functools.lru_cache(maxsize=4096)
+def _ws_query(device: int, fn: str, *args) -> int:
+    return int(getattr(lib(), fn)(*args))
 
 
 def _ws_bytes(fn: str, *args) -> int:
     # a workspace size depends on the arguments and on the current device
     # (the GEMM's K split follows its SM count): one library query per
-    # distinct (device, call shape)
-    key = (fn, torch.cuda.current_device()) + args
-    v = _ws_cache.get(key)
-    if v is None:
-        v = _ws_cache[key] = int(getattr(lib(), fn)(*args))
-    return v
+    # distinct (device, call shape), of the latest few thousand (steps of a
+    # server are ragged: every one may have a shape of its own)
+    return _ws_query(torch.cuda.current_device(), fn, *args)
 
 
 def _mm_args(x, wq, N, K, out, out_dtype=torch.float32):
