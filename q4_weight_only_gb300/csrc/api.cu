@@ -44,7 +44,7 @@ __global__ void wait_timeout_selftest_kernel(unsigned long long limit_ns, unsign
     const unsigned long long t0 = global_ns();
     while (!mbar_try_wait(&bar, 0)) {
         if (global_ns() - t0 > limit_ns) {
-            report(err, kErrWaitTimeout);
+            atomicExch(err, kErrWaitTimeout);
             return;
         }
     }

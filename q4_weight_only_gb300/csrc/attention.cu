@@ -255,7 +255,7 @@ __device__ __forceinline__ void locate(const Params &p, Start &st, int cta, int 
     };
     for (int b0 = 0; b0 < p.sequences; b0 += kThreads) {
         const int b = round(b0);
-        if (cta == 0 && b < p.sequences && !sequence_fits(p, s, b)) report(p.err, kErrBadIndex);
+        if (cta == 0 && b < p.sequences && !sequence_fits(p, s, b)) report_index(p.err);
     }
     const int64_t each = before, all = each * p.kv_heads;
     // A key tile belongs to the share in which it ends.  Every share but the
@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Group then = fetch();
                 if (now.off < 0 || now.page < 0 || now.page >= p.pages) {
                     // a page coordinate past the end reads zeros
-                    if (now.off >= 0) report(p.err, kErrBadIndex);
+                    if (now.off >= 0) report_index(p.err);
                     now.page = p.pages, now.off = 0;
                 }
                 for (int j = 0; j < now.tiles; ++j) {

@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads, 6) kv_append_kernel(const KvAppendAr
         off = pos - index * c.page_size;
         const bool turns = !a.rot || (turn_row >= 0 && turn_row < a.positions);
         if (!turns || page < 0 || page >= c.pages) {
-            if (threadIdx.x == 0) report(err, kErrBadIndex);
+            if (threadIdx.x == 0) report_index(err);
             ok = false;
         }
     }

@@ -252,7 +252,7 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, int row, const 
             float lp = empty ? -INFINITY : (g.x - v.m) - ln_s;
             if (g.token < 0) lp = 0.f;
             if (g.token >= a.vocab) {
-                report(err, kErrBadIndex);
+                report_index(err);
                 lp = __uint_as_float(0x7FC00000u);
             }
             a.logprob[row] = lp;
