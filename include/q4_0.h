@@ -402,6 +402,9 @@ typedef struct {
  *                for the row's position in its sequence.  The cache slot
  *                always follows the position in the sequence.
  *   q_out      : bfloat16 [rows][q_heads][head_dim].
+ * A row without a place (a position before its sequence's start among them,
+ * which q4_0_attention lets see nothing) or without a row of cos_sin is skipped
+ * and reported: neither q_out nor the cache is written for it.
  * Computed in fp32, rounded once to bfloat16.  head_dim and rot are
  * multiples of 8.  With rot 0 nothing is rotated: cos_sin (then NULL or not),
  * positions and row_positions are not looked at.  Rows of one call must not
@@ -425,7 +428,7 @@ int q4_0_kv_append(const void *qkv, int qkv_type, int64_t qkv_stride, int64_t ro
  *                exponentials of the row's scaled scores; or NULL.
  *   max_q_len  : at least every q_start[b + 1] - q_start[b] (a longer
  *                sequence is cut to it and reported by q4_0_device_error).
- *   scale      : > 0, multiplies q . k.
+ *   scale      : > 0 and at most 1e30, multiplies q . k.
  *   window     : 0, or the number of latest tokens a row sees, itself
  *                included; sinks: first tokens it sees all the same.
  * The row at position t sees the keys j <= t with window == 0 or

@@ -42,16 +42,17 @@
 //   the first reads and the join.
 // * A prompt is bound by the chain softmax -> P V and the next Q K of a group
 //   (1500 + 1800 cycles a pair of tiles at D = 128, of which the tensor cores
-//   are busy 2048): 8192 tokens after 8192 others take 1.34 ms, 1.54 PFLOP/s
-//   (1.42 ms in a long run, at the board's power limit).  TMEM is full (two
-//   S, two O), so a group's next scores cannot start earlier.  A shorter
-//   softmax would show; the exponential units are not what bounds it (a
-//   polynomial on the multiply-add units for 1/8 to 1/2 of the elements made
-//   it 3 to 25 % slower).
+//   are busy 2048): 8192 tokens after 8192 others take 1.34 to 1.38 ms, 1.49
+//   to 1.54 PFLOP/s (1.43 ms in a long run, at the board's power limit).
+//   TMEM is full (two S, two O), so a group's next scores cannot start
+//   earlier.  A shorter softmax would show; the exponential units are not
+//   what bounds it (a polynomial on the multiply-add units for 1/8 to 1/2 of
+//   the elements made it 3 to 18 % slower).
 // * Prompts of 2500 to 3500 tokens under a window of 1000 (24 heads on 4, D =
-//   64) take 143 us: 2750 cycles a pair of tiles, and 10000 more an item of
+//   64) take 142 us: 2750 cycles a pair of tiles, and 10000 more an item of
 //   ten, for masks at both ends of the window, both groups' start at once,
-//   the last product and the rows' stores.
+//   the last product and the rows' stores.  With 40 heads on 8, D = 128, they
+//   take 265 us.
 // * One token after 2047 takes 16.7 us against a floor of 1.2: 4.3 launch, 4
 //   join, the rest reads that wait for one another.
 #include <cuda.h>

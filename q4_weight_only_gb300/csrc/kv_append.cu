@@ -37,11 +37,12 @@ __device__ __forceinline__ void turn(float &a, float &b, float cosv, float sinv)
 
 // blockIdx.x: row of qkv, blockIdx.y: piece of `heads` heads of the row.
 // Bound by the read of qkv and the writes: 8191 fp32 rows of 7168 (352 MB)
-// take 57 us, 6.2 TB/s, 0.91 of what a copy reaches.  One bulk copy brings
-// the piece to shared memory while the CTA finds the row's place in the cache
-// (sequence, length, page); several CTAs an SM keep their pieces in flight
-// (loads into registers, 64 bytes a thread, took 76 us).  Few rows are bound
-// by latency: 16 or 272 rows take 6.3 us, 4.3 of it a launch that does
+// take 57 us, 6.2 TB/s, 0.91 of what a copy reaches; 8191 bf16 rows (239 MB)
+// 45 us, 5.3 TB/s, half the bytes behind the same look-ups.  One bulk copy
+// brings the piece to shared memory while the CTA finds the row's place in the
+// cache (sequence, length, page); several CTAs an SM keep their pieces in
+// flight (loads into registers, 64 bytes a thread, took 76 us).  Few rows are
+// bound by latency: 16 or 272 rows take 6.3 us, 4.3 of it a launch that does
 // nothing, the rest the reads for the row's place and its cosines.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 6) kv_append_kernel(const KvAppendArgs a, const KvCacheView c, int heads,

@@ -32,9 +32,11 @@
 // eight blocks shares one, and the first of them joins what the others leave
 // in its shared memory: a second kernel for that, with its workspace, made
 // one row of 32000 take 12.5 us, for 10.4.  Measured: 2048 fp32 rows of
-// 131072 take 201 us with 20 alternatives (5.3 TB/s) and 155 us with none
-// (6.9 TB/s, what a copy reaches); 16 bf16 rows of 128257 14.6 us, most of it
-// launch, first chunks and the end of the row.
+// 131072 take 201 us with 20 alternatives (5.3 TB/s) and 154 us with none
+// (7.0 TB/s, what a copy reaches).  bf16 rows of the same length are bound by
+// their instructions, 20 a logit with 20 alternatives and 12 with none: 201
+// and 124 us, where their bytes would take 79.  16 bf16 rows of
+// 128257 take 14.6 us, most of it launch, first chunks and the end of the row.
 #include <cuda_bf16.h>
 
 #include <type_traits>
