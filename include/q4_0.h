@@ -455,6 +455,98 @@ int q4_0_attention(const uint16_t *q, int64_t q_row_stride, int64_t q_head_strid
                    int64_t sinks, const q4_0_kv_cache *cache, void *workspace, size_t workspace_bytes,
                    void *stream);
 
+/* ------------------------------------------------------------------------
+ * The same cache in 4 bits: q4_0_kv_append_q4 quantises keys and values as it
+ * writes them, q4_0_kv_read_q4 reads tokens back and q4_0_attention_q4 attends
+ * to them.  A token takes 9/32 of the bytes it takes in bfloat16.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * q4_0_kv_cache_q4 -- a paged cache of Q4_0 blocks and the batch that extends
+ * or reads it.  Host struct, read during the call only; its pointers are
+ * device memory.  Along head_dim every 32 elements of a token's head are a
+ * block by the rules of q4_0_quantize, codes and scales apart:
+ *   k, v       : codes, one [kv_heads][page_size][head_dim / 2] block of bytes
+ *                per page in any order of the three outer dimensions: bytes
+ *                16 i .. 16 i + 15 of a token's head are block i's, element j
+ *                of the block in the low half of byte j, j + 16 in the high
+ *                half.  Strides in bytes, positive multiples of 16 (ignored
+ *                for a dimension of size 1); base addresses 16-byte aligned.
+ *   k_scale, v_scale : binary16, [kv_heads][page_size][head_dim / 32] per page
+ *                in the same way.  Strides in elements, positive; base
+ *                addresses element-aligned (q4_0_attention_q4: bases and
+ *                strides aligned to a token's head_dim / 32 scales).
+ *   an element is scale * (code - 8).
+ *   The batch (page_table to sequences) is that of q4_0_kv_cache.
+ * Sizes as for q4_0_kv_cache; head_dim a multiple of 32.
+ */
+typedef struct {
+    uint8_t *k, *v;
+    uint16_t *k_scale, *v_scale;
+    int64_t k_page_stride, k_head_stride, k_token_stride;
+    int64_t v_page_stride, v_head_stride, v_token_stride;
+    int64_t k_scale_page_stride, k_scale_head_stride, k_scale_token_stride;
+    int64_t v_scale_page_stride, v_scale_head_stride, v_scale_token_stride;
+    int64_t pages, page_size, kv_heads, head_dim;
+    const int32_t *page_table;
+    int64_t table_stride, table_width;
+    const int32_t *q_start, *kv_len;
+    int64_t sequences;
+} q4_0_kv_cache_q4;
+
+/*
+ * q4_0_kv_append_q4 -- q4_0_kv_append into that cache: arguments, places,
+ * skipped rows and q_out as there.  Rotated in fp32, each product and sum
+ * rounded by itself (no fma), queries rounded once to bfloat16; keys and values
+ * are quantised from fp32, so codes and scales equal q4_0_quantize's of the
+ * same fp32 elements bit for bit.  A block with an element that is NaN or
+ * larger than 65504 in size reads back as NaN (scale NaN, codes 8).
+ * Returns as q4_0_kv_append.
+ */
+int q4_0_kv_append_q4(const void *qkv, int qkv_type, int64_t qkv_stride, int64_t rows, int64_t q_heads,
+                      const float *cos_sin, int64_t positions, int64_t rot, int interleaved,
+                      const int32_t *row_positions, uint16_t *q_out, const q4_0_kv_cache_q4 *cache, void *stream);
+
+/*
+ * q4_0_kv_read_q4 -- the rows of a batch read back from the cache: row
+ * q_start[b] + i is the token at position
+ * kv_len[b] - (q_start[b + 1] - q_start[b]) + i of sequence b.  With the batch
+ * of an append these are the tokens it wrote; with q_start counting up whole
+ * sequences, all their tokens.
+ *   k_out, v_out : [rows][kv_heads][head_dim] of `out_type` (Q4_0_Y_F32:
+ *                exact; Q4_0_Y_BF16: rounded once), 16-byte aligned.
+ *   rows         : of k_out and v_out.
+ * A row of no sequence is not written; one without a place is not written
+ * either and is reported by q4_0_device_error.
+ * Returns Q4_0_OK, Q4_0_ERR_INVALID_ARG, Q4_0_ERR_UNSUPPORTED or
+ * Q4_0_ERR_CUDA.
+ */
+int q4_0_kv_read_q4(void *k_out, void *v_out, int out_type, int64_t rows, const q4_0_kv_cache_q4 *cache, void *stream);
+
+/*
+ * q4_0_attention_q4 -- q4_0_attention over that cache: arguments, what a row
+ * sees, rows that see nothing, what an unseen page or slot may hold and what
+ * is reported as there (a page out of range reads as zeros).  Scales at most
+ * 8188 in size, as q4_0_kv_append_q4 writes them.  A NaN scale of a key reaches
+ * only the rows that see it; of a value, it can also reach rows of the same
+ * sequence and call less than 256 / (q_heads / kv_heads) tokens before or after
+ * one that sees it.
+ * head_dim 64 or 128, q_heads / kv_heads <= 128, page_size a multiple of 8,
+ * rows * q_heads / kv_heads <= 2^30 (else UNSUPPORTED).
+ * Accuracy: scores, softmax statistics and sums in fp32; operands of the
+ * products are binary16: a row of q scaled by a power of two, elements of the
+ * cache and exponentials rounded once.
+ * Workspace: q4_0_attention_q4_workspace_bytes(...) bytes on the current
+ * device, 256-byte aligned, in use until the work on `stream` completes.
+ * Returns as q4_0_attention.
+ */
+size_t q4_0_attention_q4_workspace_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                         int64_t max_q_len);
+int q4_0_attention_q4(const uint16_t *q, int64_t q_row_stride, int64_t q_head_stride, void *out, int out_type,
+                      float *lse, int64_t rows, int64_t q_heads, int64_t max_q_len, float scale, int64_t window,
+                      int64_t sinks, const q4_0_kv_cache_q4 *cache, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
 /*
  * q4_0_token_logprobs -- per row of logits: log probability of a given
  * token, entropy of the distribution, and the top alternatives.

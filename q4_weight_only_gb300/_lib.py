@@ -53,6 +53,10 @@ SIGNATURES = {
     "q4_0_kv_append": ([_P, _INT, _I64, _I64, _I64, _P, _I64, _I64, _INT, _P, _P, _P, _P], _INT),
     "q4_0_attention_workspace_bytes": ([_I64, _I64, _I64, _I64, _I64], _SZ),
     "q4_0_attention": ([_P, _I64, _I64, _P, _INT, _P, _I64, _I64, _I64, _F32, _I64, _I64, _P, _P, _SZ, _P], _INT),
+    "q4_0_kv_append_q4": ([_P, _INT, _I64, _I64, _I64, _P, _I64, _I64, _INT, _P, _P, _P, _P], _INT),
+    "q4_0_kv_read_q4": ([_P, _P, _INT, _I64, _P, _P], _INT),
+    "q4_0_attention_q4_workspace_bytes": ([_I64, _I64, _I64, _I64, _I64], _SZ),
+    "q4_0_attention_q4": ([_P, _I64, _I64, _P, _INT, _P, _I64, _I64, _I64, _F32, _I64, _I64, _P, _P, _SZ, _P], _INT),
     "q4_0_token_logprobs": ([_P, _INT, _I64, _I64, _I64, _P, _INT, _P, _P, _P, _P, _P], _INT),
     "q4_0_selftest_wait_timeout": ([_I64, _P], _INT),
     "q4_0_device_error": ([ctypes.POINTER(_INT)], _INT),

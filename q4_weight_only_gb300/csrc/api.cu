@@ -436,8 +436,9 @@ int q4_0_matmul_host(const uint16_t *x_host, const uint8_t *wq, void *y_host, in
 namespace {
 bool y_type_ok(int t) { return t == Q4_0_Y_F32 || t == Q4_0_Y_BF16; }
 
-// A q4_0_kv_cache as the kernels take it; a status code.
-int cache_view(const q4_0_kv_cache *c, KvCacheView *v) {
+// What both caches' structs say of their sizes and the batch; a status code.
+extern "C++" template <typename Cache>
+int batch_fits(const Cache *c) {
     if (!c || !c->k || !c->v) return Q4_0_ERR_INVALID_ARG;
     // arrays without an element may have no address
     if (c->sequences && (!c->page_table || !c->q_start || !c->kv_len)) return Q4_0_ERR_INVALID_ARG;
@@ -450,6 +451,13 @@ int cache_view(const q4_0_kv_cache *c, KvCacheView *v) {
     if (c->pages > (1ll << 30) || c->page_size > (1ll << 20) || c->kv_heads > 1024 || c->head_dim > 1024 ||
         c->sequences > (1ll << 20) || c->table_width > (1ll << 30) / c->page_size)
         return Q4_0_ERR_UNSUPPORTED;
+    return Q4_0_OK;
+}
+
+// A q4_0_kv_cache as the kernels take it; a status code.
+int cache_view(const q4_0_kv_cache *c, KvCacheView *v) {
+    const int st = batch_fits(c);
+    if (st != Q4_0_OK) return st;
     const int64_t size[3] = {c->pages, c->kv_heads, c->page_size};
     const int64_t ks[3] = {c->k_page_stride, c->k_head_stride, c->k_token_stride};
     const int64_t vs[3] = {c->v_page_stride, c->v_head_stride, c->v_token_stride};
@@ -469,31 +477,100 @@ int cache_view(const q4_0_kv_cache *c, KvCacheView *v) {
     v->head_dim = (int)c->head_dim, v->table_width = (int)c->table_width, v->sequences = (int)c->sequences;
     return Q4_0_OK;
 }
+
+// A q4_0_kv_cache_q4 as the kernels take it; a status code.
+int cache_q4_view(const q4_0_kv_cache_q4 *c, KvQ4View *v) {
+    const int st = batch_fits(c);
+    if (st != Q4_0_OK) return st;
+    if (!c->k_scale || !c->v_scale || (reinterpret_cast<uintptr_t>(c->k_scale) & 1u) ||
+        (reinterpret_cast<uintptr_t>(c->v_scale) & 1u) || c->head_dim % 32)
+        return Q4_0_ERR_INVALID_ARG;
+    const int64_t size[3] = {c->pages, c->kv_heads, c->page_size}, scales = c->head_dim / 32;
+    const int64_t stride[4][3] = {{c->k_page_stride, c->k_head_stride, c->k_token_stride},
+                                  {c->v_page_stride, c->v_head_stride, c->v_token_stride},
+                                  {c->k_scale_page_stride, c->k_scale_head_stride, c->k_scale_token_stride},
+                                  {c->v_scale_page_stride, c->v_scale_head_stride, c->v_scale_token_stride}};
+    int64_t *const to[4] = {v->k_stride, v->v_stride, v->k_scale_stride, v->v_scale_stride};
+    for (int a = 0; a < 4; ++a)
+        for (int i = 0; i < 3; ++i) {
+            // the stride of a dimension of one element is never used
+            to[a][i] = size[i] == 1 ? (a < 2 ? 16 : scales) : stride[a][i];
+            if (to[a][i] < 1 || (a < 2 && to[a][i] % 16)) return Q4_0_ERR_INVALID_ARG;
+            if (to[a][i] >= (1ll << 38)) return Q4_0_ERR_UNSUPPORTED;
+        }
+    v->k = c->k, v->v = c->v, v->k_scale = c->k_scale, v->v_scale = c->v_scale;
+    v->page_table = c->page_table, v->q_start = c->q_start, v->kv_len = c->kv_len;
+    v->table_stride = c->table_stride;
+    v->pages = (int)c->pages, v->page_size = (int)c->page_size, v->kv_heads = (int)c->kv_heads;
+    v->head_dim = (int)c->head_dim, v->table_width = (int)c->table_width, v->sequences = (int)c->sequences;
+    return Q4_0_OK;
+}
+
+// What an append asks of its rows, for a checked cache; a status code.
+int append_fits(const void *qkv, int qkv_type, int64_t qkv_stride, int64_t rows, int64_t q_heads, const float *cos_sin,
+                int64_t positions, int64_t rot, const int32_t *row_positions, const uint16_t *q_out, int kv_heads,
+                int head_dim) {
+    if (!qkv || (rot && !cos_sin) || !q_out || !y_type_ok(qkv_type) || rows < 0 || q_heads < 1 || positions < 0)
+        return Q4_0_ERR_INVALID_ARG;
+    if (rot && positions < 1) return Q4_0_ERR_INVALID_ARG;
+    if (rot < 0 || rot > head_dim || rot % 8 || head_dim % 8) return Q4_0_ERR_INVALID_ARG;
+    if (rows > (1ll << 30) || q_heads > 4096 || positions > (1ll << 30) || qkv_stride > (1ll << 32))
+        return Q4_0_ERR_UNSUPPORTED;
+    const int64_t vec = qkv_type == Q4_0_Y_BF16 ? 8 : 4;  // elements of 16 bytes
+    if (qkv_stride < (q_heads + 2 * kv_heads) * head_dim || qkv_stride % vec) return Q4_0_ERR_INVALID_ARG;
+    if (!aligned16(qkv) || !aligned16(cos_sin) || !aligned16(q_out) ||
+        (reinterpret_cast<uintptr_t>(row_positions) & 3u))
+        return Q4_0_ERR_INVALID_ARG;
+    return Q4_0_OK;
+}
 }  // namespace
 
 int q4_0_kv_append(const void *qkv, int qkv_type, int64_t qkv_stride, int64_t rows, int64_t q_heads,
                    const float *cos_sin, int64_t positions, int64_t rot, int interleaved,
                    const int32_t *row_positions, uint16_t *q_out, const q4_0_kv_cache *cache, void *stream) {
     KvCacheView c;
-    const int st = cache_view(cache, &c);
+    int st = cache_view(cache, &c);
     if (st != Q4_0_OK) return st;
-    if (!qkv || (rot && !cos_sin) || !q_out || !y_type_ok(qkv_type) || rows < 0 || q_heads < 1 || positions < 0)
-        return Q4_0_ERR_INVALID_ARG;
-    if (rot && positions < 1) return Q4_0_ERR_INVALID_ARG;
-    if (rot < 0 || rot > c.head_dim || rot % 8 || c.head_dim % 8) return Q4_0_ERR_INVALID_ARG;
-    if (rows > (1ll << 30) || q_heads > 4096 || positions > (1ll << 30) || qkv_stride > (1ll << 32))
-        return Q4_0_ERR_UNSUPPORTED;
-    const int64_t vec = qkv_type == Q4_0_Y_BF16 ? 8 : 4;  // elements of 16 bytes
-    if (qkv_stride < (q_heads + 2 * c.kv_heads) * c.head_dim || qkv_stride % vec) return Q4_0_ERR_INVALID_ARG;
-    if (!aligned16(qkv) || !aligned16(cos_sin) || !aligned16(q_out) ||
-        (reinterpret_cast<uintptr_t>(row_positions) & 3u))
-        return Q4_0_ERR_INVALID_ARG;
+    st = append_fits(qkv, qkv_type, qkv_stride, rows, q_heads, cos_sin, positions, rot, row_positions, q_out, c.kv_heads,
+                     c.head_dim);
+    if (st != Q4_0_OK) return st;
     if (rows == 0 || c.sequences == 0) return Q4_0_OK;
     unsigned int *err = device_error_word();
     if (!err) return Q4_0_ERR_CUDA;
     const KvAppendArgs a{qkv,           qkv_stride, cos_sin, row_positions, reinterpret_cast<__nv_bfloat16 *>(q_out),
                          (int)q_heads, (int)positions, (int)rot, interleaved != 0};
     return from_cuda(launch_kv_append(a, c, rows, qkv_type == Q4_0_Y_BF16, static_cast<cudaStream_t>(stream), err));
+}
+
+int q4_0_kv_append_q4(const void *qkv, int qkv_type, int64_t qkv_stride, int64_t rows, int64_t q_heads,
+                      const float *cos_sin, int64_t positions, int64_t rot, int interleaved,
+                      const int32_t *row_positions, uint16_t *q_out, const q4_0_kv_cache_q4 *cache, void *stream) {
+    KvQ4View c;
+    int st = cache_q4_view(cache, &c);
+    if (st != Q4_0_OK) return st;
+    st = append_fits(qkv, qkv_type, qkv_stride, rows, q_heads, cos_sin, positions, rot, row_positions, q_out, c.kv_heads,
+                     c.head_dim);
+    if (st != Q4_0_OK) return st;
+    if (rows == 0 || c.sequences == 0) return Q4_0_OK;
+    unsigned int *err = device_error_word();
+    if (!err) return Q4_0_ERR_CUDA;
+    const KvAppendArgs a{qkv,           qkv_stride, cos_sin, row_positions, reinterpret_cast<__nv_bfloat16 *>(q_out),
+                         (int)q_heads, (int)positions, (int)rot, interleaved != 0};
+    return from_cuda(launch_kv_append_q4(a, c, rows, qkv_type == Q4_0_Y_BF16, static_cast<cudaStream_t>(stream), err));
+}
+
+int q4_0_kv_read_q4(void *k_out, void *v_out, int out_type, int64_t rows, const q4_0_kv_cache_q4 *cache, void *stream) {
+    KvQ4View c;
+    const int st = cache_q4_view(cache, &c);
+    if (st != Q4_0_OK) return st;
+    if (!k_out || !v_out || !y_type_ok(out_type) || rows < 0 || !aligned16(k_out) || !aligned16(v_out))
+        return Q4_0_ERR_INVALID_ARG;
+    if (rows > (1ll << 30)) return Q4_0_ERR_UNSUPPORTED;
+    if (rows == 0 || c.sequences == 0) return Q4_0_OK;
+    unsigned int *err = device_error_word();
+    if (!err) return Q4_0_ERR_CUDA;
+    return from_cuda(launch_kv_read_q4(c, rows, k_out, v_out, out_type == Q4_0_Y_BF16, static_cast<cudaStream_t>(stream),
+                                       err));
 }
 
 namespace {
@@ -503,6 +580,30 @@ int attention_sizes(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t hea
     if ((head_dim != 64 && head_dim != 128) || q_heads / kv_heads > 128 || q_heads > 4096 || rows > (1ll << 30) ||
         max_q_len > (1ll << 30))
         return Q4_0_ERR_UNSUPPORTED;
+    return Q4_0_OK;
+}
+
+// The checked arguments of an attention over a checked cache; a status code.
+int attention_args(const uint16_t *q, int64_t q_row_stride, int64_t q_head_stride, void *out, int out_type, float *lse,
+                   int64_t rows, int64_t q_heads, int64_t max_q_len, float scale, int64_t window, int64_t sinks,
+                   int kv_heads, int head_dim, int page_size, AttentionArgs *a) {
+    if (!q || !out || !y_type_ok(out_type) || window < 0 || sinks < 0 || !(scale > 0.f) || scale > 1e30f)
+        return Q4_0_ERR_INVALID_ARG;
+    const int st = attention_sizes(rows, q_heads, kv_heads, head_dim, max_q_len);
+    if (st != Q4_0_OK) return st;
+    if (page_size % 8) return Q4_0_ERR_UNSUPPORTED;
+    const int64_t hs = q_heads == 1 ? 8 : q_head_stride, rs = rows <= 1 ? 8 : q_row_stride;
+    if (hs < 1 || rs < 1 || hs % 8 || rs % 8) return Q4_0_ERR_INVALID_ARG;
+    if (hs >= (1ll << 30) || rs >= (1ll << 38)) return Q4_0_ERR_UNSUPPORTED;
+    if (!aligned16(q) || (reinterpret_cast<uintptr_t>(out) & 31u) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+        return Q4_0_ERR_INVALID_ARG;
+    const int64_t most = 1ll << 30;
+    a->q = reinterpret_cast<const __nv_bfloat16 *>(q);
+    a->q_row_stride = rs, a->q_head_stride = hs;
+    a->out = out, a->out_bf16 = out_type == Q4_0_Y_BF16, a->lse = lse;
+    a->rows = (int)rows, a->q_heads = (int)q_heads, a->max_q_len = (int)(max_q_len < rows ? max_q_len : rows);
+    a->window = (int)(window < most ? window : most), a->sinks = (int)(sinks < most ? sinks : most);
+    a->scale = scale;
     return Q4_0_OK;
 }
 }  // namespace
@@ -521,31 +622,60 @@ int q4_0_attention(const uint16_t *q, int64_t q_row_stride, int64_t q_head_strid
     KvCacheView c;
     int st = cache_view(cache, &c);
     if (st != Q4_0_OK) return st;
-    if (!q || !out || !y_type_ok(out_type) || window < 0 || sinks < 0 || !(scale > 0.f) || scale > 1e30f)
-        return Q4_0_ERR_INVALID_ARG;
-    st = attention_sizes(rows, q_heads, c.kv_heads, c.head_dim, max_q_len);
+    AttentionArgs a{};
+    st = attention_args(q, q_row_stride, q_head_stride, out, out_type, lse, rows, q_heads, max_q_len, scale, window, sinks,
+                        c.kv_heads, c.head_dim, c.page_size, &a);
     if (st != Q4_0_OK) return st;
-    if (c.page_size % 8) return Q4_0_ERR_UNSUPPORTED;
-    const int64_t hs = q_heads == 1 ? 8 : q_head_stride, rs = rows <= 1 ? 8 : q_row_stride;
-    if (hs < 1 || rs < 1 || hs % 8 || rs % 8) return Q4_0_ERR_INVALID_ARG;
-    if (hs >= (1ll << 30) || rs >= (1ll << 38)) return Q4_0_ERR_UNSUPPORTED;
-    if (!aligned16(q) || (reinterpret_cast<uintptr_t>(out) & 31u) || (reinterpret_cast<uintptr_t>(lse) & 3u))
-        return Q4_0_ERR_INVALID_ARG;
     if (rows == 0 || c.sequences == 0) return Q4_0_OK;
     const size_t need = q4_0_attention_workspace_bytes(rows, q_heads, c.kv_heads, c.head_dim, max_q_len);
     if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return Q4_0_ERR_WORKSPACE;
     unsigned int *err = device_error_word();
     if (!err) return Q4_0_ERR_CUDA;
-    const int64_t most = 1ll << 30;
-    AttentionArgs a{};
-    a.q = reinterpret_cast<const __nv_bfloat16 *>(q);
-    a.q_row_stride = rs, a.q_head_stride = hs;
-    a.out = out, a.out_bf16 = out_type == Q4_0_Y_BF16, a.lse = lse;
-    a.rows = (int)rows, a.q_heads = (int)q_heads, a.max_q_len = (int)(max_q_len < rows ? max_q_len : rows);
-    a.window = (int)(window < most ? window : most), a.sinks = (int)(sinks < most ? sinks : most);
-    a.scale = scale;
     return from_cuda(launch_attention(a, c, workspace, static_cast<cudaStream_t>(stream), err));
+}
+
+namespace {
+// As attention_sizes, for the kernels of the 4-bit cache, which number a
+// sequence's (token, head of the group) rows in 31 bits.
+int attention_q4_sizes(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_q_len) {
+    const int st = attention_sizes(rows, q_heads, kv_heads, head_dim, max_q_len);
+    return st == Q4_0_OK && rows * (q_heads / kv_heads) > (1ll << 30) ? Q4_0_ERR_UNSUPPORTED : st;
+}
+}  // namespace
+
+size_t q4_0_attention_q4_workspace_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                         int64_t max_q_len) {
+    if (rows < 1 || attention_q4_sizes(rows, q_heads, kv_heads, head_dim, max_q_len) != Q4_0_OK) return 0;
+    return attention_q4_workspace_bytes((int)q_heads, (int)kv_heads, (int)head_dim,
+                                        (int)(max_q_len < rows ? max_q_len : rows));
+}
+
+int q4_0_attention_q4(const uint16_t *q, int64_t q_row_stride, int64_t q_head_stride, void *out, int out_type,
+                      float *lse, int64_t rows, int64_t q_heads, int64_t max_q_len, float scale, int64_t window,
+                      int64_t sinks, const q4_0_kv_cache_q4 *cache, void *workspace, size_t workspace_bytes,
+                      void *stream) {
+    KvQ4View c;
+    int st = cache_q4_view(cache, &c);
+    if (st != Q4_0_OK) return st;
+    AttentionArgs a{};
+    st = attention_args(q, q_row_stride, q_head_stride, out, out_type, lse, rows, q_heads, max_q_len, scale, window, sinks,
+                        c.kv_heads, c.head_dim, c.page_size, &a);
+    if (st != Q4_0_OK) return st;
+    if (attention_q4_sizes(rows, q_heads, c.kv_heads, c.head_dim, max_q_len) != Q4_0_OK) return Q4_0_ERR_UNSUPPORTED;
+    // a token's scales are copied at once
+    const int64_t scales = c.head_dim / 32;
+    if (reinterpret_cast<uintptr_t>(c.k_scale) % (scales * 2) || reinterpret_cast<uintptr_t>(c.v_scale) % (scales * 2))
+        return Q4_0_ERR_INVALID_ARG;
+    for (int i = 0; i < 3; ++i)
+        if (c.k_scale_stride[i] % scales || c.v_scale_stride[i] % scales) return Q4_0_ERR_INVALID_ARG;
+    if (rows == 0 || c.sequences == 0) return Q4_0_OK;
+    const size_t need = q4_0_attention_q4_workspace_bytes(rows, q_heads, c.kv_heads, c.head_dim, max_q_len);
+    if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return Q4_0_ERR_WORKSPACE;
+    unsigned int *err = device_error_word();
+    if (!err) return Q4_0_ERR_CUDA;
+    return from_cuda(launch_attention_q4(a, c, workspace, static_cast<cudaStream_t>(stream), err));
 }
 
 namespace {

@@ -59,9 +59,9 @@
 #include <cuda_bf16.h>
 
 #include <cmath>
-#include <mutex>
 #include <type_traits>
 
+#include "attention_plan.cuh"
 #include "q4_0_internal.h"
 #include "q4_0_ptx.cuh"
 
@@ -104,36 +104,6 @@ struct Params {
     unsigned int *err;
 };
 
-// Flags of a CTA's record.
-constexpr int kHeadPiece = 1;     // its first piece continues an item of an earlier CTA
-constexpr int kHeadGoesOn = 2;    // ... which also goes on in the next CTA
-constexpr int kTailPiece = 4;     // its last piece starts an item that goes on in the next CTA
-
-// Bits 0 .. n - 1.
-__device__ __forceinline__ uint32_t below(int n) {
-    return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1;
-}
-
-// One sequence of the batch, clamped to what the arrays can hold.
-struct Sequence {
-    int row0, len, kv;  // first row of q, rows, tokens in the cache
-};
-
-__device__ __forceinline__ Sequence sequence(const Params &p, int b) {
-    Sequence s;
-    const int r0 = min(max(p.q_start[b], 0), p.rows);
-    const int r1 = min(max(p.q_start[b + 1], r0), min(p.rows, r0 + p.max_q_len));
-    s.row0 = r0;
-    s.len = r1 - r0;
-    s.kv = (int)min((int64_t)max(p.kv_len[b], 0), (int64_t)p.table_width * p.page_size);
-    return s;
-}
-
-// Whether the arrays hold what the call promised of sequence b.
-__device__ __forceinline__ bool sequence_fits(const Params &p, const Sequence &s, int b) {
-    return p.q_start[b] == s.row0 && p.q_start[b + 1] == s.row0 + s.len && p.kv_len[b] == s.kv;
-}
-
 __device__ __forceinline__ int items_of(const Params &p, const Sequence &s) {
     return (s.len + 2 * p.tokens - 1) / (2 * p.tokens);
 }
@@ -172,140 +142,13 @@ struct Item {
     __device__ __forceinline__ int key_tile(int t) const { return t < sink_tiles ? t : wtile + t - sink_tiles; }
 };
 
-struct Start {
-    int64_t left;  // cost from the start of the first item to the end of the share
-    int head, b, item, t0;
-    Sequence s;
-    int64_t warp_sum[kThreads / 32];
-};
-
-__device__ __forceinline__ Sequence shuffle(const Sequence &s, int lane) {
-    return Sequence{__shfl_sync(0xffffffffu, s.row0, lane), __shfl_sync(0xffffffffu, s.len, lane),
-                    __shfl_sync(0xffffffffu, s.kv, lane)};
-}
-
 __device__ __forceinline__ int tile_cost(const Params &p, const Range &r) { return p.cost[r.tokens > p.tokens]; }
+
+__device__ __forceinline__ int largest_cost(const Params &p) { return p.cost[1]; }
 
 __device__ __forceinline__ int64_t item_cost(const Params &p, const Sequence &s, int item) {
     const Range r = item_range(p, s, item);
     return (int64_t)r.n * tile_cost(p, r);
-}
-
-// Cost (for one key head) of each lane's sequence; the warp takes the items
-// of a long one together.
-__device__ __forceinline__ int64_t sequence_cost(const Params &p, const Sequence &s, int lane) {
-    const int n = items_of(p, s);
-    int64_t mine = n == 1 ? item_cost(p, s, 0) : 0;
-    for (uint32_t many = __ballot_sync(0xffffffffu, n > 1); many; many &= many - 1) {
-        const int src = __ffs(many) - 1;
-        const Sequence t = shuffle(s, src);
-        const int nt = items_of(p, t);
-        int64_t sum = 0;
-        for (int i = lane; i < nt; i += 32) sum += item_cost(p, t, i);
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (lane == src) mine = sum;
-    }
-    return mine;
-}
-
-template <typename T>
-__device__ __forceinline__ T warp_inclusive(T v, int lane) {
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const T o = __shfl_up_sync(0xffffffffu, v, d);
-        if (lane >= d) v += o;
-    }
-    return v;
-}
-
-// floor(all * i / n) without a product past 64 bits.
-template <typename T>
-__device__ __forceinline__ T share_start(T all, T n, T i) {
-    const T each = all / n;
-    return each * i + (all - each * n) * i / n;
-}
-
-// Where this CTA's share begins.  Called by all threads; the result is in
-// `st` after the call.
-__device__ __forceinline__ void locate(const Params &p, Start &st, int cta, int ctas) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    Sequence s;
-    int64_t mine, first;  // cost of this thread's sequence, and of the ones before it
-    int64_t before = 0;   // cost of earlier rounds' sequences
-    // a round: one sequence a thread
-    auto round = [&](int b0) {
-        const int b = b0 + tid;
-        s = Sequence{0, 0, 0};
-        if (b < p.sequences) s = sequence(p, b);
-        mine = sequence_cost(p, s, lane);
-        const int64_t incl = warp_inclusive(mine, lane);
-        if (lane == 31) st.warp_sum[warp] = incl;
-        __syncthreads();
-        int64_t sum = 0, ahead = 0;
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-            const int64_t v = st.warp_sum[w];
-            if (w < warp) ahead += v;
-            sum += v;
-        }
-        __syncthreads();
-        first = before + ahead + incl - mine;
-        before += sum;
-        return b;
-    };
-    for (int b0 = 0; b0 < p.sequences; b0 += kThreads) {
-        const int b = round(b0);
-        if (cta == 0 && b < p.sequences && !sequence_fits(p, s, b)) report_index(p.err);
-    }
-    const int64_t each = before, all = each * p.kv_heads;
-    // A key tile belongs to the share in which it ends.  Every share but the
-    // empty ones at the end has a tile (it is at least one tile's cost long):
-    // an item's pieces are in consecutive CTAs.
-    const int64_t n = min(max(all / p.cost[1], (int64_t)(all > 0)), (int64_t)ctas);
-    if (cta >= n) {
-        if (tid == 0) st.left = 0;
-        __syncthreads();
-        return;
-    }
-    int64_t u0, u1;
-    int head;
-    if (all < (1ll << 31)) {
-        u0 = share_start<uint32_t>((uint32_t)all, (uint32_t)n, cta);
-        u1 = share_start<uint32_t>((uint32_t)all, (uint32_t)n, cta + 1);
-        head = (int)((uint32_t)u0 / (uint32_t)each);
-    } else {
-        u0 = share_start<int64_t>(all, n, cta);
-        u1 = share_start<int64_t>(all, n, cta + 1);
-        head = (int)(u0 / each);
-    }
-    const int64_t goal = u0 - head * each;  // where the share begins within its key head
-    const bool again = p.sequences > kThreads;
-    before = 0;
-    for (int b0 = 0; b0 < p.sequences; b0 += kThreads) {
-        if (again) round(b0);
-        const uint32_t hit = __ballot_sync(0xffffffffu, goal >= first && goal < first + mine);
-        if (!hit) continue;
-        // the warp that has the sequence looks through its items
-        const int src = __ffs(hit) - 1;
-        const Sequence t = shuffle(s, src);
-        const int nt = items_of(p, t);
-        int64_t rest = goal - __shfl_sync(0xffffffffu, first, src);
-        for (int i0 = 0; i0 < nt; i0 += 32) {
-            const int64_t k = i0 + lane < nt ? item_cost(p, t, i0 + lane) : 0;
-            const int64_t incl = warp_inclusive(k, lane);
-            if (rest >= incl - k && rest < incl) {
-                const int64_t in = rest - (incl - k);
-                st.head = head, st.b = b0 + warp * 32 + src, st.item = i0 + lane, st.s = t;
-                st.t0 = (int)(in / tile_cost(p, item_range(p, t, i0 + lane)));
-                st.left = u1 - u0 + in;
-            }
-            const int64_t sum = __shfl_sync(0xffffffffu, incl, 31);
-            if (rest < sum) break;
-            rest -= sum;
-        }
-    }
-    __syncthreads();
 }
 
 // f(0), f(1), ... f(N - 1) with constants as arguments.
@@ -348,7 +191,7 @@ struct Bars {
     uint32_t tmem;
     uint32_t fills[2], q_fills;  // copies made: past the last K and V tile's ring position, and of Q
     int abort;
-    Start start;
+    Start<kThreads> start;
 };
 static_assert(sizeof(Bars<10>) <= kStatBytes, "");
 
@@ -401,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     pdl_launch_dependents();
     pdl_wait();
-    locate(p, bar.start, blockIdx.x, gridDim.x);
+    locate<kThreads>(p, bar.start, blockIdx.x, gridDim.x);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1041,24 +884,6 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
 
 // -------------------------------------------------------------------- host
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(f);
-    });
-    return fn;
-}
-
 // A 4-D bfloat16 tensor with 64-element rows of its copies swizzled over 128
 // bytes; strides in elements.
 bool make_map(EncodeTiledFn enc, CUtensorMap *map, const void *base, const int64_t (&dim)[4],
@@ -1139,11 +964,6 @@ cudaError_t launch_d(const AttentionArgs &a, const KvCacheView &c, void *workspa
     if (e != cudaSuccess) return e;
     const int blocks = (p.piece_rows + 7) / 8;  // a row a warp; past 8 blocks an item is slower (32: by 3 us)
     return launch_pdl(attention_join_kernel<D>, dim3(ctas, blocks < 8 ? blocks : 8), dim3(256), 0, s, p, ctas);
-}
-
-int current_sms() {
-    int dev = 0;
-    return cudaGetDevice(&dev) == cudaSuccess ? device_sm_count(dev) : 0;
 }
 
 }  // namespace

@@ -1,0 +1,714 @@
+// attention_q4.cu -- causal attention over a paged cache in Q4_0 blocks
+// (declared in include/q4_0.h).
+//
+// Mathematics, for a query row at position t and the keys j it sees
+// (j <= t, and j > t - window or j < sinks): with a running reference m,
+//   p_j = 2^(c (s_j - m)),  l = sum p_j,  O = sum p_j v_j,  out = O / l,
+// s_j = q . k_j, c = scale * log2 e, all of s, m, l and O in fp32.  The
+// reference follows the running maximum only when a row's maximum grew by more
+// than 2^8 in p: the result does not depend on it, and most steps then skip the
+// correction of O.  The difference s - m is made before the product with c: a
+// certain key has p = 1 exactly.
+//
+// Operands of the tensor cores are binary16:
+// * a key's codes less 8, exactly; its blocks' scales multiply the blocks' dot
+//   products in fp32;
+// * a value d (code - 8), rounded (2^-11): the format holds elements up to
+//   65504;
+// * a query row times a power of two that brings its largest element to
+//   [2^14, 2^15), undone in c: exact for every element within 2^29 of the
+//   largest, off by at most 2^-39 of that below;
+// * p, at most 2^8, rounded (2^-11, and 2^-25 where it is below 2^-14); l sums p
+//   before the rounding.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cmath>
+
+#include "attention_plan.cuh"
+#include "q4_0_internal.h"
+#include "q4_0_ptx.cuh"
+
+namespace q4_0 {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kGrow = 8.f;  // log2 of the growth of a row's maximum that moves its reference
+constexpr int kStep = 32;     // keys a warp takes at a time
+
+struct Params {
+    KvQ4View c;
+    // the batch, as sequence() reads it
+    const int32_t *page_table, *q_start, *kv_len;
+    int64_t table_stride;
+    int sequences, table_width, pages, page_size, rows, max_q_len;
+    uint32_t page_magic, page_shift;  // t / page_size = umulhi(t, magic) >> shift, t < 2^31
+    int q_heads, kv_heads, group, window, sinks;
+    int item_rows;  // rows of an item: (token, head of the group) pairs of a sequence, in order
+    const __nv_bfloat16 *q;
+    int64_t q_row_stride, q_head_stride;
+    float scale_log2;
+    void *out;
+    float *lse;
+    int out_bf16;
+    float *part;       // [CTA][head piece, tail piece][item_rows][D], unnormalised
+    float4 *part_mlc;  // the rows' m, l and c
+    int4 *record;      // per CTA: flags, then first row (token * group + head), rows and key head of the tail piece's item
+    unsigned int *err;
+};
+
+__device__ __forceinline__ int items_of(const Params &p, const Sequence &s) {
+    return (s.len * p.group + p.item_rows - 1) / p.item_rows;
+}
+
+// The tokens the rows of an item see: [0, sink_end) and [lo, hi), and the
+// steps that hold them: `sink_steps` from token 0, then from step `wstep`.
+struct Range {
+    int row0, rows;   // the item's first row within the sequence, and its rows
+    int first, last;  // positions of its first and last row
+    int lo, hi, sink_end;
+    int sink_steps, wstep, n;
+    __device__ __forceinline__ int step(int t) const { return t < sink_steps ? t : wstep + t - sink_steps; }
+};
+
+__device__ __forceinline__ Range item_range(const Params &p, const Sequence &s, int item) {
+    Range r;
+    r.row0 = item * p.item_rows;
+    r.rows = min(p.item_rows, s.len * p.group - r.row0);
+    r.first = s.kv - s.len + r.row0 / p.group;
+    r.last = s.kv - s.len + (r.row0 + r.rows - 1) / p.group;
+    r.hi = max(r.last + 1, 0);
+    r.lo = p.window ? min(max(r.first - p.window + 1, 0), r.hi) : 0;
+    r.sink_end = min(p.sinks, r.lo);
+    r.wstep = r.lo / kStep;
+    r.sink_steps = min((r.sink_end + kStep - 1) / kStep, r.wstep);
+    // rows that see nothing still need their output: one empty step
+    r.n = max(r.sink_steps + (r.hi + kStep - 1) / kStep - r.wstep, 1);
+    return r;
+}
+
+__device__ __forceinline__ int tile_cost(const Params &, const Range &) { return 1; }
+__device__ __forceinline__ int largest_cost(const Params &) { return 1; }
+__device__ __forceinline__ int64_t item_cost(const Params &p, const Sequence &s, int item) {
+    return item_range(p, s, item).n;
+}
+
+// ------------------------------------------------------------- instructions
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// An 8 x 8 matrix of 16-bit elements, transposed within the warp.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// Asynchronous copies of 16, 8 or 4 bytes; nothing is read and zeros are
+// written where `bytes` is 0.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+template <int kBytes>
+__device__ __forceinline__ void copy_small(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<__half2 *>(&v); }
+__device__ __forceinline__ uint32_t as_bits(__half2 v) { return *reinterpret_cast<uint32_t *>(&v); }
+
+// The codes less 8 of the low nibbles of a word's bytes 0 and 2, and of their
+// high nibbles, as binary16 pairs: a nibble in the mantissa of 1024 makes 1024
+// + code, or 1024 + 16 code four bits higher; both steps are exact.  `bias`
+// holds kNibbleBias.
+__device__ __forceinline__ uint32_t low_codes(uint32_t w, uint32_t bias) {
+    return as_bits(__hsub2(as_half2(and_or<0x000F000Fu>(w, bias)), __half2half2(__ushort_as_half(0x6408))));
+}
+__device__ __forceinline__ uint32_t high_codes(uint32_t w, uint32_t bias) {
+    return as_bits(__hfma2(as_half2(and_or<0x00F000F0u>(w, bias)), __half2half2(__ushort_as_half(0x2C00)),
+                           __half2half2(__ushort_as_half(0xD480))));
+}
+__device__ __forceinline__ uint32_t times(uint32_t a, __half2 b) { return as_bits(__hmul2(as_half2(a), b)); }
+
+// --------------------------------------------------------------- the kernel
+
+// Shared memory of a warp's step: codes of 32 keys and of their values, then
+// the scales of both.
+template <int D>
+struct Stage {
+    static constexpr int kRow = D / 2;           // bytes of a token's codes
+    static constexpr int kScales = D / 16;       // bytes of its scales
+    static constexpr int kV = kStep * kRow, kKScale = 2 * kV, kVScale = kKScale + kStep * kScales;
+    static constexpr int kBytes = kVScale + kStep * kScales;
+    // Where 16-byte chunk `c` of a token's row is: tokens that a load reads
+    // at once, eight consecutive ones of a key's word, or four consecutive
+    // ones of a value's eight bytes (of which half a warp reads two chunks),
+    // are then in different banks.
+    static __device__ __forceinline__ int chunk(int token, int c) {
+        if (D == 128) return c ^ ((token >> 2 & 1) | (token & 2));
+        return c ^ (token >> 2 & 1);
+    }
+};
+
+template <int D, int NT, int W>
+struct Narrow {
+    static constexpr int kThreads = W * 32, kRows = NT * 8, kBlocks = D / 32, kTiles = D / 16;
+    static constexpr int kStages = W == 16 ? 3 : 5;
+    static constexpr int kOut = W * kStages * Stage<D>::kBytes;  // offset of the merged rows
+    static constexpr int kSmem = kOut + kRows * D * 4;
+    static_assert(kStages * Stage<D>::kBytes >= NT * kTiles * 4 * 32 * 4, "a warp's O fits its ring");
+};
+
+// Token number `i` of a tile of 16 keys, by its place in the MMAs' rows: a
+// lane's two neighbouring keys are then four tokens apart, and the four lanes
+// that read a value's word at once read consecutive tokens.
+__device__ __forceinline__ int tile_token(int i) { return (i & 8) + (i >> 1 & 3) + (i & 1) * 4; }
+
+// W warps; rows of an item: NT tiles of 8.  A warp takes every W-th step of 32
+// keys of an item's piece with a reference, sum and O of its own, through a
+// ring of its own: no barrier but the merge at the piece's end.
+template <int D, int NT, int W>
+__global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_constant__ Params p, uint32_t bias) {
+    using N = Narrow<D, NT, W>;
+    using S = Stage<D>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ Start<N::kThreads> start;
+    __shared__ float2 warp_ml[W][N::kRows];   // a warp's m and l, then its factor in the merge
+    __shared__ float4 row_mlc[N::kRows];
+    constexpr int NB = N::kBlocks, MT = N::kTiles, kStages = N::kStages;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t ring = smem_u32(smem) + warp * (kStages * S::kBytes);
+    float *merged = reinterpret_cast<float *>(smem + N::kOut);
+
+    pdl_launch_dependents();
+    pdl_wait();
+    locate<N::kThreads>(p, start, blockIdx.x, gridDim.x);
+    int flags = 0;
+    int4 tail = make_int4(0, 0, 0, 0);
+    int64_t left = start.left;
+    int head = start.head, b = start.b, it = start.item, t0 = start.t0;
+    Sequence s = start.s;
+    int n_items = items_of(p, s);
+
+    while (left > 0) {
+        const Range r = item_range(p, s, it);
+        const int t1 = left >= r.n ? r.n : (int)left;
+        const int steps = t1 - t0;
+        if (t0 > 0) flags |= kHeadPiece | (t1 < r.n ? kHeadGoesOn : 0);
+        if (t0 == 0 && t1 < r.n)
+            flags |= kTailPiece, tail = make_int4(0, s.row0 * p.group + r.row0, r.rows, head);
+
+        // ------------------------------------------------------ copies
+        const uint8_t *k_base = p.c.k + head * p.c.k_stride[1], *v_base = p.c.v + head * p.c.v_stride[1];
+        const uint16_t *ks_base = p.c.k_scale + head * p.c.k_scale_stride[1];
+        const uint16_t *vs_base = p.c.v_scale + head * p.c.v_scale_stride[1];
+        const int32_t *table = p.page_table + (int64_t)b * p.table_stride;
+        // Step t0 + i of the piece into stage i / W of the warp's ring; a
+        // token no row of the item sees, or without a page, becomes zeros.
+        auto copy_step = [&](int i) {
+            if (i < steps) {
+                const uint32_t st = ring + (i / W) % kStages * S::kBytes;
+                const int token = r.step(t0 + i) * kStep + lane;
+                bool seen = token < r.sink_end || (token >= r.lo && token < r.hi);
+                int page = 0, off = 0;
+                if (seen) {
+                    const int index = __umulhi((uint32_t)token, p.page_magic) >> p.page_shift;
+                    page = table[index], off = token - index * p.page_size;
+                    if (page < 0 || page >= p.pages) {
+                        report_index(p.err);
+                        seen = false, page = 0, off = 0;
+                    }
+                }
+                const uint32_t all_seen = __ballot_sync(0xffffffffu, seen);
+                const uint64_t k = reinterpret_cast<uint64_t>(k_base + page * p.c.k_stride[0] + off * p.c.k_stride[2]);
+                const uint64_t v = reinterpret_cast<uint64_t>(v_base + page * p.c.v_stride[0] + off * p.c.v_stride[2]);
+                constexpr int kChunks = S::kRow / 16, kAtOnce = 32 / kChunks;
+                const int chunk = lane % kChunks;
+#pragma unroll
+                for (int j = 0; j < kStep / kAtOnce; ++j) {
+                    const int tok = j * kAtOnce + lane / kChunks;
+                    const uint64_t ka = __shfl_sync(0xffffffffu, k, tok), va = __shfl_sync(0xffffffffu, v, tok);
+                    const uint32_t to = st + tok * S::kRow + S::chunk(tok, chunk) * 16;
+                    const int bytes = all_seen >> tok & 1 ? 16 : 0;
+                    copy16(to, reinterpret_cast<const void *>(ka + chunk * 16), bytes);
+                    copy16(to + S::kV, reinterpret_cast<const void *>(va + chunk * 16), bytes);
+                }
+                const int bytes = seen ? S::kScales : 0;
+                copy_small<S::kScales>(st + S::kKScale + lane * S::kScales,
+                                       ks_base + page * p.c.k_scale_stride[0] + off * p.c.k_scale_stride[2], bytes);
+                copy_small<S::kScales>(st + S::kVScale + lane * S::kScales,
+                                       vs_base + page * p.c.v_scale_stride[0] + off * p.c.v_scale_stride[2], bytes);
+            }
+            copy_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) copy_step(warp + i * W);
+
+        // ---------------------------------------------------- queries
+        // q as the second operand: column g of tile n, for block j and half x
+        // of it elements 4t + x, 4t + x + 2 and 16 further
+        uint32_t qf[NT][NB][2][2];
+        float c[NT][2];  // of columns 2t and 2t + 1
+        int pos[NT][2];  // their positions
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int row = n * 8 + g;
+            uint2 lo[NB], hi[NB];
+            float top = 0.f;
+#pragma unroll
+            for (int j = 0; j < NB; ++j) lo[j] = hi[j] = make_uint2(0, 0);
+            if (row < r.rows) {
+                const int token = (r.row0 + row) / p.group, in_group = r.row0 + row - token * p.group;
+                const __nv_bfloat16 *src =
+                    p.q + (s.row0 + token) * p.q_row_stride + (head * p.group + in_group) * p.q_head_stride;
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    lo[j] = *reinterpret_cast<const uint2 *>(src + 32 * j + 4 * t);
+                    hi[j] = *reinterpret_cast<const uint2 *>(src + 32 * j + 16 + 4 * t);
+                }
+            }
+            auto low = [](uint32_t w) { return __uint_as_float(w << 16); };
+            auto high = [](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); };
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                top = fmaxf(top, fmaxf(fmaxf(fabsf(low(lo[j].x)), fabsf(high(lo[j].x))),
+                                       fmaxf(fabsf(low(lo[j].y)), fabsf(high(lo[j].y)))));
+                top = fmaxf(top, fmaxf(fmaxf(fabsf(low(hi[j].x)), fabsf(high(hi[j].x))),
+                                       fmaxf(fabsf(low(hi[j].y)), fabsf(high(hi[j].y)))));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // 2^up brings the largest element to [2^14, 2^15); a row of
+            // zeros or with an infinity is left alone
+            const int exponent = (int)(__float_as_uint(top) >> 23) - 127;
+            const int up = top > 0.f && top < INFINITY ? min(14 - exponent, 100) : 0;
+            const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+            const float down = __uint_as_float((uint32_t)(127 - up) << 23);
+            const float row_c = fminf(p.scale_log2 * down, 3e38f);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) c[n][x] = __shfl_sync(0xffffffffu, row_c, (2 * t + x) * 4);
+            auto pair = [&](float a, float z) { return as_bits(__floats2half2_rn(a * f, z * f)); };
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                qf[n][j][0][0] = pair(low(lo[j].x), low(lo[j].y)), qf[n][j][1][0] = pair(high(lo[j].x), high(lo[j].y));
+                qf[n][j][0][1] = pair(low(hi[j].x), low(hi[j].y)), qf[n][j][1][1] = pair(high(hi[j].x), high(hi[j].y));
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) pos[n][x] = s.kv - s.len + (r.row0 + n * 8 + 2 * t + x) / p.group;
+        }
+
+        // -------------------------------------------------------- keys
+        float m[NT][2], l[NT][2], o[NT][MT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+        }
+        for (int i = warp; i < steps; i += W) {
+            copy_step(i + (kStages - 1) * W);
+            copy_wait<kStages - 1>();
+            __syncwarp();
+            const uint32_t st = ring + (i / W) % kStages * S::kBytes;
+            // scores: keys by queries, two tiles of 16 keys
+            float sc[2][NT][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r0 = h * 16 + tile_token(g), r1 = r0 + 8;
+                uint32_t d0[NB / 2], d1[NB / 2];
+                if (D == 128) {
+                    const uint2 x = lds64(st + S::kKScale + r0 * 8), y = lds64(st + S::kKScale + r1 * 8);
+                    d0[0] = x.x, d0[NB / 2 - 1] = x.y, d1[0] = y.x, d1[NB / 2 - 1] = y.y;
+                } else {
+                    d0[0] = lds32(st + S::kKScale + r0 * 4), d1[0] = lds32(st + S::kKScale + r1 * 4);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) sc[h][n][0] = sc[h][n][1] = sc[h][n][2] = sc[h][n][3] = 0.f;
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    const uint32_t w0 = lds32(st + r0 * S::kRow + S::chunk(r0, j) * 16 + t * 4);
+                    const uint32_t w1 = lds32(st + r1 * S::kRow + S::chunk(r1, j) * 16 + t * 4);
+                    float acc[NT][4] = {};
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t u0 = w0 >> 8 * x, u1 = w1 >> 8 * x;
+                        const uint32_t a0 = low_codes(u0, bias), a1 = low_codes(u1, bias);
+                        const uint32_t a2 = high_codes(u0, bias), a3 = high_codes(u1, bias);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma16816(acc[n], a0, a1, a2, a3, qf[n][j][x][0], qf[n][j][x][1]);
+                    }
+                    const __half2 e0 = as_half2(d0[j / 2]), e1 = as_half2(d1[j / 2]);
+                    const float f0 = j & 1 ? __high2float(e0) : __low2float(e0);
+                    const float f1 = j & 1 ? __high2float(e1) : __low2float(e1);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        sc[h][n][0] = fmaf(f0, acc[n][0], sc[h][n][0]), sc[h][n][1] = fmaf(f0, acc[n][1], sc[h][n][1]);
+                        sc[h][n][2] = fmaf(f1, acc[n][2], sc[h][n][2]), sc[h][n][3] = fmaf(f1, acc[n][3], sc[h][n][3]);
+                    }
+                }
+            }
+            const int tok0 = r.step(t0 + i) * kStep;
+            if (tok0 + kStep - 1 > r.first || (p.window && tok0 <= r.last - p.window && tok0 + kStep > p.sinks)) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int tok = tok0 + h * 16 + tile_token(g) + (x >> 1) * 8, at = pos[n][x & 1];
+                            if (tok > at || (p.window && tok <= at - p.window && tok >= p.sinks)) sc[h][n][x] = -INFINITY;
+                        }
+            }
+            // references that a score outgrew move, in all lanes of a column
+            bool grew = false;
+            float top[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    top[n][x] = fmaxf(fmaxf(sc[0][n][x], sc[0][n][x + 2]), fmaxf(sc[1][n][x], sc[1][n][x + 2]));
+                    grew |= (top[n][x] - m[n][x]) * c[n][x] > kGrow;
+                }
+            if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float f[2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float v = fmaxf(top[n][x], m[n][x]);
+#pragma unroll
+                        for (int d = 4; d <= 16; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+                        f[x] = m[n][x] == v ? 1.f : ex2((m[n][x] - v) * c[n][x]);
+                        m[n][x] = v;
+                        l[n][x] *= f[x];
+                    }
+#pragma unroll
+                    for (int j = 0; j < MT; ++j) {
+                        o[n][j][0] *= f[0], o[n][j][1] *= f[1];
+                        o[n][j][2] *= f[0], o[n][j][3] *= f[1];
+                    }
+                }
+            }
+            // p as the second operand of values by queries
+            uint32_t pf[2][NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float base[2] = {m[n][0] == -INFINITY ? 0.f : m[n][0], m[n][1] == -INFINITY ? 0.f : m[n][1]};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float e[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        e[x] = ex2((sc[h][n][x] - base[x & 1]) * c[n][x & 1]);
+                        l[n][x & 1] += e[x];
+                    }
+                    pf[h][n][0] = transpose8x8(as_bits(__floats2half2_rn(e[0], e[1])));
+                    pf[h][n][1] = transpose8x8(as_bits(__floats2half2_rn(e[2], e[3])));
+                }
+            }
+            // values: a lane's 16 (D = 64: 8) elements of a token are 8 (4)
+            // bytes, all of one block
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t w[4][D / 64], d[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int tok = h * 16 + t + 4 * k;
+                    if (D == 128) {
+                        const uint2 x = lds64(st + S::kV + tok * S::kRow + S::chunk(tok, g >> 1) * 16 + (g & 1) * 8);
+                        w[k][0] = x.x, w[k][D / 64 - 1] = x.y;
+                        d[k] = lds16(st + S::kVScale + tok * 8 + (g >> 1) * 2);
+                    } else {
+                        w[k][0] = lds32(st + S::kV + tok * S::kRow + S::chunk(tok, g >> 2) * 16 + (g & 3) * 4);
+                        d[k] = lds16(st + S::kVScale + tok * 4 + (g >> 2) * 2);
+                    }
+                }
+                const __half2 d01 = as_half2(__byte_perm(d[0], d[1], 0x5410)), d23 = as_half2(__byte_perm(d[2], d[3], 0x5410));
+#pragma unroll
+                for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t sel = half ? 0x7632 : 0x5410;
+                        const uint32_t a = __byte_perm(w[0][j], w[1][j], sel), z = __byte_perm(w[2][j], w[3][j], sel);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const uint32_t u = a >> 8 * x, y = z >> 8 * x;
+                            const uint32_t a0 = times(low_codes(u, bias), d01), a1 = times(high_codes(u, bias), d01);
+                            const uint32_t a2 = times(low_codes(y, bias), d23), a3 = times(high_codes(y, bias), d23);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma16816(o[n][(j * 2 + half) * 2 + x], a0, a1, a2, a3, pf[h][n][0], pf[h][n][1]);
+                        }
+                    }
+            }
+            __syncwarp();
+        }
+        copy_wait<0>();
+
+        // ------------------------------------------------------- merge
+        // the warps' O into their rings, element by element as the lanes
+        // hold them
+        float *mine = reinterpret_cast<float *>(smem + warp * (kStages * S::kBytes));
+        __syncwarp();
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) mine[((n * MT + j) * 4 + x) * 32 + lane] = o[n][j][x];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                for (int d = 4; d <= 16; d <<= 1) l[n][x] += __shfl_xor_sync(0xffffffffu, l[n][x], d);
+                if (g == 0) {
+                    warp_ml[warp][n * 8 + 2 * t + x] = make_float2(m[n][x], l[n][x]);
+                    if (warp == 0) row_mlc[n * 8 + 2 * t + x].z = c[n][x];
+                }
+            }
+        }
+        __syncthreads();
+        const bool whole = t0 == 0 && t1 == r.n;
+        if (tid < N::kRows) {
+            const float row_c = row_mlc[tid].z;
+            float top = -INFINITY, sum = 0.f;
+            for (int w = 0; w < W; ++w) top = fmaxf(top, warp_ml[w][tid].x);
+            for (int w = 0; w < W; ++w) {
+                const float2 ml = warp_ml[w][tid];
+                // a warp without a step has no reference, and a sum of 0
+                const float f = ml.x == top ? 1.f : ex2((ml.x - top) * row_c);
+                sum += ml.y * f;
+                warp_ml[w][tid].x = f;
+            }
+            const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+            if (whole)
+                for (int w = 0; w < W; ++w) warp_ml[w][tid].x *= inv;
+            row_mlc[tid].x = top, row_mlc[tid].y = sum;
+        }
+        __syncthreads();
+        const float *rings = reinterpret_cast<const float *>(smem);
+        for (int e = tid; e < N::kRows * D; e += N::kThreads) {
+            const int le = e & 31, x = e >> 5 & 3, j = (e >> 7) % MT, n = (e >> 7) / MT, gg = le >> 2;
+            const int row = n * 8 + 2 * (le & 3) + (x & 1);
+            float v = 0.f;
+            for (int w = 0; w < W; ++w) v = fmaf(warp_ml[w][row].x, rings[w * (kStages * S::kBytes / 4) + e], v);
+            // the lane's byte of its block, and the element it holds
+            const int byte = (D == 128 ? 8 * (gg & 1) : 4 * (gg & 3)) + j;
+            const int d = (D == 128 ? 32 * (gg >> 1) : 32 * (gg >> 2)) + byte + (x >> 1) * 16;
+            merged[row * D + d] = v;
+        }
+        __syncthreads();
+        const int f0 = s.row0 * p.group + r.row0;
+        const int piece = (blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * p.item_rows;
+        // place of a row of the item in [rows][q_heads]
+        auto place = [&](int row) {
+            const int token = (f0 + row) / p.group;
+            return (int64_t)token * p.q_heads + head * p.group + (f0 + row - token * p.group);
+        };
+        for (int e = tid * 4; e < r.rows * D; e += N::kThreads * 4) {
+            const int row = e / D, d = e - row * D;
+            const float4 v = *reinterpret_cast<const float4 *>(merged + e);
+            const int64_t at = place(row) * D + d;
+            if (!whole)
+                *reinterpret_cast<float4 *>(p.part + (int64_t)(piece + row) * D + d) = v;
+            else if (p.out_bf16)
+                *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at) =
+                    make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+            else
+                *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = v;
+        }
+        if (tid < r.rows) {
+            const float4 mlc = row_mlc[tid];
+            if (!whole)
+                p.part_mlc[piece + tid] = mlc;
+            else if (p.lse)
+                p.lse[place(tid)] = (mlc.x * mlc.z + __log2f(mlc.y)) * kLn2;
+        }
+        __syncthreads();
+
+        // -------------------------------------------------- next item
+        left -= r.n;
+        t0 = 0;
+        if (left > 0 && ++it >= n_items) {
+            it = 0;
+            int scanned = 0;
+            do {
+                if (++b >= p.sequences) {
+                    b = 0;
+                    ++head;
+                }
+                s = sequence(p, b);
+            } while (items_of(p, s) == 0 && ++scanned <= p.sequences);
+            n_items = items_of(p, s);
+        }
+    }
+    tail.x = flags;
+    if (tid == 0) p.record[blockIdx.x] = tail;
+}
+
+// Adds the pieces of the items that a share's boundary cut.  blockIdx.x: the
+// CTA whose tail piece starts the item; a warp takes every (gridDim.y * 8)-th
+// of its rows.
+template <int D>
+__global__ void __launch_bounds__(256) attention_q4_join_kernel(const __grid_constant__ Params p, int ctas) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int4 rec = p.record[blockIdx.x];
+    // pieces: this CTA's tail, then the heads of the next ones
+    int n = 1;
+    for (bool more = true; more; n += 32) {
+        const int e = blockIdx.x + n + lane;
+        const int f = e < ctas ? p.record[e].x : 0;
+        // the first CTA whose piece is not of the item, or is its last
+        const uint32_t none = __ballot_sync(0xffffffffu, !(f & kHeadPiece));
+        const uint32_t last = __ballot_sync(0xffffffffu, (f & kHeadPiece) && !(f & kHeadGoesOn));
+        const int end_none = none ? __ffs(none) - 1 : 32, end_last = last ? __ffs(last) : 33;
+        const int end = min(end_none, end_last);
+        if (end <= 32 && (none | last)) {
+            n += end - 32;
+            more = false;
+        }
+    }
+    if (!(rec.x & kTailPiece)) return;
+    constexpr int kOwn = D / 32;
+    auto place = [&](int i, int r) { return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * p.item_rows + r; };
+    for (int row = blockIdx.y * 8 + warp; row < rec.z; row += gridDim.y * 8) {
+        float m = -INFINITY;
+        for (int i = lane; i < n; i += 32) m = fmaxf(m, p.part_mlc[place(i, row)].x);
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        float acc[kOwn] = {}, l = 0.f, c = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float4 mlc = p.part_mlc[place(i, row)];
+            const float *src = p.part + place(i, row) * D + lane * kOwn;
+            float v[kOwn];
+#pragma unroll
+            for (int e = 0; e < kOwn; e += 2) {
+                const float2 x = *reinterpret_cast<const float2 *>(src + e);
+                v[e] = x.x, v[e + 1] = x.y;
+            }
+            c = mlc.z;
+            const float f = mlc.x == m ? 1.f : ex2((mlc.x - m) * c);
+            l += mlc.y * f;
+#pragma unroll
+            for (int e = 0; e < kOwn; ++e) acc[e] = fmaf(v[e], f, acc[e]);
+        }
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        const int token = (rec.y + row) / p.group;
+        const int64_t at = (int64_t)token * p.q_heads + rec.w * p.group + (rec.y + row - token * p.group);
+#pragma unroll
+        for (int e = 0; e < kOwn; e += 2) {
+            const int64_t to = at * D + lane * kOwn + e;
+            if (p.out_bf16)
+                *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.out) + to) =
+                    pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+            else
+                *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + to) = make_float2(acc[e] * inv, acc[e + 1] * inv);
+        }
+        if (p.lse && lane == 0) p.lse[at] = (m * c + __log2f(l)) * kLn2;
+    }
+}
+
+// -------------------------------------------------------------------- host
+
+// Rows of an item: tiles of 8, as few as hold the rows of a sequence.
+int item_rows(int group, int max_q_len) {
+    const int64_t rows = (int64_t)group * max_q_len;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+}
+
+struct WorkspaceLayout {
+    size_t mlc_off, rec_off, bytes;
+    WorkspaceLayout(int ctas, int D, int rows_each) {
+        const size_t rows = (size_t)ctas * 2 * rows_each;
+        mlc_off = rows * D * 4;
+        rec_off = mlc_off + rows * 16;
+        bytes = (rec_off + (size_t)ctas * 16 + 255) / 256 * 256;
+    }
+};
+
+template <int D, int NT, int W>
+cudaError_t launch_narrow(const Params &p, int ctas, cudaStream_t s) {
+    using N = Narrow<D, NT, W>;
+    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(attention_q4_kernel<D, NT, W>), N::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(attention_q4_kernel<D, NT, W>, dim3(ctas), dim3(N::kThreads), N::kSmem, s, p, kNibbleBias);
+}
+
+template <int D>
+cudaError_t launch_d(const AttentionArgs &a, const KvQ4View &c, void *workspace, int ctas, cudaStream_t s,
+                     unsigned int *err) {
+    Params p{};
+    p.c = c;
+    p.page_table = c.page_table, p.q_start = c.q_start, p.kv_len = c.kv_len, p.table_stride = c.table_stride;
+    p.sequences = c.sequences, p.table_width = c.table_width, p.pages = c.pages, p.page_size = c.page_size;
+    p.rows = a.rows, p.max_q_len = a.max_q_len;
+    // with 2^s < page_size <= 2^(s + 1), t = floor(t m / 2^(32 + s)) for m the
+    // next whole number from 2^(32 + s) / page_size and t < 2^31
+    while ((2 << p.page_shift) < c.page_size) ++p.page_shift;
+    p.page_magic = (uint32_t)(((1ull << (32 + p.page_shift)) + c.page_size - 1) / c.page_size);
+    p.q_heads = a.q_heads, p.kv_heads = c.kv_heads, p.group = a.q_heads / c.kv_heads;
+    p.window = a.window, p.sinks = a.sinks;
+    p.item_rows = item_rows(p.group, a.max_q_len);
+    p.q = a.q, p.q_row_stride = a.q_row_stride, p.q_head_stride = a.q_head_stride;
+    p.scale_log2 = a.scale * kLog2e;
+    p.out = a.out, p.lse = a.lse, p.out_bf16 = a.out_bf16;
+    const WorkspaceLayout w(ctas, D, p.item_rows);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.part = reinterpret_cast<float *>(ws);
+    p.part_mlc = reinterpret_cast<float4 *>(ws + w.mlc_off);
+    p.record = reinterpret_cast<int4 *>(ws + w.rec_off);
+    p.err = err;
+    cudaError_t e = p.item_rows == 8    ? launch_narrow<D, 1, 16>(p, ctas, s)
+                    : p.item_rows == 16 ? launch_narrow<D, 2, 8>(p, ctas, s)
+                                        : launch_narrow<D, 4, 8>(p, ctas, s);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(attention_q4_join_kernel<D>, dim3(ctas, p.item_rows / 8), dim3(256), 0, s, p, ctas);
+}
+
+}  // namespace
+
+size_t attention_q4_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q_len) {
+    return WorkspaceLayout(current_sms(), head_dim, item_rows(q_heads / kv_heads, max_q_len)).bytes;
+}
+
+cudaError_t launch_attention_q4(const AttentionArgs &a, const KvQ4View &c, void *workspace, cudaStream_t s,
+                                unsigned int *err) {
+    const int sms = current_sms();
+    if (sms < 1) return cudaErrorInvalidDevice;
+    return c.head_dim == 128 ? launch_d<128>(a, c, workspace, sms, s, err)
+                             : launch_d<64>(a, c, workspace, sms, s, err);
+}
+
+}  // namespace q4_0

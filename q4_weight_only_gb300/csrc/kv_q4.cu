@@ -1,0 +1,315 @@
+// kv_q4.cu -- a paged key and value cache in Q4_0 blocks: queries and keys of
+// fused QKV rows rotated by position, keys and values quantised as they are
+// appended, and tokens read back (declared in include/q4_0.h).
+//
+// Mathematics: a key's pair (a, b) at position t becomes
+//   (a cos - b sin, b cos + a sin),  cos, sin = table[t][p],
+// every product and sum rounded to fp32 by itself: the codes are discontinuous
+// in their inputs, so an fma in the place of a product and a sum would give
+// others here and there than any other fp32 implementation does.  A block of
+// 32 elements w of a head is then
+//   d = (w of the largest |w|, the first of equals) / -8,
+//   code = clamp(round(w / d) + 8, 0, 15), halves away from zero,
+// with d in fp32 for the codes and rounded to binary16 for the cache: the
+// rules of the weights' quantizer (quantize.cu), element j of a block in the
+// low half of byte j, j + 16 in its high half.  A block reads back as
+// d (code - 8), exactly in fp32.
+//
+// This translation unit must not be built with fast-math: the codes depend on
+// correctly rounded division and on roundf's tie rule.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "q4_0_internal.h"
+#include "q4_0_ptx.cuh"
+
+namespace q4_0 {
+
+namespace {
+
+constexpr int kVec = 8;  // elements of one work item
+constexpr int kThreads = 256;
+constexpr int kPieceBytes = 32 * 1024;  // most of a row that one CTA holds
+constexpr float kLargest = 65504.f;     // of an element: what binary16 holds, and what attention reads
+
+// Four consecutive elements as fp32.
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+    const uint2 a = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xFFFF0000u), __uint_as_float(a.y << 16),
+                       __uint_as_float(a.y & 0xFFFF0000u));
+}
+
+// (a, b) -> (a cos - b sin, b cos + a sin), without an fma.
+__device__ __forceinline__ void turn(float &a, float &b, float cosv, float sinv) {
+    const float a0 = a;
+    a = __fsub_rn(__fmul_rn(a0, cosv), __fmul_rn(b, sinv));
+    b = __fadd_rn(__fmul_rn(b, cosv), __fmul_rn(a0, sinv));
+}
+
+__device__ __forceinline__ uint32_t code_of(float w, float d) {
+    // w / d is within half a step of [-8, 8]; 0 / 0 and a d that became 0
+    // give codes that its scale of 0 makes no difference of
+    return (uint32_t)(int)(fminf(fmaxf(roundf(__fdiv_rn(w, d)), -8.f), 7.f) + 8.f);
+}
+
+// The largest element of a block so far.
+struct Largest {
+    float size, value;
+    int at;
+    __device__ __forceinline__ void add(float w, int i) {
+        const float a = fabsf(w);
+        const float s = a <= kLargest ? a : INFINITY;  // NaN too
+        if (s > size) size = s, value = w, at = i;
+    }
+};
+
+// A quad of lanes (`mask`) quantises a block, lane j of it elements 4j .. 4j +
+// 3 (u) and 16 + 4j .. (v), to bytes 4j .. 4j + 3 of `codes`.
+__device__ __forceinline__ void quantise_quad(float4 u, float4 v, int j, uint32_t mask, uint8_t *codes,
+                                              uint16_t *scale) {
+    Largest m{-1.f, 0.f, 0};
+    m.add(u.x, 4 * j), m.add(u.y, 4 * j + 1), m.add(u.z, 4 * j + 2), m.add(u.w, 4 * j + 3);
+    m.add(v.x, 16 + 4 * j), m.add(v.y, 17 + 4 * j), m.add(v.z, 18 + 4 * j), m.add(v.w, 19 + 4 * j);
+#pragma unroll
+    for (int d = 1; d <= 2; d <<= 1) {
+        const float size = __shfl_xor_sync(mask, m.size, d), value = __shfl_xor_sync(mask, m.value, d);
+        const int at = __shfl_xor_sync(mask, m.at, d);
+        if (size > m.size || (size == m.size && at < m.at)) m.size = size, m.value = value, m.at = at;
+    }
+    uint32_t w = 0x88888888u;
+    uint16_t s = 0;
+    if (m.size == INFINITY) {
+        s = 0x7FFF;  // the block reads back as NaN
+    } else if (m.size > 0.f) {
+        const float d = __fmul_rn(m.value, -0.125f);
+        s = __half_as_ushort(__float2half_rn(d));
+        w = code_of(u.x, d) | code_of(v.x, d) << 4 | code_of(u.y, d) << 8 | code_of(v.y, d) << 12 |
+            code_of(u.z, d) << 16 | code_of(v.z, d) << 20 | code_of(u.w, d) << 24 | code_of(v.w, d) << 28;
+    }
+    *reinterpret_cast<uint32_t *>(codes + 4 * j) = w;
+    if (j == 0) *scale = s;
+}
+
+// The place of a row of the batch: its sequence's page and the token in it.
+struct Place {
+    int pos, page, off;
+    bool in_sequence, ok;
+};
+
+__device__ __forceinline__ Place place_of(const KvQ4View &c, int row, int ended) {
+    Place p{0, -1, 0, false, false};
+    p.in_sequence = ended < c.sequences && row >= c.q_start[0];
+    if (!p.in_sequence) return p;
+    p.pos = c.kv_len[ended] - c.q_start[ended + 1] + row;
+    const int index = p.pos >= 0 ? p.pos / c.page_size : -1;
+    p.page = index >= 0 && index < c.table_width ? c.page_table[(int64_t)ended * c.table_stride + index] : -1;
+    p.off = p.pos - index * c.page_size;
+    p.ok = p.page >= 0 && p.page < c.pages;
+    return p;
+}
+
+// blockIdx.x: row of qkv, blockIdx.y: piece of `heads` heads of the row.  One
+// bulk copy brings the piece to shared memory while the CTA finds the row's
+// place in the cache.  Queries are rotated to q_out, keys in shared memory
+// (in the piece itself for fp32, beside it for bfloat16), and four lanes then
+// quantise a block.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 6) kv_append_q4_kernel(const KvAppendArgs a, const KvQ4View c, int heads,
+                                                                   unsigned int *err) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t full;
+    __shared__ int abort_flag;
+    constexpr bool kInPlace = sizeof(T) == 4;
+    T *piece = reinterpret_cast<T *>(smem);
+    const int row = blockIdx.x, head0 = blockIdx.y * heads;
+    const int n_heads = min(heads, a.q_heads + 2 * c.kv_heads - head0);
+    // keys [key0, value0) and values [value0, n_heads) of the piece
+    const int key0 = min(max(a.q_heads - head0, 0), n_heads);
+    const int value0 = min(max(a.q_heads + c.kv_heads - head0, 0), n_heads);
+    // keys in fp32, by the head's number in the piece
+    float *keys = kInPlace ? reinterpret_cast<float *>(smem)
+                           : reinterpret_cast<float *>(smem + heads * c.head_dim * sizeof(T)) - key0 * c.head_dim;
+    if (threadIdx.x == 0) {
+        mbar_init(&full, 1);
+        abort_flag = 0;
+        mbar_fence_init();
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+    if (threadIdx.x == 0) {
+        const uint32_t bytes = (uint32_t)(n_heads * c.head_dim * sizeof(T));
+        mbar_arrive_expect_tx(&full, bytes);
+        bulk_g2s(smem, static_cast<const T *>(a.qkv) + (int64_t)row * a.qkv_stride + (int64_t)head0 * c.head_dim, bytes,
+                 &full);
+    }
+    // the sequence the row belongs to: how many end at or before it
+    int ended = 0;
+    for (int base = 0; base < c.sequences; base += kThreads) {
+        const int b = base + threadIdx.x;
+        ended += __syncthreads_count(b < c.sequences && c.q_start[b + 1] <= row);
+    }
+    const Place place = place_of(c, row, ended);
+    bool ok = place.ok;
+    int turn_row = 0;
+    if (place.in_sequence) {
+        if (a.rot) turn_row = a.row_positions ? a.row_positions[row] : place.pos;
+        if (a.rot && (turn_row < 0 || turn_row >= a.positions)) ok = false;
+        if (!ok && threadIdx.x == 0) report_index(err);
+    }
+    const bool landed = mbar_wait(&full, 0, &abort_flag, err);
+    // (every thread waits for the same barrier, but gives up by itself)
+    if (!__syncthreads_and(ok && landed)) {
+        // a wait that was given up has been reported; the copy lands first
+        if (!landed) mbar_drain(&full, 0);
+        return;
+    }
+    const float *cs = a.cos_sin + (int64_t)turn_row * a.rot;
+    __nv_bfloat16 *q_row = a.q_out + (int64_t)row * a.q_heads * c.head_dim;
+    const int per_head = c.head_dim / kVec, half = a.rot / 2;
+    for (int it = threadIdx.x; it < value0 * per_head; it += kThreads) {
+        const int in_piece = it / per_head, i = it - in_piece * per_head;
+        const bool turned = i * kVec < a.rot, query = in_piece < key0;
+        if (kInPlace && !turned && !query) continue;
+        // first elements of the item's two halves
+        int e0 = i * kVec, e1 = e0 + 4;
+        if (turned && !a.interleaved) e0 = i * 4, e1 = half + i * 4;
+        const T *s = piece + in_piece * c.head_dim;
+        float4 u = load4(s + e0), v = load4(s + e1);
+        if (turned) {
+            const float4 cosv = load4(cs + i * 4), sinv = load4(cs + half + i * 4);
+            if (a.interleaved) {
+                turn(u.x, u.y, cosv.x, sinv.x), turn(u.z, u.w, cosv.y, sinv.y);
+                turn(v.x, v.y, cosv.z, sinv.z), turn(v.z, v.w, cosv.w, sinv.w);
+            } else {
+                turn(u.x, v.x, cosv.x, sinv.x), turn(u.y, v.y, cosv.y, sinv.y);
+                turn(u.z, v.z, cosv.z, sinv.z), turn(u.w, v.w, cosv.w, sinv.w);
+            }
+        }
+        if (query) {
+            __nv_bfloat16 *dst = q_row + (int64_t)(head0 + in_piece) * c.head_dim;
+            *reinterpret_cast<uint2 *>(dst + e0) = make_uint2(pack_bf16(u.x, u.y), pack_bf16(u.z, u.w));
+            *reinterpret_cast<uint2 *>(dst + e1) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+        } else {
+            float *dst = keys + in_piece * c.head_dim;
+            *reinterpret_cast<float4 *>(dst + e0) = u;
+            *reinterpret_cast<float4 *>(dst + e1) = v;
+        }
+    }
+    if (key0 == n_heads) return;
+    __syncthreads();
+    const int blocks = c.head_dim / 32, j = threadIdx.x & 3;
+    const uint32_t quad = 15u << (threadIdx.x & 28);
+    for (int it = threadIdx.x >> 2; it < (n_heads - key0) * blocks; it += kThreads / 4) {
+        const int in_piece = key0 + it / blocks, block = it % blocks, e = block * 32 + 4 * j;
+        const bool key = in_piece < value0;
+        float4 u, v;
+        if (key) {
+            u = load4(keys + in_piece * c.head_dim + e), v = load4(keys + in_piece * c.head_dim + e + 16);
+        } else {
+            u = load4(piece + in_piece * c.head_dim + e), v = load4(piece + in_piece * c.head_dim + e + 16);
+        }
+        const int head = head0 + in_piece - a.q_heads - (key ? 0 : c.kv_heads);
+        const int64_t *st = key ? c.k_stride : c.v_stride, *ss = key ? c.k_scale_stride : c.v_scale_stride;
+        uint8_t *codes = (key ? c.k : c.v) + place.page * st[0] + head * st[1] + place.off * st[2] + block * 16;
+        uint16_t *scale = (key ? c.k_scale : c.v_scale) + place.page * ss[0] + head * ss[1] + place.off * ss[2] + block;
+        quantise_quad(u, v, j, quad, codes, scale);
+    }
+}
+
+template <typename T>
+cudaError_t launch_append(const KvAppendArgs &a, const KvQ4View &c, int64_t rows, cudaStream_t s, unsigned int *err) {
+    // a head is at most 4 KB (head_dim <= 1024)
+    const int all = a.q_heads + 2 * c.kv_heads, fit = kPieceBytes / (c.head_dim * (int)sizeof(T));
+    const int pieces = (all + fit - 1) / fit, heads = (all + pieces - 1) / pieces;
+    int smem = heads * c.head_dim * (int)sizeof(T);
+    if (sizeof(T) == 2) smem += (heads < c.kv_heads ? heads : c.kv_heads) * c.head_dim * 4;
+    // past 48 KB, the kernel's own variables among them, a launch has to ask
+    if (smem > 47 * 1024) {
+        const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kv_append_q4_kernel<T>), smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(kv_append_q4_kernel<T>, dim3((unsigned)rows, pieces), dim3(kThreads), smem, s, a, c, heads, err);
+}
+
+// The values of four nibbles (the low ones, or after a shift the high ones, of
+// a word's bytes) times d.
+__device__ __forceinline__ float4 values4(uint32_t w, float d) {
+    // 2^23 + code less 2^23 + 8: exact
+    const float base = 8388616.f;
+    const uint32_t m = 0x4B000000u;
+    return make_float4((__uint_as_float((w & 15u) | m) - base) * d, (__uint_as_float((w >> 8 & 15u) | m) - base) * d,
+                       (__uint_as_float((w >> 16 & 15u) | m) - base) * d, (__uint_as_float((w >> 24 & 15u) | m) - base) * d);
+}
+
+__device__ __forceinline__ void store8(float *p, float4 a, float4 b) {
+    *reinterpret_cast<float4 *>(p) = a;
+    *reinterpret_cast<float4 *>(p + 4) = b;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, float4 a, float4 b) {
+    *reinterpret_cast<uint4 *>(p) =
+        make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
+}
+
+constexpr int kReadRows = 8;  // rows of a CTA, each warp finds the place of one
+
+// blockIdx.x: kReadRows rows of the batch.  A thread reads half a block (8
+// bytes of codes) and writes its 16 values.  Bound by the writes.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) kv_read_q4_kernel(const KvQ4View c, int rows, T *k_out, T *v_out,
+                                                              unsigned int *err) {
+    __shared__ int2 at[kReadRows];  // page (-1: none) and token of each row
+    pdl_launch_dependents();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row0 = blockIdx.x * kReadRows;
+    {
+        const int row = row0 + warp;
+        int ended = 0;
+        for (int base = 0; base < c.sequences; base += 32) {
+            const int b = base + lane;
+            ended += __popc(__ballot_sync(0xffffffffu, b < c.sequences && c.q_start[b + 1] <= row));
+        }
+        if (lane == 0) {
+            const Place p = row < rows ? place_of(c, row, ended) : Place{};
+            if (p.in_sequence && !p.ok) report_index(err);
+            at[warp] = make_int2(p.ok ? p.page : -1, p.off);
+        }
+    }
+    __syncthreads();
+    const int halves = c.head_dim / 16, per_side = c.kv_heads * halves, per_row = 2 * per_side;
+    for (int it = threadIdx.x; it < kReadRows * per_row; it += kThreads) {
+        const int r = it / per_row, i = it - r * per_row;
+        const int2 place = at[r];
+        if (place.x < 0) continue;
+        const bool key = i < per_side;
+        const int in_side = key ? i : i - per_side, head = in_side / halves, h = in_side - head * halves;
+        const int64_t *st = key ? c.k_stride : c.v_stride, *ss = key ? c.k_scale_stride : c.v_scale_stride;
+        const uint2 w = *reinterpret_cast<const uint2 *>((key ? c.k : c.v) + place.x * st[0] + head * st[1] +
+                                                         place.y * st[2] + h * 8);
+        const float d = __half2float(__ushort_as_half(
+            (key ? c.k_scale : c.v_scale)[place.x * ss[0] + head * ss[1] + place.y * ss[2] + (h >> 1)]));
+        T *dst = (key ? k_out : v_out) + ((int64_t)(row0 + r) * c.kv_heads + head) * c.head_dim + (h >> 1) * 32 +
+                 (h & 1) * 8;
+        store8(dst, values4(w.x, d), values4(w.y, d));
+        store8(dst + 16, values4(w.x >> 4, d), values4(w.y >> 4, d));
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append_q4(const KvAppendArgs &a, const KvQ4View &c, int64_t rows, bool bf16, cudaStream_t s,
+                                unsigned int *err) {
+    return bf16 ? launch_append<__nv_bfloat16>(a, c, rows, s, err) : launch_append<float>(a, c, rows, s, err);
+}
+
+cudaError_t launch_kv_read_q4(const KvQ4View &c, int64_t rows, void *k_out, void *v_out, bool bf16, cudaStream_t s,
+                              unsigned int *err) {
+    const dim3 grid((unsigned)((rows + kReadRows - 1) / kReadRows));
+    if (bf16)
+        return launch_pdl(kv_read_q4_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, s, c, (int)rows,
+                          static_cast<__nv_bfloat16 *>(k_out), static_cast<__nv_bfloat16 *>(v_out), err);
+    return launch_pdl(kv_read_q4_kernel<float>, grid, dim3(kThreads), 0, s, c, (int)rows, static_cast<float *>(k_out),
+                      static_cast<float *>(v_out), err);
+}
+
+}  // namespace q4_0

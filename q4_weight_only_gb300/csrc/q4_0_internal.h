@@ -143,6 +143,29 @@ size_t attention_workspace_bytes(int q_heads, int kv_heads, int head_dim, int ma
 cudaError_t launch_attention(const AttentionArgs &a, const KvCacheView &c, void *workspace, cudaStream_t s,
                              unsigned int *err);
 
+// The same with keys and values in Q4_0 blocks (q4_0_kv_cache_q4, checked):
+// codes with strides in bytes, scales with strides in elements, each for
+// {page, head, token}.
+struct KvQ4View {
+    uint8_t *k, *v;
+    uint16_t *k_scale, *v_scale;  // binary16
+    int64_t k_stride[3], v_stride[3], k_scale_stride[3], v_scale_stride[3];
+    const int32_t *page_table, *q_start, *kv_len;
+    int64_t table_stride;
+    int pages, page_size, kv_heads, head_dim, table_width, sequences;
+};
+
+cudaError_t launch_kv_append_q4(const KvAppendArgs &a, const KvQ4View &c, int64_t rows, bool bf16, cudaStream_t s,
+                                unsigned int *err);
+
+// k_out, v_out: fp32 or bfloat16 [rows][kv_heads][head_dim].
+cudaError_t launch_kv_read_q4(const KvQ4View &c, int64_t rows, void *k_out, void *v_out, bool bf16, cudaStream_t s,
+                              unsigned int *err);
+
+size_t attention_q4_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q_len);
+cudaError_t launch_attention_q4(const AttentionArgs &a, const KvQ4View &c, void *workspace, cudaStream_t s,
+                                unsigned int *err);
+
 struct LogprobArgs {
     const void *logits;  // fp32 or bfloat16 rows, row_stride elements apart
     int64_t row_stride;

@@ -1,5 +1,6 @@
 """Python binding of the operators around the matmuls: kv_append, attention
-and token_logprobs (argument marshalling only, see include/q4_0.h).
+and token_logprobs, and kv_append_q4, kv_read_q4 and attention_q4 for a cache
+in 4 bits (argument marshalling only, see include/q4_0.h).
 
 A paged cache is a pair of bfloat16 tensors [pages, kv_heads, page_size,
 head_dim] in any memory order whose head_dim elements are adjacent (a
@@ -9,12 +10,18 @@ head_dim] in any memory order whose head_dim elements are adjacent (a
 and kv_len [sequences] (its tokens in the cache, the new ones included).
 They are read on the device only, so a captured CUDA graph follows them.
 
+A cache in 4 bits is a KVCacheQ4: codes uint8 [pages, kv_heads, page_size,
+head_dim / 2] and scales float16 [pages, kv_heads, page_size, head_dim / 32] of
+keys and of values, in any memory order of the outer dimensions as above
+(kv_cache_q4 makes one).  An element is scale * (code - 8), in blocks of 32.
+
 A call with `stream` reads its inputs and writes its results there: that
 stream waits for whoever writes the inputs, and whoever reads the results
 waits for it, both in the caller's hands.  Results and workspaces that are not
 given are that stream's own memory.
 """
 import struct
+from typing import NamedTuple
 
 import torch
 
@@ -23,11 +30,23 @@ from ._lib import Y_BF16, Y_F32, _check, _need, _ws_bytes, lib
 MAX_TOP = 32
 
 _F32, _BF16, _I32, _I64 = torch.float32, torch.bfloat16, torch.int32, torch.int64
+_F16, _U8 = torch.float16, torch.uint8
 _TYPES = {_F32: Y_F32, _BF16: Y_BF16}
 
 # q4_0_kv_cache: two pointers, six strides, four sizes, the table and its two
 # sizes, two pointers and a size, all 64 bits
 _KV_CACHE = struct.Struct("=18q")
+
+# q4_0_kv_cache_q4: four pointers, twelve strides, four sizes and the batch
+_KV_CACHE_Q4 = struct.Struct("=26q")
+
+
+class KVCacheQ4(NamedTuple):
+    """A paged cache in Q4_0 blocks."""
+    k_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
 
 
 # The checks of a call run on every decode step and cost as much as its
@@ -129,23 +148,55 @@ def _cache(k_cache, v_cache, page_table, q_start, kv_len, device):
     return packed, heads, dim
 
 
-def kv_append(qkv: torch.Tensor, cos_sin: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
-              page_table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, *, q_heads: int,
-              interleaved: bool = False, positions: torch.Tensor = None, out: torch.Tensor = None,
-              stream=None) -> torch.Tensor:
-    """Rotate the queries and keys of qkv [rows, (q_heads + 2 kv_heads) *
-    head_dim] (fp32 or bf16: query, key and value heads) by position, append
-    keys and values to the cache in place, and return the queries, bf16
-    [rows, q_heads, head_dim].
+def kv_cache_q4(pages: int, kv_heads: int, page_size: int, head_dim: int, *, token_major: bool = False) -> KVCacheQ4:
+    """A cache of `pages` pages on the current device, all zeros; token_major:
+    a page holds [page_size, kv_heads, ...] instead of [kv_heads, page_size,
+    ...] (the tensors' shapes are the same)."""
+    if head_dim < 32 or head_dim % 32:
+        raise ValueError("head_dim must be a positive multiple of 32")
 
-    cos_sin: fp32 [positions, rot], cosines then sines of the rot / 2 pairs
-    (halves of the first rot elements, or neighbours when interleaved).
-    positions: int32 [rows], the row of cos_sin to use instead of the
-    position in the sequence."""
-    dev = torch.cuda.current_device()
+    def make(width, dtype):
+        if token_major:
+            return torch.zeros((pages, page_size, kv_heads, width), dtype=dtype, device="cuda").transpose(1, 2)
+        return torch.zeros((pages, kv_heads, page_size, width), dtype=dtype, device="cuda")
+
+    return KVCacheQ4(*(make(*kind) for kind in ((head_dim // 2, _U8), (head_dim // 32, _F16)) * 2))
+
+
+_BYTE, _HALF = (_U8,), (_F16,)
+
+
+def _cache_q4(cache, page_table, q_start, kv_len, device):
+    """The q4_0_kv_cache_q4 of these tensors, packed, and its heads and head_dim."""
+    k, k_scale, v, v_scale = cache
+    ks, vs = _rows(k, "k_codes", _BYTE, 4, device), _rows(v, "v_codes", _BYTE, 4, device)
+    kss, vss = _rows(k_scale, "k_scales", _HALF, 4, device), _rows(v_scale, "v_scales", _HALF, 4, device)
+    ts = _rows(page_table, "page_table", (_I32,), 2, device)
+    _plain(q_start, "q_start", _I32, 1, device)
+    _plain(kv_len, "kv_len", _I32, 1, device)
+    shape, scales = k.shape, k_scale.shape
+    if shape != v.shape or scales != v_scale.shape:
+        raise ValueError("keys and values must have the same shapes")
+    pages, heads, size, half = shape
+    if half % 16 or scales != (pages, heads, size, half // 16):
+        raise ValueError("codes must be [pages, kv_heads, page_size, head_dim / 2] and scales [pages, kv_heads, "
+                         "page_size, head_dim / 32]")
+    n = kv_len.shape[0]
+    sequences, width = page_table.shape
+    if q_start.shape[0] != n + 1 or sequences != n:
+        raise ValueError("page_table, q_start and kv_len must be of sequences, sequences + 1 and sequences rows")
+    packed = _KV_CACHE_Q4.pack(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                               *ks[:3], *vs[:3], *kss[:3], *vss[:3], pages, size, heads, 2 * half,
+                               page_table.data_ptr(), ts[0] if n > 1 else width, width, q_start.data_ptr(),
+                               kv_len.data_ptr(), n)
+    return packed, heads, 2 * half
+
+
+def _append(entry, cache_of, batch, qkv, cos_sin, q_heads, interleaved, positions, out, stream, dev):
+    """What both appends do with their arguments."""
     qs = _rows(qkv, "qkv", _TYPES, 2, dev)
     _plain(cos_sin, "cos_sin", _F32, 2, dev)
-    cache, kv_heads, dim = _cache(k_cache, v_cache, page_table, q_start, kv_len, dev)
+    cache, kv_heads, dim = cache_of(*batch)
     rows, width = qkv.shape
     if width != (q_heads + 2 * kv_heads) * dim:
         raise ValueError("qkv must be [rows, (q_heads + 2 * kv_heads) * head_dim]")
@@ -162,13 +213,31 @@ def kv_append(qkv: torch.Tensor, cos_sin: torch.Tensor, k_cache: torch.Tensor, v
     if rows == 0:
         return out
     turns, rot = cos_sin.shape
-    st = lib().q4_0_kv_append(qkv.data_ptr(), _TYPES[qkv.dtype], qs[0] if rows > 1 else width, rows, q_heads,
-                              cos_sin.data_ptr(), turns, rot, 1 if interleaved else 0,
-                              positions.data_ptr() if positions is not None else None, out.data_ptr(), cache,
-                              _stream_of(stream, dev))
+    st = getattr(lib(), entry)(qkv.data_ptr(), _TYPES[qkv.dtype], qs[0] if rows > 1 else width, rows, q_heads,
+                               cos_sin.data_ptr(), turns, rot, 1 if interleaved else 0,
+                               positions.data_ptr() if positions is not None else None, out.data_ptr(), cache,
+                               _stream_of(stream, dev))
     if st:
-        _check(st, "q4_0_kv_append")
+        _check(st, entry)
     return out
+
+
+def kv_append(qkv: torch.Tensor, cos_sin: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+              page_table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, *, q_heads: int,
+              interleaved: bool = False, positions: torch.Tensor = None, out: torch.Tensor = None,
+              stream=None) -> torch.Tensor:
+    """Rotate the queries and keys of qkv [rows, (q_heads + 2 kv_heads) *
+    head_dim] (fp32 or bf16: query, key and value heads) by position, append
+    keys and values to the cache in place, and return the queries, bf16
+    [rows, q_heads, head_dim].
+
+    cos_sin: fp32 [positions, rot], cosines then sines of the rot / 2 pairs
+    (halves of the first rot elements, or neighbours when interleaved).
+    positions: int32 [rows], the row of cos_sin to use instead of the
+    position in the sequence."""
+    dev = torch.cuda.current_device()
+    return _append("q4_0_kv_append", _cache, (k_cache, v_cache, page_table, q_start, kv_len, dev), qkv, cos_sin,
+                   q_heads, interleaved, positions, out, stream, dev)
 
 
 def attention_workspace_bytes(rows: int, q_heads: int, kv_heads: int, head_dim: int, max_q_len: int) -> int:
@@ -176,23 +245,12 @@ def attention_workspace_bytes(rows: int, q_heads: int, kv_heads: int, head_dim: 
     return _ws_bytes("q4_0_attention_workspace_bytes", rows, q_heads, kv_heads, head_dim, max_q_len)
 
 
-def attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
-              q_start: torch.Tensor, kv_len: torch.Tensor, *, max_q_len: int, scale: float = None, window: int = 0,
-              sinks: int = 0, out: torch.Tensor = None, out_dtype=torch.bfloat16, lse: torch.Tensor = None,
-              workspace: torch.Tensor = None, stream=None) -> torch.Tensor:
-    """Causal attention of q [rows, q_heads, head_dim] (bf16, any strides of
-    rows and heads) over the paged cache, the rows' own tokens included:
-    [rows, q_heads, head_dim] of out_dtype (bf16 or fp32).
-
-    max_q_len: the most new tokens of a sequence.  scale: head_dim ** -0.5
-    when not given.  window, sinks: a row sees its latest `window` tokens (0:
-    all) and the first `sinks`.  lse: fp32 [rows, q_heads] to receive the
-    natural logarithms of the softmax sums."""
+def _attend(entry, cache_of, batch, q, max_q_len, scale, window, sinks, out, out_dtype, lse, workspace, stream, dev):
+    """What both attentions do with their arguments."""
     if out_dtype not in _TYPES:
         raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
-    dev = torch.cuda.current_device()
     qs = _rows(q, "q", (_BF16,), 3, dev)
-    cache, kv_heads, cache_dim = _cache(k_cache, v_cache, page_table, q_start, kv_len, dev)
+    cache, kv_heads, cache_dim = cache_of(*batch)
     rows, q_heads, dim = shape = q.shape
     if dim != cache_dim:
         raise ValueError("q and the cache must have the same head_dim")
@@ -209,15 +267,91 @@ def attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pag
             raise ValueError("lse must be [rows, q_heads]")
     if rows == 0:
         return out
-    ws = _scratch(attention_workspace_bytes(rows, q_heads, kv_heads, dim, max_q_len), dev, workspace, other)
-    st = lib().q4_0_attention(q.data_ptr(), qs[0], qs[1], out.data_ptr(), _TYPES[out_dtype],
-                              lse.data_ptr() if lse is not None else None, rows, q_heads, max_q_len,
-                              dim ** -0.5 if scale is None else scale, window, sinks, cache,
-                              ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
-                              _stream_of(stream, dev))
+    ws = _scratch(_ws_bytes(entry + "_workspace_bytes", rows, q_heads, kv_heads, dim, max_q_len), dev, workspace, other)
+    st = getattr(lib(), entry)(q.data_ptr(), qs[0], qs[1], out.data_ptr(), _TYPES[out_dtype],
+                               lse.data_ptr() if lse is not None else None, rows, q_heads, max_q_len,
+                               dim ** -0.5 if scale is None else scale, window, sinks, cache,
+                               ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
+                               _stream_of(stream, dev))
     if st:
-        _check(st, "q4_0_attention")
+        _check(st, entry)
     return out
+
+
+def attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+              q_start: torch.Tensor, kv_len: torch.Tensor, *, max_q_len: int, scale: float = None, window: int = 0,
+              sinks: int = 0, out: torch.Tensor = None, out_dtype=torch.bfloat16, lse: torch.Tensor = None,
+              workspace: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """Causal attention of q [rows, q_heads, head_dim] (bf16, any strides of
+    rows and heads) over the paged cache, the rows' own tokens included:
+    [rows, q_heads, head_dim] of out_dtype (bf16 or fp32).
+
+    max_q_len: the most new tokens of a sequence.  scale: head_dim ** -0.5
+    when not given.  window, sinks: a row sees its latest `window` tokens (0:
+    all) and the first `sinks`.  lse: fp32 [rows, q_heads] to receive the
+    natural logarithms of the softmax sums."""
+    dev = torch.cuda.current_device()
+    return _attend("q4_0_attention", _cache, (k_cache, v_cache, page_table, q_start, kv_len, dev), q, max_q_len,
+                   scale, window, sinks, out, out_dtype, lse, workspace, stream, dev)
+
+
+def kv_append_q4(qkv: torch.Tensor, cos_sin: torch.Tensor, cache: KVCacheQ4, page_table: torch.Tensor,
+                 q_start: torch.Tensor, kv_len: torch.Tensor, *, q_heads: int, interleaved: bool = False,
+                 positions: torch.Tensor = None, out: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """kv_append into a cache in 4 bits: keys and values are quantised as they
+    are written.  A block of 32 elements with a NaN or one past 65504 in size
+    reads back as NaN."""
+    dev = torch.cuda.current_device()
+    return _append("q4_0_kv_append_q4", _cache_q4, (cache, page_table, q_start, kv_len, dev), qkv, cos_sin,
+                   q_heads, interleaved, positions, out, stream, dev)
+
+
+def kv_read_q4(cache: KVCacheQ4, page_table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, *, rows: int,
+               out_dtype=torch.bfloat16, out=None, stream=None):
+    """(k, v) of a batch's rows read back, each [rows, kv_heads, head_dim] of
+    out_dtype (bf16, or fp32, which is exact): row q_start[b] + i is the token
+    at position kv_len[b] - (q_start[b + 1] - q_start[b]) + i of sequence b --
+    what an append of this batch wrote, or whole sequences where q_start counts
+    all their tokens up.  rows: q_start[-1], known to the host; rows of no
+    sequence are left as they were.  out: a pair of tensors to write to."""
+    if out_dtype not in _TYPES:
+        raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
+    dev = torch.cuda.current_device()
+    packed, kv_heads, dim = _cache_q4(cache, page_table, q_start, kv_len, dev)
+    if rows < 0:
+        raise ValueError("rows must not be negative")
+    shape = (rows, kv_heads, dim)
+    if out is None:
+        other = _other(stream, dev)
+        k, v = _empty(shape, out_dtype, dev, other), _empty(shape, out_dtype, dev, other)
+    else:
+        k, v = out
+        for t, name in ((k, "out[0]"), (v, "out[1]")):
+            _plain(t, name, out_dtype, 3, dev)
+            if tuple(t.shape) != shape:
+                raise ValueError("out must be a pair of [rows, kv_heads, head_dim]")
+    if rows == 0:
+        return k, v
+    st = lib().q4_0_kv_read_q4(k.data_ptr(), v.data_ptr(), _TYPES[out_dtype], rows, packed, _stream_of(stream, dev))
+    if st:
+        _check(st, "q4_0_kv_read_q4")
+    return k, v
+
+
+def attention_q4_workspace_bytes(rows: int, q_heads: int, kv_heads: int, head_dim: int, max_q_len: int) -> int:
+    """Scratch of attention_q4 on the current device (0 for sizes it refuses)."""
+    return _ws_bytes("q4_0_attention_q4_workspace_bytes", rows, q_heads, kv_heads, head_dim, max_q_len)
+
+
+def attention_q4(q: torch.Tensor, cache: KVCacheQ4, page_table: torch.Tensor, q_start: torch.Tensor,
+                 kv_len: torch.Tensor, *, max_q_len: int, scale: float = None, window: int = 0, sinks: int = 0,
+                 out: torch.Tensor = None, out_dtype=torch.bfloat16, lse: torch.Tensor = None,
+                 workspace: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """attention over a cache in 4 bits (attention_q4_workspace_bytes is its
+    scratch)."""
+    dev = torch.cuda.current_device()
+    return _attend("q4_0_attention_q4", _cache_q4, (cache, page_table, q_start, kv_len, dev), q, max_q_len,
+                   scale, window, sinks, out, out_dtype, lse, workspace, stream, dev)
 
 
 def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, top: int = 0, stream=None):
