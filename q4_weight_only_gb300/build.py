@@ -17,7 +17,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "lib", "libq4_0.so")
 SOURCES = ["api.cu", "quantize.cu", "gemv.cu", "gemv_tc.cu", "gemm.cu", "noalloc.cu", "pad.cu", "kv_append.cu", "attention.cu",
            "logprobs.cu", "kv_q4.cu", "attention_q4.cu"]
-HEADERS = ["q4_0_internal.h", "q4_0_ptx.cuh", "attention_plan.cuh"]
+HEADERS = ["q4_0_internal.h", "q4_0_ptx.cuh", "attention_plan.cuh", "cache_q4.cuh"]
 PUBLIC_HEADER = os.path.join(os.path.dirname(HERE), "include", "q4_0.h")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -62,6 +62,7 @@
 #include <type_traits>
 
 #include "attention_plan.cuh"
+#include "cache_q4.cuh"
 #include "q4_0_internal.h"
 #include "q4_0_ptx.cuh"
 
@@ -74,7 +75,8 @@ constexpr int kThreads = 384;
 // registers a thread: the launch gives 168 each; the copy and MMA warps give
 // theirs up to the softmax warps (128 * 56 + 256 * 224 = 384 * 168)
 constexpr int kRoleRegs = 56, kSoftmaxRegs = 224;
-constexpr int kStatBytes = 2048;
+// 4 bits: warps 0, 2 and 3 unpack a tile's 32-token parts in turn
+constexpr int kUnpackers = 3, kCodeStages = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;    // log2 of the growth of a row's maximum that moves its reference
@@ -83,6 +85,9 @@ constexpr float kGrow = 8.f;    // log2 of the growth of a row's maximum that mo
 // apart at least: the next power of two in the place of c gives the same
 // p, 1 or nothing, without a rounding.
 constexpr float kHuge = 1 << 30;
+// binary16 holds less: at 2^26 the factor is at most 2^4, so p at most 2^12;
+// a score's own rounding to fp32 is up to 4 in the exponent there.
+constexpr float kHugeQ4 = 1 << 26;
 
 struct Params {
     const int32_t *page_table, *q_start, *kv_len;
@@ -104,8 +109,17 @@ struct Params {
     unsigned int *err;
 };
 
+// The same over a cache in Q4_0 blocks.
+struct ParamsQ4 : Params {
+    CacheQ4 cache;
+    int least;  // sequences of fewer (token, head of the group) rows are another kernel's
+};
+
 __device__ __forceinline__ int items_of(const Params &p, const Sequence &s) {
     return (s.len + 2 * p.tokens - 1) / (2 * p.tokens);
+}
+__device__ __forceinline__ int items_of(const ParamsQ4 &p, const Sequence &s) {
+    return s.len * p.group < p.least ? 0 : items_of(static_cast<const Params &>(p), s);
 }
 
 // The tokens the queries of an item see: [0, sink_end) and [lo, hi), and the
@@ -160,25 +174,28 @@ __device__ __forceinline__ void each_step(F &&f) {
     }
 }
 
-template <int D>
+template <int D, bool kQ4>
 struct Layout {
     static constexpr int kHalves = D / 64;                 // 64-element column blocks
     static constexpr int kTileBytes = kTile * D * 2;
     static constexpr int kBlock = kTile * 128;             // bytes of one column block
-    static constexpr int kStages = D == 128 ? 5 : 10;      // K or V tiles in the ring
+    static constexpr int kStages = (D == 128 ? 5 : 10) - (kQ4 ? 1 : 0);  // K or V tiles in the ring
     static constexpr int kQTiles = D == 128 ? 2 : 4;       // Q tiles held
     static constexpr int kQ = 0;
     static constexpr int kRing = kQTiles * kTileBytes;
-    static constexpr int kBars = kRing + kStages * kTileBytes;
+    // 4 bits: codes and scales of 32 tokens, a few of each unpacking warp
+    static constexpr int kCodes = kRing + kStages * kTileBytes;
+    static constexpr int kCodeRow = D / 2, kScaleRow = D / 16, kCodeBytes = 32 * (kCodeRow + kScaleRow);
+    static constexpr int kBars = kCodes + (kQ4 ? kUnpackers * kCodeStages * kCodeBytes : 0);
+    static constexpr int kStatBytes = kQ4 ? 3072 : 2048;
     static constexpr int kSmem = kBars + kStatBytes + 1024;  // + alignment
 };
 
 constexpr int kItems = 4;     // items handed out ahead
-constexpr int kReaders = 11;  // warps that read them
 
 constexpr int kMaxQTiles = 4;
 
-template <int kStages>
+template <int kStages, bool kQ4>
 struct Bars {
     uint64_t full[kStages], empty[kStages];
     uint64_t q_full[kMaxQTiles], q_empty[kMaxQTiles];
@@ -188,41 +205,78 @@ struct Bars {
     uint64_t drain;
     Item item[kItems];
     float2 ml[kTile];
+    // 4 bits: Q tiles turned to binary16, and what a narrow item's rows were
+    // scaled by, for group B
+    uint64_t q_ready[kQ4 ? kMaxQTiles : 1];
+    float q_down[kQ4 ? kTile : 1];
     uint32_t tmem;
     uint32_t fills[2], q_fills;  // copies made: past the last K and V tile's ring position, and of Q
     int abort;
     Start<kThreads> start;
 };
-static_assert(sizeof(Bars<10>) <= kStatBytes, "");
+static_assert(sizeof(Bars<10, false>) <= Layout<64, false>::kStatBytes, "");
+static_assert(sizeof(Bars<9, true>) <= Layout<64, true>::kStatBytes, "");
 
 // Tensor memory columns.
 constexpr uint32_t kTmemCols = 512;
 __device__ __forceinline__ uint32_t col_s(int g) { return g * 128; }
 __device__ __forceinline__ uint32_t col_o(int g) { return 256 + g * 128; }
 
+// A row of a Q tile to binary16 in place, times a power of two that brings its
+// largest element to [2^14, 2^15): exact for every element within 2^29 of the
+// largest, off by at most 2^-39 of that below.  Returns the power's inverse; a
+// row of zeros or with an infinity or NaN is not scaled.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
-    attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                     const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Params p) {
-    using L = Layout<D>;
+__device__ __forceinline__ float q_to_f16(uint8_t *tile, int block, int row) {
+    uint4 v[D / 8];
+    uint32_t top2 = 0;  // as whole numbers, sizes of bfloat16 pairs are ordered
+    auto at = [&](int i) {
+        return reinterpret_cast<uint4 *>(tile + (i >> 3) * block + row * 128 + (((i & 7) ^ (row & 7)) << 4));
+    };
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+        v[i] = *at(i);
+        top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
+                                       __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu)));
+    }
+    const uint32_t top = max(top2 & 0xFFFFu, top2 >> 16);
+    const int exponent = (int)(top >> 7);
+    const int up = top && exponent < 255 ? min(14 + 127 - exponent, 100) : 0;
+    const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+    auto turn = [&](uint32_t w) {
+        return pack_f16(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
+    };
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) *at(i) = make_uint4(turn(v[i].x), turn(v[i].y), turn(v[i].z), turn(v[i].w));
+    return __uint_as_float((uint32_t)(127 - up) << 23);
+}
+
+// kmap, vmap: of a bfloat16 cache.  P: Params, or ParamsQ4 for a cache in 4
+// bits, whose codes warps 0, 2 and 3 unpack into the ring's tiles.
+template <int D, typename P>
+__device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMap *kmap, const CUtensorMap *vmap,
+                                       const P &p) {
+    constexpr bool kQ4 = std::is_same<P, ParamsQ4>::value;
+    using L = Layout<D, kQ4>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
     uint8_t *ring = smem + L::kRing;
     constexpr int kStages = L::kStages;
-    Bars<kStages> &bar = *reinterpret_cast<Bars<kStages> *>(smem + L::kBars);
+    Bars<kStages, kQ4> &bar = *reinterpret_cast<Bars<kStages, kQ4> *>(smem + L::kBars);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int *abort_flag = &bar.abort;
 
     if (warp == 1) tmem_alloc(&bar.tmem, kTmemCols);
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&bar.full[i], 1);
+            mbar_init(&bar.full[i], kQ4 ? kTile / 32 : 1);
             mbar_init(&bar.empty[i], 1);
         }
         for (int i = 0; i < L::kQTiles; ++i) {
             mbar_init(&bar.q_full[i], 1);
             mbar_init(&bar.q_empty[i], 1);
+            if (kQ4) mbar_init(&bar.q_ready[i], 4);
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(&bar.s_full[g], 1);
@@ -233,14 +287,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&bar.merged, 4);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&bar.item_full[i], 1);
-            mbar_init(&bar.item_empty[i], kReaders);
+            mbar_init(&bar.item_empty[i], kQ4 ? 12 : 11);  // warps that read items
         }
         mbar_init(&bar.drain, 1);
         bar.abort = 0;
         mbar_fence_init();
         tma_prefetch_desc(&qmap);
-        tma_prefetch_desc(&kmap);
-        tma_prefetch_desc(&vmap);
+        if (!kQ4) {
+            tma_prefetch_desc(kmap);
+            tma_prefetch_desc(vmap);
+        }
     }
     pdl_launch_dependents();
     pdl_wait();
@@ -266,9 +322,230 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++items;
     };
 
+    // Warp 3 hands out the items.
+    struct Publisher {
+        int64_t left;
+        int flags, head, b, it, t0, n_items;
+        uint32_t count;
+        int4 tail;
+        Sequence s;
+    };
+    auto publisher = [&]() {
+        return Publisher{bar.start.left, 0, bar.start.head, bar.start.b, bar.start.item, bar.start.t0,
+                         items_of(p, bar.start.s), 0, make_int4(0, 0, 0, 0), bar.start.s};
+    };
+    // The next one, or one without tiles at the share's end; false after that
+    // and when a wait was abandoned.
+    auto publish = [&](Publisher &w) {
+        Item o{};
+        int64_t cost = 0;
+        if (w.left > 0) {
+            const Range r = item_range(p, w.s, w.it);
+            const int each = tile_cost(p, r);
+            cost = (int64_t)r.n * each;
+            o.t0 = w.t0, o.t1 = w.left >= cost ? r.n : (int)(w.left / each), o.n = r.n;
+            o.head = w.head, o.b = w.b, o.row0 = w.s.row0 + w.it * 2 * p.tokens, o.tokens = r.tokens, o.pos0 = r.pos0;
+            o.lo = r.lo, o.hi = r.hi, o.sink_end = r.sink_end, o.sink_tiles = r.sink_tiles, o.wtile = r.wtile;
+            if (o.t0 > 0) w.flags |= kHeadPiece | (o.t1 < o.n ? kHeadGoesOn : 0);
+            if (o.t0 == 0 && o.t1 > 0 && o.t1 < o.n)
+                w.flags |= kTailPiece, w.tail = make_int4(0, o.row0, o.tokens, w.head);
+        }
+        const int i = w.count % kItems;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bar.item_empty[i], (w.count / kItems & 1) ^ 1, abort_flag, p.err)))
+            return false;
+        if (lane == 0) {
+            bar.item[i] = o;
+            mbar_arrive(&bar.item_full[i]);
+        }
+        __syncwarp();
+        ++w.count;
+        w.left -= cost;
+        if (o.t0 == o.t1) return false;
+        w.t0 = 0;
+        if (w.left > 0 && ++w.it >= w.n_items) {
+            w.it = 0;
+            int scanned = 0;
+            do {
+                if (++w.b >= p.sequences) {
+                    w.b = 0;
+                    ++w.head;
+                }
+                w.s = sequence(p, w.b);
+                w.n_items = items_of(p, w.s);
+            } while (w.n_items == 0 && ++scanned <= p.sequences);
+        }
+        return true;
+    };
+    auto publish_end = [&](Publisher &w) {
+        w.tail.x = w.flags;
+        if (lane == 0) p.record[blockIdx.x] = w.tail;
+    };
+    // A tile of Q into its slot, when there is room.
+    auto load_q = [&](uint32_t q, int head, int row0) {
+        const int at = q % L::kQTiles;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bar.q_empty[at], (q / L::kQTiles & 1) ^ 1, abort_flag, p.err)))
+            return false;
+        if (elect_one()) {
+            mbar_arrive_expect_tx(&bar.q_full[at], L::kHalves * p.tokens * p.group * 128);
+            for (int h = 0; h < L::kHalves; ++h)
+                tma_load_4d(smem + L::kQ + at * L::kTileBytes + h * L::kBlock, &qmap, h * 64, 0, head, row0,
+                            &bar.q_full[at]);
+        }
+        __syncwarp();
+        return true;
+    };
+
+    // 4 bits.  A tile is unpacked in four parts of 32 tokens; part number n of
+    // the share (fill n / 4 of the ring) is warp n mod 3's.  The codes come by
+    // asynchronous copies, two parts ahead, and their page numbers one part
+    // before that.
+    auto unpack = [&]() {
+        if constexpr (kQ4) {
+            const int me = warp ? warp - 1 : 0;  // warps 0, 2, 3
+            const KvQ4View &c = p.cache.c;
+            const uint32_t stages = smem_u32(smem + L::kCodes) + me * (kCodeStages * L::kCodeBytes);
+            Publisher w{};
+            bool publishing = me == 2;
+            if (publishing) {
+                w = publisher();
+                publishing = publish(w);
+            }
+            // the part to be copied next, and the parts of its item
+            uint32_t part = me, begin = 0, end = 0;
+            bool open = false, ended = false;
+            int kv = 0, page = 0, off = 0, head = 0;
+            bool seen = false;
+            auto look = [&]() {
+                while (part >= end) {
+                    if (open) done_item();
+                    open = next_item();
+                    if (!open) {
+                        ended = true;
+                        return;
+                    }
+                    begin = end, end += 8 * (cur.t1 - cur.t0);
+                    if (publishing) publishing = publish(w);
+                }
+                const int local = (int)(part - begin);
+                kv = local >> 2 & 1, head = cur.head;
+                const int token = cur.key_tile(cur.t0 + (local >> 3)) * kTile + (local & 3) * 32 + lane;
+                seen = token < cur.sink_end || (token >= cur.lo && token < cur.hi);
+                const int index = __umulhi((uint32_t)token, p.cache.page_magic) >> p.cache.page_shift;
+                if (seen) page = p.page_table[(int64_t)cur.b * p.table_stride + index];
+                off = token - index * p.page_size;
+                part += kUnpackers;
+            };
+            uint32_t stage = 0;
+            auto copy_next = [&]() {
+                if (!ended) {
+                    if (seen && (page < 0 || page >= p.pages)) {
+                        report_index(p.err);
+                        seen = false;
+                    }
+                    if (!seen) page = off = 0;
+                    const uint32_t all_seen = __ballot_sync(0xffffffffu, seen), to = stages + stage * L::kCodeBytes;
+                    const int64_t *st = kv ? c.v_stride : c.k_stride, *ss = kv ? c.v_scale_stride : c.k_scale_stride;
+                    const uint64_t row =
+                        reinterpret_cast<uint64_t>((kv ? c.v : c.k) + page * st[0] + head * st[1] + off * st[2]);
+                    constexpr int kChunks = L::kCodeRow / 16, kAtOnce = 32 / kChunks;
+                    const int chunk = lane % kChunks;
+#pragma unroll
+                    for (int j = 0; j < 32 / kAtOnce; ++j) {
+                        const int tok = j * kAtOnce + lane / kChunks;
+                        const uint64_t from = __shfl_sync(0xffffffffu, row, tok);
+                        copy16(to + tok * L::kCodeRow + (chunk ^ (D == 128 ? tok >> 1 & 3 : tok >> 2 & 1)) * 16,
+                               reinterpret_cast<const void *>(from + chunk * 16), all_seen >> tok & 1 ? 16 : 0);
+                    }
+                    copy_small<L::kScaleRow>(to + 32 * L::kCodeRow + lane * L::kScaleRow,
+                                             (kv ? c.v_scale : c.k_scale) + page * ss[0] + head * ss[1] + off * ss[2],
+                                             seen ? L::kScaleRow : 0);
+                    look();
+                }
+                copy_commit();
+                stage = stage + 1 == kCodeStages ? 0 : stage + 1;
+            };
+            look();
+#pragma unroll
+            for (int i = 0; i < kCodeStages - 1; ++i) copy_next();
+            uint32_t from = 0;
+            // warp 3 loads an item's Q after its parts of the first K tile
+            // (Q waits for room).  The item's record stays until the softmax
+            // warps have had that Q.
+            uint32_t q = 0, q_item = 0, q_part = 0;
+            const uint32_t bias = p.cache.bias;
+            for (uint32_t n = me;; n += kUnpackers) {
+                const bool all_copied = ended;
+                copy_next();
+                if (all_copied && n >= end) break;
+                copy_wait<kCodeStages - 1>();
+                __syncwarp();
+                const uint32_t fill = n >> 2, slot = fill % kStages;
+                if (!__all_sync(0xffffffffu, mbar_wait(&bar.empty[slot], (fill / kStages & 1) ^ 1, abort_flag, p.err)))
+                    break;
+                const uint32_t src = stages + from * L::kCodeBytes;
+                const int row = (n & 3) * 32 + lane;
+                uint32_t d[2];
+                if (D == 128) {
+                    const uint2 x = lds64(src + 32 * L::kCodeRow + lane * 8);
+                    d[0] = x.x, d[1] = x.y;
+                } else {
+                    d[0] = d[1] = lds32(src + 32 * L::kCodeRow + lane * 4);
+                }
+                const uint32_t dst = smem_u32(ring) + slot * L::kTileBytes + row * 128;
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j) {
+                    const uint4 x =
+                        lds128(src + lane * L::kCodeRow + (j ^ (D == 128 ? lane >> 1 & 3 : lane >> 2 & 1)) * 16);
+                    const __half2 e = as_half2(d[j / 2]);
+                    const __half2 scale = j & 1 ? __high2half2(e) : __low2half2(e);
+                    const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        // eight bytes: elements 8h .. 8h + 7 of the block and 16 further
+                        uint32_t lo[4], hi[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t t = __byte_perm(words[2 * h + i / 2], 0, i & 1 ? 0x4342 : 0x4140);
+                            lo[i] = times(low_codes(t, bias), scale), hi[i] = times(high_codes(t, bias), scale);
+                        }
+                        const uint32_t at = dst + (j >> 1) * L::kBlock;
+                        const int first = (j & 1) * 4 + h;
+                        sts128(at + ((first ^ (row & 7)) * 16), lo);
+                        sts128(at + (((first + 2) ^ (row & 7)) * 16), hi);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.full[slot]);
+                from = from + 1 == kCodeStages ? 0 : from + 1;
+                if (me == 2 && n >= q_part) {
+                    const Item &o = bar.item[q_item++ % kItems];
+                    const int q_head = o.head;
+                    int q_row = o.row0, tokens = o.tokens;
+                    q_part += 8 * (o.t1 - o.t0);
+                    bool ok = true;
+                    for (; ok && tokens > 0; tokens -= p.tokens, q_row += p.tokens) {
+                        ok = load_q(q, q_head, q_row);
+                        q += ok;
+                    }
+                    if (!ok) break;
+                }
+            }
+            copy_wait<0>();
+            if (me == 2) {
+                publish_end(w);
+                if (lane == 0) bar.q_fills = q;
+            } else if (lane == 0) {
+                bar.fills[me] = 0;  // no copies of theirs are on barriers
+            }
+        }
+    };
+
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
-        if (warp == 0 || warp == 2) {
+        if (kQ4 && warp != 1) {
+            unpack();
+        } else if (!kQ4 && (warp == 0 || warp == 2)) {
             // ------------------------------------------------ copies
             // K and V tiles alternate in one ring; each warp fills its own.
             // A warp may not be two uses of a slot ahead (its wait would take
@@ -276,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // order in which the slot of fill f - 7, waited for at fill
             // f - 2, is freed after that of f - 10.
             const int kv = warp >> 1;  // warp 0: Q and K, warp 2: V
-            const CUtensorMap *map = kv ? &vmap : &kmap;
+            const CUtensorMap *map = kv ? vmap : kmap;
             uint32_t fill = kv;        // ring position of the next tile
             uint32_t slot = kv, phase = 1;
             bool ok = true;
@@ -349,17 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (slot >= kStages) slot -= kStages, phase ^= 1;
                     // an item's Q after its first K tile: Q waits for room
                     for (; kv == 0 && now.tokens > 0; now.tokens -= p.tokens, now.row0 += p.tokens) {
-                        const int at = q % L::kQTiles;
-                        ok = __all_sync(0xffffffffu, mbar_wait(&bar.q_empty[at], (q / L::kQTiles & 1) ^ 1, abort_flag,
-                                                               p.err));
+                        ok = load_q(q, now.head, now.row0);
                         if (!ok) break;
-                        if (elect_one()) {
-                            mbar_arrive_expect_tx(&bar.q_full[at], L::kHalves * p.tokens * p.group * 128);
-                            for (int h = 0; h < L::kHalves; ++h)
-                                tma_load_4d(smem + L::kQ + at * L::kTileBytes + h * L::kBlock, &qmap, h * 64, 0,
-                                            now.head, now.row0, &bar.q_full[at]);
-                        }
-                        __syncwarp();
                         ++q;
                     }
                     if (!ok) break;
@@ -370,59 +638,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bar.fills[kv] = fill;
                 if (kv == 0) bar.q_fills = q;
             }
-        } else if (warp == 3) {
+        } else if (!kQ4 && warp == 3) {
             // ------------------------------------------------- items
-            int flags = 0;
-            int4 tail = make_int4(0, 0, 0, 0);
-            int64_t left = bar.start.left;
-            int head = bar.start.head, b = bar.start.b, it = bar.start.item, t0 = bar.start.t0;
-            Sequence s = bar.start.s;
-            int n_items = items_of(p, s);
-            for (;; ++items) {
-                Item o{};
-                int64_t cost = 0;
-                if (left > 0) {
-                    const Range r = item_range(p, s, it);
-                    const int each = tile_cost(p, r);
-                    cost = (int64_t)r.n * each;
-                    o.t0 = t0, o.t1 = left >= cost ? r.n : (int)(left / each), o.n = r.n;
-                    o.head = head, o.b = b, o.row0 = s.row0 + it * 2 * p.tokens, o.tokens = r.tokens, o.pos0 = r.pos0;
-                    o.lo = r.lo, o.hi = r.hi, o.sink_end = r.sink_end, o.sink_tiles = r.sink_tiles, o.wtile = r.wtile;
-                    if (o.t0 > 0) flags |= kHeadPiece | (o.t1 < o.n ? kHeadGoesOn : 0);
-                    if (o.t0 == 0 && o.t1 > 0 && o.t1 < o.n)
-                        flags |= kTailPiece, tail = make_int4(0, o.row0, o.tokens, head);
-                }
-                const int i = items % kItems;
-                if (!__all_sync(0xffffffffu,
-                                mbar_wait(&bar.item_empty[i], (items / kItems & 1) ^ 1, abort_flag, p.err)))
-                    break;
-                if (lane == 0) {
-                    bar.item[i] = o;
-                    mbar_arrive(&bar.item_full[i]);
-                }
-                __syncwarp();
-                left -= cost;
-                if (o.t0 == o.t1) break;
-                t0 = 0;
-                if (left > 0 && ++it >= n_items) {
-                    it = 0;
-                    int scanned = 0;
-                    do {
-                        if (++b >= p.sequences) {
-                            b = 0;
-                            ++head;
-                        }
-                        s = sequence(p, b);
-                    } while (s.len == 0 && ++scanned <= p.sequences);
-                    n_items = items_of(p, s);
-                }
+            Publisher w = publisher();
+            while (publish(w)) {
             }
-            tail.x = flags;
-            if (lane == 0) p.record[blockIdx.x] = tail;
+            publish_end(w);
         } else if (warp == 1) {
         // ------------------------------------------------------ MMAs
-        constexpr uint32_t idesc_qk = idesc_bf16_f32(kTile, kTile, false);
-        constexpr uint32_t idesc_pv = idesc_bf16_f32(kTile, D, true);
+        constexpr uint32_t idesc_qk = kQ4 ? idesc_f16_f32(kTile, kTile) : idesc_bf16_f32(kTile, kTile, false);
+        constexpr uint32_t idesc_pv = kQ4 ? idesc_f16_f32(kTile, D, true) : idesc_bf16_f32(kTile, D, true);
         uint32_t fills = 0;  // ring position of the next K tile
         uint32_t q = 0;      // Q tiles of earlier items
         uint32_t p_phase[2] = {0, 0};
@@ -450,7 +675,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(&bar.s_full[g]);
             if (last) mma_commit(&bar.q_empty[qt]);
         };
-        auto q_full = [&](uint32_t qt) { return wait(&bar.q_full[qt % L::kQTiles], qt / L::kQTiles & 1); };
+        auto q_full = [&](uint32_t qt) {
+            return wait(kQ4 ? &bar.q_ready[qt % L::kQTiles] : &bar.q_full[qt % L::kQTiles], qt / L::kQTiles & 1);
+        };
         // O_g (+)= P_g V (one elected thread)
         auto values = [&](int g, uint32_t slot, bool first) {
             const uint32_t a = tmem + col_s(g), b = v_lo + slot * kTileStep, d = tmem + col_o(g);
@@ -472,7 +699,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // Boxes that no query sees were filled with zeros; what remains are
         // the unseen ends of the boxes that hold the ends of the seen ranges.
+        // (4 bits: they were unpacked as zeros.)
         auto clear_unseen = [&](int t, int slot) {
+            if (kQ4) return;
             const int tok0 = cur.key_tile(t) * kTile;
             const int sink = cur.sink_end - tok0, lo = cur.lo - tok0, hi = cur.hi - tok0;
             if (hi >= kTile && (lo <= 0 || sink >= kTile)) return;
@@ -579,8 +808,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const uint32_t ts = tmem + lanes + col_s(g), to = tmem + lanes + col_o(g);
         const int my_token = row / p.group, my_head = row - my_token * p.group;
-        const float c = p.scale_log2;
-        uint32_t s_phase = 0, o_phase = 0;
+        float c = p.scale_log2, c_pow2 = p.scale_pow2;
+        uint32_t s_phase = 0, o_phase = 0, q_tiles = 0;
         bool ok = true;
         auto wait = [&](uint64_t *b, uint32_t parity) {
             ok = __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag, p.err));
@@ -599,6 +828,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pos_a = cur.pos0 + half * p.tokens;
             const int pos_z = cur.pos0 + min((half + 1) * p.tokens, cur.tokens) - 1;
             const int step = wide ? 1 : 2;
+            if constexpr (kQ4) {
+                // the group's tile of Q to binary16; a narrow item's is group
+                // A's, which tells B what its rows were scaled by
+                const uint32_t qt = q_tiles + half, at = qt % L::kQTiles, parity = qt / L::kQTiles & 1;
+                q_tiles += wide ? 2 : 1;
+                float down = 1.f;
+                if (wide || g == 0) {
+                    if (!wait(&bar.q_full[at], parity)) break;
+                    if (valid) down = q_to_f16<D>(smem + L::kQ + at * L::kTileBytes, L::kBlock, row);
+                    if (!wide) bar.q_down[row] = down;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.q_ready[at]);
+                } else {
+                    if (!wait(&bar.q_ready[at], parity)) break;
+                    down = bar.q_down[row];
+                }
+                c = fminf(p.scale_log2 * down, 3e38f), c_pow2 = fminf(p.scale_pow2 * down, 3e38f);
+            }
             // A row whose maximum grew moves the references of its warp's
             // rows (each its own, one by one, took prompts 1 to 4 % longer).
             // Lanes that are no row of the item must not: they hold other
@@ -641,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
                     // (nothing is above an infinite reference)
                     if (__any_sync(0xffffffffu, fmaf(top, c_row, -mc) > kGrow)) {
-                        const float c_top = fabsf(top * c) > kHuge ? p.scale_pow2 : c;
+                        const float c_top = fabsf(top * c) > (kQ4 ? kHugeQ4 : kHuge) ? c_pow2 : c;
                         const float mc_new = __fmul_rn(top, c_top);
                         const bool above = mc_new > mc;
                         const float f = mc == -INFINITY ? 0.f : above ? ex2(mc - mc_new) : 1.f;
@@ -675,7 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             unpack2(fma2(s2, c2, mc2), a, b);
                             a = ex2(a), b = ex2(b);
                             sum[e & 3] = add2(sum[e & 3], pack2(a, b));
-                            w[e] = pack_bf16(a, b);
+                            w[e] = kQ4 ? pack_f16(a, b) : pack_bf16(a, b);
                         }
                         tmem_st16(ts + q * 16, w);
                     }
@@ -793,6 +1041,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_drain(&bar.q_full[f % L::kQTiles], f / L::kQTiles & 1);
     }
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Params p) {
+    attend<D>(qmap, &kmap, &vmap, p);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_q4_wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ ParamsQ4 p) {
+    attend<D>(qmap, nullptr, nullptr, p);
 }
 
 // Adds the pieces of the items that a share's boundary cut.  blockIdx.x: the
@@ -915,12 +1176,9 @@ struct WorkspaceLayout {
     }
 };
 
-template <int D>
-cudaError_t launch_d(const AttentionArgs &a, const KvCacheView &c, void *workspace, int ctas, cudaStream_t s,
-                     unsigned int *err) {
-    EncodeTiledFn enc = encode_fn();
-    if (!enc) return cudaErrorNotSupported;
-    Params p{};
+// What the kernels of both caches take; View: KvCacheView or KvQ4View.
+template <int D, typename View>
+void fill_params(Params &p, const AttentionArgs &a, const View &c, void *workspace, int ctas, unsigned int *err) {
     p.page_table = c.page_table, p.q_start = c.q_start, p.kv_len = c.kv_len, p.table_stride = c.table_stride;
     p.sequences = c.sequences, p.table_width = c.table_width, p.pages = c.pages, p.page_size = c.page_size;
     p.rows = a.rows, p.q_heads = a.q_heads, p.kv_heads = c.kv_heads, p.group = a.q_heads / c.kv_heads;
@@ -947,23 +1205,61 @@ cudaError_t launch_d(const AttentionArgs &a, const KvCacheView &c, void *workspa
     p.part_ml = reinterpret_cast<float2 *>(ws + w.ml_off);
     p.record = reinterpret_cast<int4 *>(ws + w.rec_off);
     p.err = err;
+}
+
+// q as {element, head of the group, key head, row}
+template <int D>
+bool make_q_map(EncodeTiledFn enc, CUtensorMap *map, const AttentionArgs &a, const Params &p) {
+    return make_map(enc, map, a.q, {D, p.group, p.kv_heads, a.rows},
+                    {a.q_head_stride, a.q_head_stride * p.group, a.q_row_stride}, p.group, p.tokens);
+}
+
+template <int D>
+cudaError_t launch_join(const Params &p, int ctas, cudaStream_t s) {
+    const int blocks = (p.piece_rows + 7) / 8;  // a row a warp; past 8 blocks an item is slower (32: by 3 us)
+    return launch_pdl(attention_join_kernel<D>, dim3(ctas, blocks < 8 ? blocks : 8), dim3(256), 0, s, p, ctas);
+}
+
+template <int D>
+cudaError_t launch_d(const AttentionArgs &a, const KvCacheView &c, void *workspace, int ctas, cudaStream_t s,
+                     unsigned int *err) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    Params p{};
+    fill_params<D>(p, a, c, workspace, ctas, err);
     CUtensorMap qmap, kmap, vmap;
-    // q as {element, head of the group, key head, row}
-    if (!make_map(enc, &qmap, a.q, {D, p.group, p.kv_heads, a.rows},
-                  {a.q_head_stride, a.q_head_stride * p.group, a.q_row_stride}, p.group, p.tokens))
-        return cudaErrorInvalidValue;
+    if (!make_q_map<D>(enc, &qmap, a, p)) return cudaErrorInvalidValue;
     // k and v as {element, token of the page, key head, page}
     if (!make_map(enc, &kmap, c.k, {D, c.page_size, c.kv_heads, c.pages},
                   {c.k_stride[2], c.k_stride[1], c.k_stride[0]}, p.box, 1) ||
         !make_map(enc, &vmap, c.v, {D, c.page_size, c.kv_heads, c.pages},
                   {c.v_stride[2], c.v_stride[1], c.v_stride[0]}, p.box, 1))
         return cudaErrorInvalidValue;
-    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(attention_kernel<D>), Layout<D>::kSmem);
+    constexpr int kSmem = Layout<D, false>::kSmem;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(attention_kernel<D>), kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(attention_kernel<D>, dim3(ctas), dim3(kThreads), Layout<D>::kSmem, s, qmap, kmap, vmap, p);
+    e = launch_pdl(attention_kernel<D>, dim3(ctas), dim3(kThreads), kSmem, s, qmap, kmap, vmap, p);
     if (e != cudaSuccess) return e;
-    const int blocks = (p.piece_rows + 7) / 8;  // a row a warp; past 8 blocks an item is slower (32: by 3 us)
-    return launch_pdl(attention_join_kernel<D>, dim3(ctas, blocks < 8 ? blocks : 8), dim3(256), 0, s, p, ctas);
+    return launch_join<D>(p, ctas, s);
+}
+
+template <int D>
+cudaError_t launch_q4_d(const AttentionArgs &a, const KvQ4View &c, int least, void *workspace, int ctas, cudaStream_t s,
+                        unsigned int *err) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    ParamsQ4 p{};
+    fill_params<D>(p, a, c, workspace, ctas, err);
+    p.cache = cache_q4(c);
+    p.least = least;
+    CUtensorMap qmap;
+    if (!make_q_map<D>(enc, &qmap, a, p)) return cudaErrorInvalidValue;
+    constexpr int kSmem = Layout<D, true>::kSmem;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(attention_q4_wide_kernel<D>), kSmem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(attention_q4_wide_kernel<D>, dim3(ctas), dim3(kThreads), kSmem, s, qmap, p);
+    if (e != cudaSuccess) return e;
+    return launch_join<D>(p, ctas, s);
 }
 
 }  // namespace
@@ -978,6 +1274,14 @@ cudaError_t launch_attention(const AttentionArgs &a, const KvCacheView &c, void 
     if (sms < 1) return cudaErrorInvalidDevice;
     return c.head_dim == 128 ? launch_d<128>(a, c, workspace, sms, s, err)
                              : launch_d<64>(a, c, workspace, sms, s, err);
+}
+
+cudaError_t launch_attention_q4_wide(const AttentionArgs &a, const KvQ4View &c, int least, void *workspace,
+                                     cudaStream_t s, unsigned int *err) {
+    const int sms = current_sms();
+    if (sms < 1) return cudaErrorInvalidDevice;
+    return c.head_dim == 128 ? launch_q4_d<128>(a, c, least, workspace, sms, s, err)
+                             : launch_q4_d<64>(a, c, least, workspace, sms, s, err);
 }
 
 }  // namespace q4_0

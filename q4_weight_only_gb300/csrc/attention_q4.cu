@@ -26,6 +26,7 @@
 #include <cmath>
 
 #include "attention_plan.cuh"
+#include "cache_q4.cuh"
 #include "q4_0_internal.h"
 #include "q4_0_ptx.cuh"
 
@@ -39,13 +40,13 @@ constexpr float kGrow = 8.f;  // log2 of the growth of a row's maximum that move
 constexpr int kStep = 32;     // keys a warp takes at a time
 
 struct Params {
-    KvQ4View c;
+    CacheQ4 cache;
     // the batch, as sequence() reads it
     const int32_t *page_table, *q_start, *kv_len;
     int64_t table_stride;
     int sequences, table_width, pages, page_size, rows, max_q_len;
-    uint32_t page_magic, page_shift;  // t / page_size = umulhi(t, magic) >> shift, t < 2^31
     int q_heads, kv_heads, group, window, sinks;
+    int most_rows;  // of a sequence; longer ones are another kernel's
     int item_rows;  // rows of an item: (token, head of the group) pairs of a sequence, in order
     const __nv_bfloat16 *q;
     int64_t q_row_stride, q_head_stride;
@@ -60,7 +61,7 @@ struct Params {
 };
 
 __device__ __forceinline__ int items_of(const Params &p, const Sequence &s) {
-    return (s.len * p.group + p.item_rows - 1) / p.item_rows;
+    return s.len * p.group > p.most_rows ? 0 : (s.len * p.group + p.item_rows - 1) / p.item_rows;
 }
 
 // The tokens the rows of an item see: [0, sink_end) and [lo, hi), and the
@@ -99,7 +100,7 @@ __device__ __forceinline__ int64_t item_cost(const Params &p, const Sequence &s,
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -112,53 +113,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-
-// Asynchronous copies of 16, 8 or 4 bytes; nothing is read and zeros are
-// written where `bytes` is 0.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-template <int kBytes>
-__device__ __forceinline__ void copy_small(uint32_t dst, const void *src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
-}
-
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-    uint16_t v;
-    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<__half2 *>(&v); }
-__device__ __forceinline__ uint32_t as_bits(__half2 v) { return *reinterpret_cast<uint32_t *>(&v); }
-
-// The codes less 8 of the low nibbles of a word's bytes 0 and 2, and of their
-// high nibbles, as binary16 pairs: a nibble in the mantissa of 1024 makes 1024
-// + code, or 1024 + 16 code four bits higher; both steps are exact.  `bias`
-// holds kNibbleBias.
-__device__ __forceinline__ uint32_t low_codes(uint32_t w, uint32_t bias) {
-    return as_bits(__hsub2(as_half2(and_or<0x000F000Fu>(w, bias)), __half2half2(__ushort_as_half(0x6408))));
-}
-__device__ __forceinline__ uint32_t high_codes(uint32_t w, uint32_t bias) {
-    return as_bits(__hfma2(as_half2(and_or<0x00F000F0u>(w, bias)), __half2half2(__ushort_as_half(0x2C00)),
-                           __half2half2(__ushort_as_half(0xD480))));
-}
-__device__ __forceinline__ uint32_t times(uint32_t a, __half2 b) { return as_bits(__hmul2(as_half2(a), b)); }
 
 // --------------------------------------------------------------- the kernel
 
@@ -198,7 +152,7 @@ __device__ __forceinline__ int tile_token(int i) { return (i & 8) + (i >> 1 & 3)
 // keys of an item's piece with a reference, sum and O of its own, through a
 // ring of its own: no barrier but the merge at the piece's end.
 template <int D, int NT, int W>
-__global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_constant__ Params p, uint32_t bias) {
+__global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_constant__ Params p) {
     using N = Narrow<D, NT, W>;
     using S = Stage<D>;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -207,7 +161,7 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
     __shared__ float4 row_mlc[N::kRows];
     constexpr int NB = N::kBlocks, MT = N::kTiles, kStages = N::kStages;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const uint32_t ring = smem_u32(smem) + warp * (kStages * S::kBytes);
+    const uint32_t bias = p.cache.bias, ring = smem_u32(smem) + warp * (kStages * S::kBytes);
     float *merged = reinterpret_cast<float *>(smem + N::kOut);
 
     pdl_launch_dependents();
@@ -229,9 +183,10 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
             flags |= kTailPiece, tail = make_int4(0, s.row0 * p.group + r.row0, r.rows, head);
 
         // ------------------------------------------------------ copies
-        const uint8_t *k_base = p.c.k + head * p.c.k_stride[1], *v_base = p.c.v + head * p.c.v_stride[1];
-        const uint16_t *ks_base = p.c.k_scale + head * p.c.k_scale_stride[1];
-        const uint16_t *vs_base = p.c.v_scale + head * p.c.v_scale_stride[1];
+        const KvQ4View &c = p.cache.c;
+        const uint8_t *k_base = c.k + head * c.k_stride[1], *v_base = c.v + head * c.v_stride[1];
+        const uint16_t *ks_base = c.k_scale + head * c.k_scale_stride[1];
+        const uint16_t *vs_base = c.v_scale + head * c.v_scale_stride[1];
         const int32_t *table = p.page_table + (int64_t)b * p.table_stride;
         // Step t0 + i of the piece into stage i / W of the warp's ring; a
         // token no row of the item sees, or without a page, becomes zeros.
@@ -240,18 +195,10 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
                 const uint32_t st = ring + (i / W) % kStages * S::kBytes;
                 const int token = r.step(t0 + i) * kStep + lane;
                 bool seen = token < r.sink_end || (token >= r.lo && token < r.hi);
-                int page = 0, off = 0;
-                if (seen) {
-                    const int index = __umulhi((uint32_t)token, p.page_magic) >> p.page_shift;
-                    page = table[index], off = token - index * p.page_size;
-                    if (page < 0 || page >= p.pages) {
-                        report_index(p.err);
-                        seen = false, page = 0, off = 0;
-                    }
-                }
+                const Slot at = slot_of(p.cache, table, token, seen, p.err);
                 const uint32_t all_seen = __ballot_sync(0xffffffffu, seen);
-                const uint64_t k = reinterpret_cast<uint64_t>(k_base + page * p.c.k_stride[0] + off * p.c.k_stride[2]);
-                const uint64_t v = reinterpret_cast<uint64_t>(v_base + page * p.c.v_stride[0] + off * p.c.v_stride[2]);
+                const uint64_t k = reinterpret_cast<uint64_t>(k_base + at.page * c.k_stride[0] + at.off * c.k_stride[2]);
+                const uint64_t v = reinterpret_cast<uint64_t>(v_base + at.page * c.v_stride[0] + at.off * c.v_stride[2]);
                 constexpr int kChunks = S::kRow / 16, kAtOnce = 32 / kChunks;
                 const int chunk = lane % kChunks;
 #pragma unroll
@@ -265,9 +212,9 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
                 }
                 const int bytes = seen ? S::kScales : 0;
                 copy_small<S::kScales>(st + S::kKScale + lane * S::kScales,
-                                       ks_base + page * p.c.k_scale_stride[0] + off * p.c.k_scale_stride[2], bytes);
+                                       ks_base + at.page * c.k_scale_stride[0] + at.off * c.k_scale_stride[2], bytes);
                 copy_small<S::kScales>(st + S::kVScale + lane * S::kScales,
-                                       vs_base + page * p.c.v_scale_stride[0] + off * p.c.v_scale_stride[2], bytes);
+                                       vs_base + at.page * c.v_scale_stride[0] + at.off * c.v_scale_stride[2], bytes);
             }
             copy_commit();
         };
@@ -278,7 +225,7 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
         // q as the second operand: column g of tile n, for block j and half x
         // of it elements 4t + x, 4t + x + 2 and 16 further
         uint32_t qf[NT][NB][2][2];
-        float c[NT][2];  // of columns 2t and 2t + 1
+        float cs[NT][2];  // c of columns 2t and 2t + 1
         int pos[NT][2];  // their positions
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -316,7 +263,7 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
             const float down = __uint_as_float((uint32_t)(127 - up) << 23);
             const float row_c = fminf(p.scale_log2 * down, 3e38f);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) c[n][x] = __shfl_sync(0xffffffffu, row_c, (2 * t + x) * 4);
+            for (int x = 0; x < 2; ++x) cs[n][x] = __shfl_sync(0xffffffffu, row_c, (2 * t + x) * 4);
             auto pair = [&](float a, float z) { return as_bits(__floats2half2_rn(a * f, z * f)); };
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
@@ -397,7 +344,7 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     top[n][x] = fmaxf(fmaxf(sc[0][n][x], sc[0][n][x + 2]), fmaxf(sc[1][n][x], sc[1][n][x + 2]));
-                    grew |= (top[n][x] - m[n][x]) * c[n][x] > kGrow;
+                    grew |= (top[n][x] - m[n][x]) * cs[n][x] > kGrow;
                 }
             if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -408,7 +355,7 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
                         float v = fmaxf(top[n][x], m[n][x]);
 #pragma unroll
                         for (int d = 4; d <= 16; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-                        f[x] = m[n][x] == v ? 1.f : ex2((m[n][x] - v) * c[n][x]);
+                        f[x] = m[n][x] == v ? 1.f : ex2((m[n][x] - v) * cs[n][x]);
                         m[n][x] = v;
                         l[n][x] *= f[x];
                     }
@@ -429,7 +376,7 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
                     float e[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        e[x] = ex2((sc[h][n][x] - base[x & 1]) * c[n][x & 1]);
+                        e[x] = ex2((sc[h][n][x] - base[x & 1]) * cs[n][x & 1]);
                         l[n][x & 1] += e[x];
                     }
                     pf[h][n][0] = transpose8x8(as_bits(__floats2half2_rn(e[0], e[1])));
@@ -492,7 +439,7 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
                 for (int d = 4; d <= 16; d <<= 1) l[n][x] += __shfl_xor_sync(0xffffffffu, l[n][x], d);
                 if (g == 0) {
                     warp_ml[warp][n * 8 + 2 * t + x] = make_float2(m[n][x], l[n][x]);
-                    if (warp == 0) row_mlc[n * 8 + 2 * t + x].z = c[n][x];
+                    if (warp == 0) row_mlc[n * 8 + 2 * t + x].z = cs[n][x];
                 }
             }
         }
@@ -642,10 +589,14 @@ __global__ void __launch_bounds__(256) attention_q4_join_kernel(const __grid_con
 
 // -------------------------------------------------------------------- host
 
+// Rows (tokens times heads of the group) of the sequences that these kernels
+// take; those of longer ones fill tcgen05's tiles (attention.cu).
+constexpr int kMostRows = 32;
+
 // Rows of an item: tiles of 8, as few as hold the rows of a sequence.
 int item_rows(int group, int max_q_len) {
     const int64_t rows = (int64_t)group * max_q_len;
-    return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : kMostRows;
 }
 
 struct WorkspaceLayout {
@@ -663,24 +614,20 @@ cudaError_t launch_narrow(const Params &p, int ctas, cudaStream_t s) {
     using N = Narrow<D, NT, W>;
     const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(attention_q4_kernel<D, NT, W>), N::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attention_q4_kernel<D, NT, W>, dim3(ctas), dim3(N::kThreads), N::kSmem, s, p, kNibbleBias);
+    return launch_pdl(attention_q4_kernel<D, NT, W>, dim3(ctas), dim3(N::kThreads), N::kSmem, s, p);
 }
 
 template <int D>
 cudaError_t launch_d(const AttentionArgs &a, const KvQ4View &c, void *workspace, int ctas, cudaStream_t s,
                      unsigned int *err) {
     Params p{};
-    p.c = c;
+    p.cache = cache_q4(c);
     p.page_table = c.page_table, p.q_start = c.q_start, p.kv_len = c.kv_len, p.table_stride = c.table_stride;
     p.sequences = c.sequences, p.table_width = c.table_width, p.pages = c.pages, p.page_size = c.page_size;
     p.rows = a.rows, p.max_q_len = a.max_q_len;
-    // with 2^s < page_size <= 2^(s + 1), t = floor(t m / 2^(32 + s)) for m the
-    // next whole number from 2^(32 + s) / page_size and t < 2^31
-    while ((2 << p.page_shift) < c.page_size) ++p.page_shift;
-    p.page_magic = (uint32_t)(((1ull << (32 + p.page_shift)) + c.page_size - 1) / c.page_size);
     p.q_heads = a.q_heads, p.kv_heads = c.kv_heads, p.group = a.q_heads / c.kv_heads;
     p.window = a.window, p.sinks = a.sinks;
-    p.item_rows = item_rows(p.group, a.max_q_len);
+    p.item_rows = item_rows(p.group, a.max_q_len), p.most_rows = kMostRows;
     p.q = a.q, p.q_row_stride = a.q_row_stride, p.q_head_stride = a.q_head_stride;
     p.scale_log2 = a.scale * kLog2e;
     p.out = a.out, p.lse = a.lse, p.out_bf16 = a.out_bf16;
@@ -700,15 +647,23 @@ cudaError_t launch_d(const AttentionArgs &a, const KvQ4View &c, void *workspace,
 }  // namespace
 
 size_t attention_q4_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q_len) {
-    return WorkspaceLayout(current_sms(), head_dim, item_rows(q_heads / kv_heads, max_q_len)).bytes;
+    const int group = q_heads / kv_heads;
+    const size_t narrow = WorkspaceLayout(current_sms(), head_dim, item_rows(group, max_q_len)).bytes;
+    return narrow + ((int64_t)group * max_q_len > kMostRows
+                         ? attention_workspace_bytes(q_heads, kv_heads, head_dim, max_q_len)
+                         : 0);
 }
 
 cudaError_t launch_attention_q4(const AttentionArgs &a, const KvQ4View &c, void *workspace, cudaStream_t s,
                                 unsigned int *err) {
-    const int sms = current_sms();
+    const int sms = current_sms(), group = a.q_heads / c.kv_heads;
     if (sms < 1) return cudaErrorInvalidDevice;
-    return c.head_dim == 128 ? launch_d<128>(a, c, workspace, sms, s, err)
-                             : launch_d<64>(a, c, workspace, sms, s, err);
+    cudaError_t e = cudaSuccess;
+    if (group <= kMostRows)
+        e = c.head_dim == 128 ? launch_d<128>(a, c, workspace, sms, s, err) : launch_d<64>(a, c, workspace, sms, s, err);
+    if (e != cudaSuccess || (int64_t)group * a.max_q_len <= kMostRows) return e;
+    const size_t narrow = WorkspaceLayout(sms, c.head_dim, item_rows(group, a.max_q_len)).bytes;
+    return launch_attention_q4_wide(a, c, kMostRows + 1, static_cast<uint8_t *>(workspace) + narrow, s, err);
 }
 
 }  // namespace q4_0

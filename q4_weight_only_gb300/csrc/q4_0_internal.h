@@ -162,6 +162,11 @@ cudaError_t launch_kv_append_q4(const KvAppendArgs &a, const KvQ4View &c, int64_
 cudaError_t launch_kv_read_q4(const KvQ4View &c, int64_t rows, void *k_out, void *v_out, bool bf16, cudaStream_t s,
                               unsigned int *err);
 
+// The tcgen05 kernel over that cache, for the sequences with at least `least`
+// (token, head of the group) rows; workspace as launch_attention.
+cudaError_t launch_attention_q4_wide(const AttentionArgs &a, const KvQ4View &c, int least, void *workspace,
+                                     cudaStream_t s, unsigned int *err);
+
 size_t attention_q4_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_q_len);
 cudaError_t launch_attention_q4(const AttentionArgs &a, const KvQ4View &c, void *workspace, cudaStream_t s,
                                 unsigned int *err);

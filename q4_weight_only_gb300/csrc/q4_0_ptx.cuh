@@ -215,6 +215,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return r;
 }
 
+// The same as binary16.
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // 2^x (approximate, subnormal results flushed to zero).
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -518,12 +525,13 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(uint32_t M, uint32_t N, bo
     return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
-// Instruction descriptor, kind::f16: fp16 A and B (both K-major), fp32 D,
-// MMA shape M x N.
-__host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N) {
+// Instruction descriptor, kind::f16: fp16 A and B, fp32 D, MMA shape M x N; B
+// is K-major, or MN-major when `b_mn`.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, bool b_mn = false) {
     return (1u << 4)            // D format: fp32
            | (0u << 7)          // A format: fp16
            | (0u << 10)         // B format: fp16
+           | ((b_mn ? 1u : 0u) << 16)
            | ((N >> 3) << 17)   // N / 8
            | ((M >> 4) << 24);  // M / 16
 }
