@@ -71,12 +71,17 @@ namespace q4_0 {
 namespace {
 
 constexpr int kTile = 128;      // rows of a tile, and tokens of a key tile
-constexpr int kThreads = 384;
-// registers a thread: the launch gives 168 each; the copy and MMA warps give
-// theirs up to the softmax warps (128 * 56 + 256 * 224 = 384 * 168)
-constexpr int kRoleRegs = 56, kSoftmaxRegs = 224;
-// 4 bits: warps 0, 2 and 3 unpack a tile's 32-token parts in turn
-constexpr int kUnpackers = 3, kCodeStages = 3;
+// Threads and their registers.  The launch gives 168 each; the copy and MMA
+// warps give theirs up to the softmax warps (128 * 56 + 256 * 224 = 384 *
+// 168).  4 bits: warps 12 to 15 unpack a tile's four parts of 32 tokens (128 *
+// (40 + 56) + 256 * 208 = 512 * 128).
+template <bool kQ4>
+struct Roles {
+    static constexpr int kThreads = kQ4 ? 512 : 384;
+    static constexpr int kRoleRegs = kQ4 ? 40 : 56, kUnpackRegs = 56, kSoftmaxRegs = kQ4 ? 208 : 224;
+    static constexpr int kReaders = kQ4 ? 14 : 11;  // warps that read items
+};
+constexpr int kUnpackers = 4, kCodeStages = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;    // log2 of the growth of a row's maximum that moves its reference
@@ -212,7 +217,7 @@ struct Bars {
     uint32_t tmem;
     uint32_t fills[2], q_fills;  // copies made: past the last K and V tile's ring position, and of Q
     int abort;
-    Start<kThreads> start;
+    Start<Roles<kQ4>::kThreads> start;
 };
 static_assert(sizeof(Bars<10, false>) <= Layout<64, false>::kStatBytes, "");
 static_assert(sizeof(Bars<9, true>) <= Layout<64, true>::kStatBytes, "");
@@ -252,7 +257,7 @@ __device__ __forceinline__ float q_to_f16(uint8_t *tile, int block, int row) {
 }
 
 // kmap, vmap: of a bfloat16 cache.  P: Params, or ParamsQ4 for a cache in 4
-// bits, whose codes warps 0, 2 and 3 unpack into the ring's tiles.
+// bits, whose codes warps 12 to 15 unpack into the ring's tiles.
 template <int D, typename P>
 __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMap *kmap, const CUtensorMap *vmap,
                                        const P &p) {
@@ -287,7 +292,7 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
         mbar_init(&bar.merged, 4);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&bar.item_full[i], 1);
-            mbar_init(&bar.item_empty[i], kQ4 ? 12 : 11);  // warps that read items
+            mbar_init(&bar.item_empty[i], Roles<kQ4>::kReaders);
         }
         mbar_init(&bar.drain, 1);
         bar.abort = 0;
@@ -300,7 +305,7 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
     }
     pdl_launch_dependents();
     pdl_wait();
-    locate<kThreads>(p, bar.start, blockIdx.x, gridDim.x);
+    locate<Roles<kQ4>::kThreads>(p, bar.start, blockIdx.x, gridDim.x);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -395,58 +400,51 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
         return true;
     };
 
-    // 4 bits.  A tile is unpacked in four parts of 32 tokens; part number n of
-    // the share (fill n / 4 of the ring) is warp n mod 3's.  The codes come by
-    // asynchronous copies, two parts ahead, and their page numbers one part
-    // before that.
+    // 4 bits.  Warp 12 + i unpacks part i, tokens 32 i to 32 i + 31, of every
+    // tile of the ring.  The codes come by asynchronous copies, two tiles
+    // ahead, and their page numbers a key tile before that.
     auto unpack = [&]() {
         if constexpr (kQ4) {
-            const int me = warp ? warp - 1 : 0;  // warps 0, 2, 3
+            const int part = warp - 12;
             const KvQ4View &c = p.cache.c;
-            const uint32_t stages = smem_u32(smem + L::kCodes) + me * (kCodeStages * L::kCodeBytes);
-            Publisher w{};
-            bool publishing = me == 2;
-            if (publishing) {
-                w = publisher();
-                publishing = publish(w);
-            }
-            // the part to be copied next, and the parts of its item
-            uint32_t part = me, begin = 0, end = 0;
-            bool open = false, ended = false;
-            int kv = 0, page = 0, off = 0, head = 0;
-            bool seen = false;
+            const uint32_t stages = smem_u32(smem + L::kCodes) + part * (kCodeStages * L::kCodeBytes);
+            const uint32_t bias = p.cache.bias;
+            // the key tile to be copied next, and the lane's token of it
+            bool open = false, ended = false, seen = false;
+            int t = 0, head = 0, page = 0, off = 0;
             auto look = [&]() {
-                while (part >= end) {
+                if (!open || ++t == cur.t1) {
                     if (open) done_item();
                     open = next_item();
                     if (!open) {
                         ended = true;
                         return;
                     }
-                    begin = end, end += 8 * (cur.t1 - cur.t0);
-                    if (publishing) publishing = publish(w);
+                    t = cur.t0;
                 }
-                const int local = (int)(part - begin);
-                kv = local >> 2 & 1, head = cur.head;
-                const int token = cur.key_tile(cur.t0 + (local >> 3)) * kTile + (local & 3) * 32 + lane;
+                head = cur.head;
+                const int token = cur.key_tile(t) * kTile + part * 32 + lane;
                 seen = token < cur.sink_end || (token >= cur.lo && token < cur.hi);
                 const int index = __umulhi((uint32_t)token, p.cache.page_magic) >> p.cache.page_shift;
                 if (seen) page = p.page_table[(int64_t)cur.b * p.table_stride + index];
                 off = token - index * p.page_size;
-                part += kUnpackers;
             };
-            uint32_t stage = 0;
+            uint32_t copied = 0, to = stages;  // tiles of the ring, K and V in turn
             auto copy_next = [&]() {
                 if (!ended) {
-                    if (seen && (page < 0 || page >= p.pages)) {
-                        report_index(p.err);
-                        seen = false;
+                    const bool value = copied & 1;
+                    if (!value) {
+                        if (seen && (page < 0 || page >= p.pages)) {
+                            report_index(p.err);
+                            seen = false;
+                        }
+                        if (!seen) page = off = 0;
                     }
-                    if (!seen) page = off = 0;
-                    const uint32_t all_seen = __ballot_sync(0xffffffffu, seen), to = stages + stage * L::kCodeBytes;
-                    const int64_t *st = kv ? c.v_stride : c.k_stride, *ss = kv ? c.v_scale_stride : c.k_scale_stride;
+                    const uint32_t all_seen = __ballot_sync(0xffffffffu, seen);
+                    const int64_t *st = value ? c.v_stride : c.k_stride;
+                    const int64_t *ss = value ? c.v_scale_stride : c.k_scale_stride;
                     const uint64_t row =
-                        reinterpret_cast<uint64_t>((kv ? c.v : c.k) + page * st[0] + head * st[1] + off * st[2]);
+                        reinterpret_cast<uint64_t>((value ? c.v : c.k) + page * st[0] + head * st[1] + off * st[2]);
                     constexpr int kChunks = L::kCodeRow / 16, kAtOnce = 32 / kChunks;
                     const int chunk = lane % kChunks;
 #pragma unroll
@@ -457,45 +455,40 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                                reinterpret_cast<const void *>(from + chunk * 16), all_seen >> tok & 1 ? 16 : 0);
                     }
                     copy_small<L::kScaleRow>(to + 32 * L::kCodeRow + lane * L::kScaleRow,
-                                             (kv ? c.v_scale : c.k_scale) + page * ss[0] + head * ss[1] + off * ss[2],
+                                             (value ? c.v_scale : c.k_scale) + page * ss[0] + head * ss[1] + off * ss[2],
                                              seen ? L::kScaleRow : 0);
-                    look();
+                    ++copied;
+                    if (value) look();
                 }
                 copy_commit();
-                stage = stage + 1 == kCodeStages ? 0 : stage + 1;
+                to = to + L::kCodeBytes == stages + kCodeStages * L::kCodeBytes ? stages : to + L::kCodeBytes;
             };
             look();
 #pragma unroll
             for (int i = 0; i < kCodeStages - 1; ++i) copy_next();
-            uint32_t from = 0;
-            // warp 3 loads an item's Q after its parts of the first K tile
-            // (Q waits for room).  The item's record stays until the softmax
-            // warps have had that Q.
-            uint32_t q = 0, q_item = 0, q_part = 0;
-            const uint32_t bias = p.cache.bias;
-            for (uint32_t n = me;; n += kUnpackers) {
-                const bool all_copied = ended;
+            uint32_t from = stages, slot = 0, phase = 1;
+            const int row = part * 32 + lane;
+            for (uint32_t fill = 0;; ++fill) {
                 copy_next();
-                if (all_copied && n >= end) break;
+                if (fill == copied) break;
                 copy_wait<kCodeStages - 1>();
                 __syncwarp();
-                const uint32_t fill = n >> 2, slot = fill % kStages;
-                if (!__all_sync(0xffffffffu, mbar_wait(&bar.empty[slot], (fill / kStages & 1) ^ 1, abort_flag, p.err)))
-                    break;
-                const uint32_t src = stages + from * L::kCodeBytes;
-                const int row = (n & 3) * 32 + lane;
+                if (!__all_sync(0xffffffffu, mbar_wait(&bar.empty[slot], phase, abort_flag, p.err))) break;
                 uint32_t d[2];
                 if (D == 128) {
-                    const uint2 x = lds64(src + 32 * L::kCodeRow + lane * 8);
+                    const uint2 x = lds64(from + 32 * L::kCodeRow + lane * 8);
                     d[0] = x.x, d[1] = x.y;
                 } else {
-                    d[0] = d[1] = lds32(src + 32 * L::kCodeRow + lane * 4);
+                    d[0] = d[1] = lds32(from + 32 * L::kCodeRow + lane * 4);
                 }
+                uint4 codes[D / 32];  // all before the first store, which no load passes
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j)
+                    codes[j] = lds128(from + lane * L::kCodeRow + (j ^ (D == 128 ? lane >> 1 & 3 : lane >> 2 & 1)) * 16);
                 const uint32_t dst = smem_u32(ring) + slot * L::kTileBytes + row * 128;
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j) {
-                    const uint4 x =
-                        lds128(src + lane * L::kCodeRow + (j ^ (D == 128 ? lane >> 1 & 3 : lane >> 2 & 1)) * 16);
+                    const uint4 x = codes[j];
                     const __half2 e = as_half2(d[j / 2]);
                     const __half2 scale = j & 1 ? __high2half2(e) : __low2half2(e);
                     const uint32_t words[4] = {x.x, x.y, x.z, x.w};
@@ -505,8 +498,8 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                         uint32_t lo[4], hi[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const uint32_t t = __byte_perm(words[2 * h + i / 2], 0, i & 1 ? 0x4342 : 0x4140);
-                            lo[i] = times(low_codes(t, bias), scale), hi[i] = times(high_codes(t, bias), scale);
+                            const uint32_t w = __byte_perm(words[2 * h + i / 2], 0, i & 1 ? 0x4342 : 0x4140);
+                            lo[i] = times(low_codes(w, bias), scale), hi[i] = times(high_codes(w, bias), scale);
                         }
                         const uint32_t at = dst + (j >> 1) * L::kBlock;
                         const int first = (j & 1) * 4 + h;
@@ -517,34 +510,28 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.full[slot]);
-                from = from + 1 == kCodeStages ? 0 : from + 1;
-                if (me == 2 && n >= q_part) {
-                    const Item &o = bar.item[q_item++ % kItems];
-                    const int q_head = o.head;
-                    int q_row = o.row0, tokens = o.tokens;
-                    q_part += 8 * (o.t1 - o.t0);
-                    bool ok = true;
-                    for (; ok && tokens > 0; tokens -= p.tokens, q_row += p.tokens) {
-                        ok = load_q(q, q_head, q_row);
-                        q += ok;
-                    }
-                    if (!ok) break;
-                }
+                from = from + L::kCodeBytes == stages + kCodeStages * L::kCodeBytes ? stages : from + L::kCodeBytes;
+                if (++slot == kStages) slot = 0, phase ^= 1;
             }
             copy_wait<0>();
-            if (me == 2) {
-                publish_end(w);
-                if (lane == 0) bar.q_fills = q;
-            } else if (lane == 0) {
-                bar.fills[me] = 0;  // no copies of theirs are on barriers
-            }
         }
     };
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
-        if (kQ4 && warp != 1) {
-            unpack();
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Roles<kQ4>::kRoleRegs));
+        if (kQ4 && (warp == 0 || warp == 2)) {
+            // 4 bits: warp 0 copies Q
+            uint32_t q = 0;
+            if (warp == 0) {
+                for (bool ok = true; ok && next_item(); done_item()) {
+                    for (int done = 0; ok && done < cur.tokens; done += p.tokens) {
+                        ok = load_q(q, cur.head, cur.row0 + done);
+                        q += ok;
+                    }
+                    if (!ok) break;
+                }
+                if (lane == 0) bar.q_fills = q, bar.fills[0] = bar.fills[1] = 0;
+            }
         } else if (!kQ4 && (warp == 0 || warp == 2)) {
             // ------------------------------------------------ copies
             // K and V tiles alternate in one ring; each warp fills its own.
@@ -638,7 +625,7 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                 bar.fills[kv] = fill;
                 if (kv == 0) bar.q_fills = q;
             }
-        } else if (!kQ4 && warp == 3) {
+        } else if (warp == 3) {
             // ------------------------------------------------- items
             Publisher w = publisher();
             while (publish(w)) {
@@ -799,9 +786,12 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
         __syncwarp();
         mbar_drain(&bar.drain, 0);
         }
+    } else if (kQ4 && warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Roles<kQ4>::kUnpackRegs));
+        unpack();
     } else {
         // --------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Roles<kQ4>::kSoftmaxRegs));
         const int g = (warp - 4) >> 2;                 // group
         const int quad = warp & 3;                     // its tensor-memory lanes
         const int row = quad * 32 + lane;              // row of the tile
@@ -1044,14 +1034,14 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Roles<false>::kThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Params p) {
     attend<D>(qmap, &kmap, &vmap, p);
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Roles<true>::kThreads, 1)
     attention_q4_wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ ParamsQ4 p) {
     attend<D>(qmap, nullptr, nullptr, p);
 }
@@ -1238,7 +1228,7 @@ cudaError_t launch_d(const AttentionArgs &a, const KvCacheView &c, void *workspa
     constexpr int kSmem = Layout<D, false>::kSmem;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(attention_kernel<D>), kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(attention_kernel<D>, dim3(ctas), dim3(kThreads), kSmem, s, qmap, kmap, vmap, p);
+    e = launch_pdl(attention_kernel<D>, dim3(ctas), dim3(Roles<false>::kThreads), kSmem, s, qmap, kmap, vmap, p);
     if (e != cudaSuccess) return e;
     return launch_join<D>(p, ctas, s);
 }
@@ -1257,7 +1247,7 @@ cudaError_t launch_q4_d(const AttentionArgs &a, const KvQ4View &c, int least, vo
     constexpr int kSmem = Layout<D, true>::kSmem;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(attention_q4_wide_kernel<D>), kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(attention_q4_wide_kernel<D>, dim3(ctas), dim3(kThreads), kSmem, s, qmap, p);
+    e = launch_pdl(attention_q4_wide_kernel<D>, dim3(ctas), dim3(Roles<true>::kThreads), kSmem, s, qmap, p);
     if (e != cudaSuccess) return e;
     return launch_join<D>(p, ctas, s);
 }
