@@ -74,14 +74,13 @@ constexpr int kTile = 128;      // rows of a tile, and tokens of a key tile
 // Threads and their registers.  The launch gives 168 each; the copy and MMA
 // warps give theirs up to the softmax warps (128 * 56 + 256 * 224 = 384 *
 // 168).  4 bits: warps 12 to 15 unpack a tile's four parts of 32 tokens (128 *
-// (40 + 56) + 256 * 208 = 512 * 128).
+// (48 + 48) + 256 * 208 = 512 * 128).
 template <bool kQ4>
 struct Roles {
     static constexpr int kThreads = kQ4 ? 512 : 384;
-    static constexpr int kRoleRegs = kQ4 ? 40 : 56, kUnpackRegs = 56, kSoftmaxRegs = kQ4 ? 208 : 224;
-    static constexpr int kReaders = kQ4 ? 14 : 11;  // warps that read items
+    static constexpr int kRoleRegs = kQ4 ? 48 : 56, kUnpackRegs = 48, kSoftmaxRegs = kQ4 ? 208 : 224;
+    static constexpr int kReaders = kQ4 ? 15 : 11;  // warps that read items
 };
-constexpr int kUnpackers = 4, kCodeStages = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;    // log2 of the growth of a row's maximum that moves its reference
@@ -184,15 +183,16 @@ struct Layout {
     static constexpr int kHalves = D / 64;                 // 64-element column blocks
     static constexpr int kTileBytes = kTile * D * 2;
     static constexpr int kBlock = kTile * 128;             // bytes of one column block
-    static constexpr int kStages = (D == 128 ? 5 : 10) - (kQ4 ? 1 : 0);  // K or V tiles in the ring
+    static constexpr int kStages = kQ4 ? (D == 128 ? 4 : 8) : (D == 128 ? 5 : 10);  // K or V tiles in the ring
+    static constexpr int kCodeStages = D == 128 ? 3 : 6;                            // 4 bits: tiles' codes
     static constexpr int kQTiles = D == 128 ? 2 : 4;       // Q tiles held
     static constexpr int kQ = 0;
     static constexpr int kRing = kQTiles * kTileBytes;
-    // 4 bits: codes and scales of 32 tokens, a few of each unpacking warp
+    // 4 bits: a ring of tiles' codes and scales
     static constexpr int kCodes = kRing + kStages * kTileBytes;
-    static constexpr int kCodeRow = D / 2, kScaleRow = D / 16, kCodeBytes = 32 * (kCodeRow + kScaleRow);
-    static constexpr int kBars = kCodes + (kQ4 ? kUnpackers * kCodeStages * kCodeBytes : 0);
-    static constexpr int kStatBytes = kQ4 ? 3072 : 2048;
+    static constexpr int kCodeRow = D / 2, kScaleRow = D / 16, kCodeBytes = kTile * (kCodeRow + kScaleRow);
+    static constexpr int kBars = kCodes + (kQ4 ? kCodeStages * kCodeBytes : 0);
+    static constexpr int kStatBytes = kQ4 ? 4096 : 2048;
     static constexpr int kSmem = kBars + kStatBytes + 1024;  // + alignment
 };
 
@@ -202,6 +202,7 @@ constexpr int kMaxQTiles = 4;
 
 template <int kStages, bool kQ4>
 struct Bars {
+    static constexpr int kMaxCodes = 6;
     uint64_t full[kStages], empty[kStages];
     uint64_t q_full[kMaxQTiles], q_empty[kMaxQTiles];
     uint64_t s_full[2], p_full[2], o_full[2];
@@ -210,17 +211,18 @@ struct Bars {
     uint64_t drain;
     Item item[kItems];
     float2 ml[kTile];
-    // 4 bits: Q tiles turned to binary16, and what a narrow item's rows were
-    // scaled by, for group B
+    // 4 bits: the ring of codes, Q tiles turned to binary16 and what undoes
+    // their rows' scaling
     uint64_t q_ready[kQ4 ? kMaxQTiles : 1];
-    float q_down[kQ4 ? kTile : 1];
+    uint64_t codes_full[kQ4 ? kMaxCodes : 1], codes_empty[kQ4 ? kMaxCodes : 1];
+    float q_down[kQ4 ? 2 : 1][kQ4 ? kTile : 1];
     uint32_t tmem;
     uint32_t fills[2], q_fills;  // copies made: past the last K and V tile's ring position, and of Q
     int abort;
     Start<Roles<kQ4>::kThreads> start;
 };
 static_assert(sizeof(Bars<10, false>) <= Layout<64, false>::kStatBytes, "");
-static_assert(sizeof(Bars<9, true>) <= Layout<64, true>::kStatBytes, "");
+static_assert(sizeof(Bars<8, true>) <= Layout<64, true>::kStatBytes, "");
 
 // Tensor memory columns.
 constexpr uint32_t kTmemCols = 512;
@@ -256,10 +258,10 @@ __device__ __forceinline__ float q_to_f16(uint8_t *tile, int block, int row) {
     return __uint_as_float((uint32_t)(127 - up) << 23);
 }
 
-// kmap, vmap: of a bfloat16 cache.  P: Params, or ParamsQ4 for a cache in 4
-// bits, whose codes warps 12 to 15 unpack into the ring's tiles.
+// P: Params, or ParamsQ4 for a cache in 4 bits: kmap and vmap are then of its
+// codes, which warps 12 to 15 unpack into the ring of tiles.
 template <int D, typename P>
-__device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMap *kmap, const CUtensorMap *vmap,
+__device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
                                        const P &p) {
     constexpr bool kQ4 = std::is_same<P, ParamsQ4>::value;
     using L = Layout<D, kQ4>;
@@ -267,7 +269,7 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
     uint8_t *ring = smem + L::kRing;
-    constexpr int kStages = L::kStages;
+    constexpr int kStages = L::kStages, kCodeStages = L::kCodeStages;
     Bars<kStages, kQ4> &bar = *reinterpret_cast<Bars<kStages, kQ4> *>(smem + L::kBars);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int *abort_flag = &bar.abort;
@@ -277,6 +279,10 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&bar.full[i], kQ4 ? kTile / 32 : 1);
             mbar_init(&bar.empty[i], 1);
+        }
+        for (int i = 0; kQ4 && i < kCodeStages; ++i) {
+            mbar_init(&bar.codes_full[i], 1 + 32);  // the codes' bytes, and each lane's scales
+            mbar_init(&bar.codes_empty[i], kTile / 32);
         }
         for (int i = 0; i < L::kQTiles; ++i) {
             mbar_init(&bar.q_full[i], 1);
@@ -298,10 +304,8 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
         bar.abort = 0;
         mbar_fence_init();
         tma_prefetch_desc(&qmap);
-        if (!kQ4) {
-            tma_prefetch_desc(kmap);
-            tma_prefetch_desc(vmap);
-        }
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
     }
     pdl_launch_dependents();
     pdl_wait();
@@ -312,14 +316,19 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
     const uint32_t tmem = bar.tmem;
 
     // The next item of the share, or false at its end or when a wait was
-    // abandoned; done_item() hands its record back.
+    // abandoned; done_item() hands its record back.  4 bits: the record is
+    // read where it lies, a copy of it would spill other registers.
     uint32_t items = 0;
-    Item cur;
+    Item copy;
+    auto item = [&]() -> const Item & {
+        if constexpr (kQ4) return bar.item[items % kItems];
+        return copy;
+    };
     auto next_item = [&]() {
         const int i = items % kItems;
         if (!__all_sync(0xffffffffu, mbar_wait(&bar.item_full[i], items / kItems & 1, abort_flag, p.err))) return false;
-        cur = bar.item[i];
-        return cur.t0 < cur.t1;
+        if constexpr (!kQ4) copy = bar.item[i];
+        return item().t0 < item().t1;
     };
     auto done_item = [&]() {
         __syncwarp();
@@ -401,146 +410,81 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
     };
 
     // 4 bits.  Warp 12 + i unpacks part i, tokens 32 i to 32 i + 31, of every
-    // tile of the ring.  The codes come by asynchronous copies, two tiles
-    // ahead, and their page numbers a key tile before that.
+    // tile from the ring of codes to the ring of tiles.  A lane has a token: a
+    // store is then 16 bytes of 32 rows, which the tiles' swizzle spreads over
+    // the banks.
     auto unpack = [&]() {
         if constexpr (kQ4) {
-            const int part = warp - 12;
-            const KvQ4View &c = p.cache.c;
-            const uint32_t stages = smem_u32(smem + L::kCodes) + part * (kCodeStages * L::kCodeBytes);
-            const uint32_t bias = p.cache.bias;
-            // the key tile to be copied next, and the lane's token of it
-            bool open = false, ended = false, seen = false;
-            int t = 0, head = 0, page = 0, off = 0;
-            auto look = [&]() {
-                if (!open || ++t == cur.t1) {
-                    if (open) done_item();
-                    open = next_item();
-                    if (!open) {
-                        ended = true;
-                        return;
+            const int row = (warp - 12) * 32 + lane;
+            const uint32_t bias = p.cache.bias, codes = smem_u32(smem + L::kCodes), tiles = smem_u32(ring) + row * 128;
+            const int turn = D == 128 ? row >> 1 & 3 : row >> 2 & 1;  // the swizzle of a row of codes
+            uint32_t from = 0, from_phase = 0, slot = 0, phase = 1;
+            bool ok = true;
+            for (; ok && next_item(); done_item()) {
+                for (int n = 2 * (item().t1 - item().t0); n > 0; --n) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bar.codes_full[from], from_phase, abort_flag, p.err) &&
+                                                     mbar_wait(&bar.empty[slot], phase, abort_flag, p.err));
+                    if (!ok) break;
+                    const uint32_t src = codes + from * L::kCodeBytes;
+                    uint32_t d[2];
+                    if (D == 128) {
+                        const uint2 x = lds64(src + kTile * L::kCodeRow + row * 8);
+                        d[0] = x.x, d[1] = x.y;
+                    } else {
+                        d[0] = d[1] = lds32(src + kTile * L::kCodeRow + row * 4);
                     }
-                    t = cur.t0;
-                }
-                head = cur.head;
-                const int token = cur.key_tile(t) * kTile + part * 32 + lane;
-                seen = token < cur.sink_end || (token >= cur.lo && token < cur.hi);
-                const int index = __umulhi((uint32_t)token, p.cache.page_magic) >> p.cache.page_shift;
-                if (seen) page = p.page_table[(int64_t)cur.b * p.table_stride + index];
-                off = token - index * p.page_size;
-            };
-            uint32_t copied = 0, to = stages;  // tiles of the ring, K and V in turn
-            auto copy_next = [&]() {
-                if (!ended) {
-                    const bool value = copied & 1;
-                    if (!value) {
-                        if (seen && (page < 0 || page >= p.pages)) {
-                            report_index(p.err);
-                            seen = false;
+                    uint4 x[D / 32];  // all before the first store, which no load passes
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j) x[j] = lds128(src + row * L::kCodeRow + (j ^ turn) * 16);
+                    const uint32_t dst = tiles + slot * L::kTileBytes;
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j) {
+                        const __half2 e = as_half2(d[j / 2]);
+                        const __half2 scale = j & 1 ? __high2half2(e) : __low2half2(e);
+                        const uint32_t words[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            // eight bytes: elements 8h .. 8h + 7 of the block and 16 further
+                            uint32_t lo[4], hi[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t w = __byte_perm(words[2 * h + i / 2], 0, i & 1 ? 0x4342 : 0x4140);
+                                lo[i] = times(low_codes(w, bias), scale), hi[i] = times(high_codes(w, bias), scale);
+                            }
+                            const uint32_t at = dst + (j >> 1) * L::kBlock;
+                            const int first = (j & 1) * 4 + h;
+                            sts128(at + ((first ^ (row & 7)) * 16), lo);
+                            sts128(at + (((first + 2) ^ (row & 7)) * 16), hi);
                         }
-                        if (!seen) page = off = 0;
                     }
-                    const uint32_t all_seen = __ballot_sync(0xffffffffu, seen);
-                    const int64_t *st = value ? c.v_stride : c.k_stride;
-                    const int64_t *ss = value ? c.v_scale_stride : c.k_scale_stride;
-                    const uint64_t row =
-                        reinterpret_cast<uint64_t>((value ? c.v : c.k) + page * st[0] + head * st[1] + off * st[2]);
-                    constexpr int kChunks = L::kCodeRow / 16, kAtOnce = 32 / kChunks;
-                    const int chunk = lane % kChunks;
-#pragma unroll
-                    for (int j = 0; j < 32 / kAtOnce; ++j) {
-                        const int tok = j * kAtOnce + lane / kChunks;
-                        const uint64_t from = __shfl_sync(0xffffffffu, row, tok);
-                        copy16(to + tok * L::kCodeRow + (chunk ^ (D == 128 ? tok >> 1 & 3 : tok >> 2 & 1)) * 16,
-                               reinterpret_cast<const void *>(from + chunk * 16), all_seen >> tok & 1 ? 16 : 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&bar.full[slot]);
+                        mbar_arrive(&bar.codes_empty[from]);
                     }
-                    copy_small<L::kScaleRow>(to + 32 * L::kCodeRow + lane * L::kScaleRow,
-                                             (value ? c.v_scale : c.k_scale) + page * ss[0] + head * ss[1] + off * ss[2],
-                                             seen ? L::kScaleRow : 0);
-                    ++copied;
-                    if (value) look();
+                    if (++from == kCodeStages) from = 0, from_phase ^= 1;
+                    if (++slot == kStages) slot = 0, phase ^= 1;
                 }
-                copy_commit();
-                to = to + L::kCodeBytes == stages + kCodeStages * L::kCodeBytes ? stages : to + L::kCodeBytes;
-            };
-            look();
-#pragma unroll
-            for (int i = 0; i < kCodeStages - 1; ++i) copy_next();
-            uint32_t from = stages, slot = 0, phase = 1;
-            const int row = part * 32 + lane;
-            for (uint32_t fill = 0;; ++fill) {
-                copy_next();
-                if (fill == copied) break;
-                copy_wait<kCodeStages - 1>();
-                __syncwarp();
-                if (!__all_sync(0xffffffffu, mbar_wait(&bar.empty[slot], phase, abort_flag, p.err))) break;
-                uint32_t d[2];
-                if (D == 128) {
-                    const uint2 x = lds64(from + 32 * L::kCodeRow + lane * 8);
-                    d[0] = x.x, d[1] = x.y;
-                } else {
-                    d[0] = d[1] = lds32(from + 32 * L::kCodeRow + lane * 4);
-                }
-                uint4 codes[D / 32];  // all before the first store, which no load passes
-#pragma unroll
-                for (int j = 0; j < D / 32; ++j)
-                    codes[j] = lds128(from + lane * L::kCodeRow + (j ^ (D == 128 ? lane >> 1 & 3 : lane >> 2 & 1)) * 16);
-                const uint32_t dst = smem_u32(ring) + slot * L::kTileBytes + row * 128;
-#pragma unroll
-                for (int j = 0; j < D / 32; ++j) {
-                    const uint4 x = codes[j];
-                    const __half2 e = as_half2(d[j / 2]);
-                    const __half2 scale = j & 1 ? __high2half2(e) : __low2half2(e);
-                    const uint32_t words[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        // eight bytes: elements 8h .. 8h + 7 of the block and 16 further
-                        uint32_t lo[4], hi[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t w = __byte_perm(words[2 * h + i / 2], 0, i & 1 ? 0x4342 : 0x4140);
-                            lo[i] = times(low_codes(w, bias), scale), hi[i] = times(high_codes(w, bias), scale);
-                        }
-                        const uint32_t at = dst + (j >> 1) * L::kBlock;
-                        const int first = (j & 1) * 4 + h;
-                        sts128(at + ((first ^ (row & 7)) * 16), lo);
-                        sts128(at + (((first + 2) ^ (row & 7)) * 16), hi);
-                    }
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.full[slot]);
-                from = from + L::kCodeBytes == stages + kCodeStages * L::kCodeBytes ? stages : from + L::kCodeBytes;
-                if (++slot == kStages) slot = 0, phase ^= 1;
+                if (!ok) break;
             }
-            copy_wait<0>();
         }
     };
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Roles<kQ4>::kRoleRegs));
-        if (kQ4 && (warp == 0 || warp == 2)) {
-            // 4 bits: warp 0 copies Q
-            uint32_t q = 0;
-            if (warp == 0) {
-                for (bool ok = true; ok && next_item(); done_item()) {
-                    for (int done = 0; ok && done < cur.tokens; done += p.tokens) {
-                        ok = load_q(q, cur.head, cur.row0 + done);
-                        q += ok;
-                    }
-                    if (!ok) break;
-                }
-                if (lane == 0) bar.q_fills = q, bar.fills[0] = bar.fills[1] = 0;
-            }
-        } else if (!kQ4 && (warp == 0 || warp == 2)) {
+        if (warp == 0 || warp == 2) {
             // ------------------------------------------------ copies
-            // K and V tiles alternate in one ring; each warp fills its own.
+            // K and V tiles (4 bits: their codes and scales) alternate in one
+            // ring; each warp fills its own.
             // A warp may not be two uses of a slot ahead (its wait would take
             // the older phase for the newer): the MMA warp frees tiles in an
             // order in which the slot of fill f - 7, waited for at fill
             // f - 2, is freed after that of f - 10.
             const int kv = warp >> 1;  // warp 0: Q and K, warp 2: V
-            const CUtensorMap *map = kv ? vmap : kmap;
+            constexpr int kRingStages = kQ4 ? kCodeStages : kStages;
+            uint64_t *const full = kQ4 ? bar.codes_full : bar.full, *const empty = kQ4 ? bar.codes_empty : bar.empty;
+            const CUtensorMap *map = kv ? &vmap : &kmap;
             uint32_t fill = kv;        // ring position of the next tile
             uint32_t slot = kv, phase = 1;
             bool ok = true;
@@ -552,33 +496,39 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                 int tiles;                 // 0: the share has ended
                 int page, off;             // off < 0: a box that no query sees
                 int head, row0, tokens;    // tokens 0: not the item's first group
+                int clip;                  // 4 bits: tokens [0, a) and [b, e) of the box are seen, 7 bits each
             };
             int t = 0;
             uint32_t q = 0;  // Q tiles copied
-            bool open = false;  // `cur` holds an item with tiles from t on
+            bool open = false;  // an item is held with tiles from t on
             auto fetch = [&]() {
                 Group o{};
                 if (!open) {
                     if (!next_item()) return o;
                     open = true;
-                    t = cur.t0;
-                    o.row0 = cur.row0, o.tokens = cur.tokens;
+                    t = item().t0;
+                    if (!kQ4) o.row0 = item().row0, o.tokens = item().tokens;
                 }
-                o.head = cur.head;
-                o.tiles = min(per_load, cur.t1 - t);
+                o.head = item().head;
+                o.tiles = min(per_load, item().t1 - t);
                 o.off = -1;
                 const int mine = lane / boxes;
                 if (mine < o.tiles) {
-                    const int tok = cur.key_tile(t + mine) * kTile + (lane - mine * boxes) * p.box;
+                    const int tok = item().key_tile(t + mine) * kTile + (lane - mine * boxes) * p.box;
                     // only boxes that hold a token some query sees
-                    if (tok < cur.sink_end || (tok < cur.hi && tok + p.box > cur.lo)) {
+                    if (tok < item().sink_end || (tok < item().hi && tok + p.box > item().lo)) {
                         const int index = tok / p.page_size;
-                        o.page = p.page_table[(int64_t)cur.b * p.table_stride + index];
+                        o.page = p.page_table[(int64_t)item().b * p.table_stride + index];
                         o.off = tok - index * p.page_size;
+                        if (kQ4) {
+                            const int a = min(max(item().sink_end - tok, 0), p.box);
+                            const int b = max(item().lo - tok, 0), e = min(item().hi - tok, p.box);
+                            o.clip = a | min(b, p.box) << 7 | e << 14;
+                        }
                     }
                 }
                 t += o.tiles;
-                if (t == cur.t1) {
+                if (t == item().t1) {
                     open = false;
                     done_item();
                 }
@@ -593,26 +543,49 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                     now.page = p.pages, now.off = 0;
                 }
                 for (int j = 0; j < now.tiles; ++j) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&bar.empty[slot], phase, abort_flag, p.err));
+                    ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], phase, abort_flag, p.err));
                     if (!ok) break;
                     const bool issue = elect_one();
-                    uint8_t *dst = ring + slot * L::kTileBytes;
-                    if (issue) mbar_arrive_expect_tx(&bar.full[slot], L::kTileBytes);
-                    for (int i = 0; i < boxes; ++i, dst += p.box * 128) {
+                    uint8_t *dst = kQ4 ? smem + L::kCodes + slot * L::kCodeBytes : ring + slot * L::kTileBytes;
+                    if (issue) mbar_arrive_expect_tx(&full[slot], kQ4 ? kTile * L::kCodeRow : L::kTileBytes);
+                    if constexpr (kQ4) {
+                        // Scales of the tokens that some query sees.  Others'
+                        // become zeros: their values may be anything (0 *
+                        // NaN).
+                        const KvQ4View &c = p.cache.c;
+                        const int64_t *st = kv ? c.v_scale_stride : c.k_scale_stride;
+                        const uint16_t *base = (kv ? c.v_scale : c.k_scale) + now.head * st[1];
+                        const uint32_t to = smem_u32(dst) + kTile * L::kCodeRow;
+                        const int shift = __ffs(p.box) - 1;
+#pragma unroll 1
+                        for (int t = lane; t < kTile; t += 32) {
+                            const int box = t >> shift, in_box = t & (p.box - 1);
+                            const int page = __shfl_sync(0xffffffffu, now.page, j * boxes + box);
+                            const int off = __shfl_sync(0xffffffffu, now.off, j * boxes + box) + in_box;
+                            const int clip = __shfl_sync(0xffffffffu, now.clip, j * boxes + box);
+                            const bool seen = page < p.pages && (in_box < (clip & 127) || (in_box >= (clip >> 7 & 127) &&
+                                                                                           in_box < clip >> 14));
+                            copy_small<L::kScaleRow>(to + t * L::kScaleRow,
+                                                     base + (seen ? page * st[0] + off * st[2] : 0),
+                                                     seen ? L::kScaleRow : 0);
+                        }
+                        copy_arrive(&full[slot]);
+                    }
+                    for (int i = 0; i < boxes; ++i, dst += p.box * (kQ4 ? L::kCodeRow : 128)) {
                         const int page = __shfl_sync(0xffffffffu, now.page, j * boxes + i);
                         const int off = __shfl_sync(0xffffffffu, now.off, j * boxes + i);
                         if (issue) {
 #pragma unroll
-                            for (int h = 0; h < L::kHalves; ++h)
-                                tma_load_4d(dst + h * L::kBlock, map, h * 64, off, now.head, page, &bar.full[slot]);
+                            for (int h = 0; h < (kQ4 ? 1 : L::kHalves); ++h)
+                                tma_load_4d(dst + h * L::kBlock, map, h * 64, off, now.head, page, &full[slot]);
                         }
                     }
                     __syncwarp();
                     fill += 2;
                     slot += 2;
-                    if (slot >= kStages) slot -= kStages, phase ^= 1;
+                    if (slot >= kRingStages) slot -= kRingStages, phase ^= 1;
                     // an item's Q after its first K tile: Q waits for room
-                    for (; kv == 0 && now.tokens > 0; now.tokens -= p.tokens, now.row0 += p.tokens) {
+                    for (; !kQ4 && kv == 0 && now.tokens > 0; now.tokens -= p.tokens, now.row0 += p.tokens) {
                         ok = load_q(q, now.head, now.row0);
                         if (!ok) break;
                         ++q;
@@ -623,12 +596,28 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
             }
             if (lane == 0) {
                 bar.fills[kv] = fill;
-                if (kv == 0) bar.q_fills = q;
+                if (!kQ4 && kv == 0) bar.q_fills = q;
             }
         } else if (warp == 3) {
             // ------------------------------------------------- items
             Publisher w = publisher();
-            while (publish(w)) {
+            bool more = publish(w);
+            if constexpr (kQ4) {
+                // and copies each item's Q, with the next item handed out:
+                // the copying warps have no registers for it
+                uint32_t q = 0;
+                bool ok = true;
+                for (uint32_t i = 0; ok && bar.item[i % kItems].t0 < bar.item[i % kItems].t1; ++i) {
+                    if (more) more = publish(w);
+                    const Item &o = bar.item[i % kItems];
+                    for (int done = 0; ok && done < o.tokens; done += p.tokens) {
+                        ok = load_q(q, o.head, o.row0 + done);
+                        q += ok;
+                    }
+                }
+                if (lane == 0) bar.q_fills = q;
+            } else {
+                while (more) more = publish(w);
             }
             publish_end(w);
         } else if (warp == 1) {
@@ -686,11 +675,11 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
         };
         // Boxes that no query sees were filled with zeros; what remains are
         // the unseen ends of the boxes that hold the ends of the seen ranges.
-        // (4 bits: they were unpacked as zeros.)
+        // (4 bits: their scales were copied as zeros.)
         auto clear_unseen = [&](int t, int slot) {
             if (kQ4) return;
-            const int tok0 = cur.key_tile(t) * kTile;
-            const int sink = cur.sink_end - tok0, lo = cur.lo - tok0, hi = cur.hi - tok0;
+            const int tok0 = item().key_tile(t) * kTile;
+            const int sink = item().sink_end - tok0, lo = item().lo - tok0, hi = item().hi - tok0;
             if (hi >= kTile && (lo <= 0 || sink >= kTile)) return;
             const int mask = ~(p.box - 1);  // a power of two
             if (sink > 0 && sink < kTile) clear_rows(slot, sink, min((sink - 1 & mask) + p.box, max(lo, sink)));
@@ -700,8 +689,8 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
             __syncwarp();
         };
         for (; ok && next_item(); done_item()) {
-            const bool wide = cur.tokens > p.tokens;
-            const int n = cur.t1 - cur.t0;
+            const bool wide = item().tokens > p.tokens;
+            const int n = item().t1 - item().t0;
             if (!q_full(q)) break;
             if (wide) {
                 uint32_t slot_k = fills % kStages, slot_v = (fills + 1) % kStages;
@@ -718,7 +707,7 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                     const bool more = t + 1 < n;
                     slot_v = v % kStages, slot_k = (v + 1) % kStages;
                     if (!full(v)) break;
-                    clear_unseen(cur.t0 + t, slot_v);
+                    clear_unseen(item().t0 + t, slot_v);
                     if (more && !full(v + 1)) break;
                     if (!wait(&bar.p_full[0], p_phase[0])) break;
                     p_phase[0] ^= 1;
@@ -758,7 +747,7 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                     const uint32_t v = fills + 2 * t + 1, k = v + 3;
                     const int g = t & 1;
                     if (!full(v)) break;
-                    clear_unseen(cur.t0 + t, v % kStages);
+                    clear_unseen(item().t0 + t, v % kStages);
                     if (!wait(&bar.p_full[g], p_phase[g])) break;
                     p_phase[g] ^= 1;
                     tc_fence_after();
@@ -797,8 +786,7 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
         const int row = quad * 32 + lane;              // row of the tile
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const uint32_t ts = tmem + lanes + col_s(g), to = tmem + lanes + col_o(g);
-        const int my_token = row / p.group, my_head = row - my_token * p.group;
-        float c = p.scale_log2, c_pow2 = p.scale_pow2;
+        const int my_token = row / p.group;
         uint32_t s_phase = 0, o_phase = 0, q_tiles = 0;
         bool ok = true;
         auto wait = [&](uint64_t *b, uint32_t parity) {
@@ -808,43 +796,37 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
         uint32_t merge_phase = 0;
         bool unmerged = false;  // group B: A may not have read O of the last item yet
         for (; ok && next_item(); done_item()) {
-            const bool wide = cur.tokens > p.tokens;
+            const bool wide = item().tokens > p.tokens;
             const int half = wide ? g : 0;                  // the tile of the item
             const int i = half * p.tokens + my_token;       // token within the item
-            const bool valid = my_token < p.tokens && i < cur.tokens;
+            const bool valid = my_token < p.tokens && i < item().tokens;
             const bool busy = __any_sync(0xffffffffu, valid);
-            const int pos = cur.pos0 + i;
-            // positions of the tile's first and last query
-            const int pos_a = cur.pos0 + half * p.tokens;
-            const int pos_z = cur.pos0 + min((half + 1) * p.tokens, cur.tokens) - 1;
+            const int pos = item().pos0 + i;
             const int step = wide ? 1 : 2;
             if constexpr (kQ4) {
-                // the group's tile of Q to binary16; a narrow item's is group
-                // A's, which tells B what its rows were scaled by
+                // the group's tile of Q to binary16; a narrow item's is group A's
                 const uint32_t qt = q_tiles + half, at = qt % L::kQTiles, parity = qt / L::kQTiles & 1;
                 q_tiles += wide ? 2 : 1;
-                float down = 1.f;
                 if (wide || g == 0) {
                     if (!wait(&bar.q_full[at], parity)) break;
-                    if (valid) down = q_to_f16<D>(smem + L::kQ + at * L::kTileBytes, L::kBlock, row);
-                    if (!wide) bar.q_down[row] = down;
+                    bar.q_down[half][row] = valid ? q_to_f16<D>(smem + L::kQ + at * L::kTileBytes, L::kBlock, row) : 1.f;
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.q_ready[at]);
-                } else {
-                    if (!wait(&bar.q_ready[at], parity)) break;
-                    down = bar.q_down[row];
+                } else if (!wait(&bar.q_ready[at], parity)) {
+                    break;
                 }
-                c = fminf(p.scale_log2 * down, 3e38f), c_pow2 = fminf(p.scale_pow2 * down, 3e38f);
             }
+            // scale * log2 e, and the next power of two, for the row as it is
+            auto c_of = [&](float scale) { return kQ4 ? fminf(scale * bar.q_down[half][row], 3e38f) : scale; };
             // A row whose maximum grew moves the references of its warp's
             // rows (each its own, one by one, took prompts 1 to 4 % longer).
             // Lanes that are no row of the item must not: they hold other
             // sequences' rows, or what an earlier kernel left in shared
             // memory.  Nothing is above their reference.
-            float mc = valid ? -INFINITY : INFINITY, c_row = c, l = 0.f;
+            float mc = valid ? -INFINITY : INFINITY, c_row = c_of(p.scale_log2), l = 0.f;
             bool started = false;
-            for (int t = cur.t0 + (wide ? 0 : g); t < cur.t1; t += step) {
+            for (int t = item().t0 + (wide ? 0 : g); t < item().t1; t += step) {
                 if (!wait(&bar.s_full[g], s_phase)) break;
                 s_phase ^= 1;
                 tc_fence_after();
@@ -853,7 +835,10 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
 #pragma unroll
                     for (int q = 0; q < 4; ++q) tmem_ld32(ts + q * 32, s[q]);
                     tmem_wait_ld();
-                    const int tok0 = cur.key_tile(t) * kTile;
+                    const int tok0 = item().key_tile(t) * kTile;
+                    // positions of the tile's first and last query
+                    const int pos_a = item().pos0 + half * p.tokens;
+                    const int pos_z = item().pos0 + min((half + 1) * p.tokens, item().tokens) - 1;
                     if (tok0 + kTile - 1 > pos_a || (p.window && tok0 <= pos_z - p.window && tok0 + kTile > p.sinks)) {
                         const int end = pos + 1 - tok0;
                         const int first = p.window ? end - p.window : 0;
@@ -879,7 +864,8 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                     const float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
                     // (nothing is above an infinite reference)
                     if (__any_sync(0xffffffffu, fmaf(top, c_row, -mc) > kGrow)) {
-                        const float c_top = fabsf(top * c) > (kQ4 ? kHugeQ4 : kHuge) ? c_pow2 : c;
+                        const float c = c_of(p.scale_log2);
+                        const float c_top = fabsf(top * c) > (kQ4 ? kHugeQ4 : kHuge) ? c_of(p.scale_pow2) : c;
                         const float mc_new = __fmul_rn(top, c_top);
                         const bool above = mc_new > mc;
                         const float f = mc == -INFINITY ? 0.f : above ? ex2(mc - mc_new) : 1.f;
@@ -936,7 +922,7 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
             // o_phase counts the group's second products: wait for the last
             if (started && !wait(&bar.o_full[g], o_phase ^ 1)) break;
             tc_fence_after();
-            mc *= c_row == c ? 1.f : p.scale_back;
+            mc *= c_row == c_of(p.scale_log2) ? 1.f : p.scale_back;
             if (!wide && g == 1) {
                 if (unmerged && !wait(&bar.merged, merge_phase ^ 1)) break;
                 bar.ml[row] = make_float2(mc, l);
@@ -957,11 +943,11 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                     fa = ex2(mc - base), fb = ex2(other.x - base);
                     l = l * fa + other.y * fb;
                 }
-                const bool both = !wide && cur.t1 - cur.t0 > 1;
+                const bool both = !wide && item().t1 - item().t0 > 1;
                 if (busy) {
-                    const bool whole = cur.t0 == 0 && cur.t1 == cur.n;
-                    const int64_t at = ((int64_t)cur.row0 + i) * p.q_heads + cur.head * p.group + my_head;
-                    const int piece = blockIdx.x * 2 + (cur.t0 == 0 ? 1 : 0);
+                    const bool whole = item().t0 == 0 && item().t1 == item().n;
+                    const int64_t at = ((int64_t)item().row0 + i) * p.q_heads + item().head * p.group + (row - my_token * p.group);
+                    const int piece = blockIdx.x * 2 + (item().t0 == 0 ? 1 : 0);
                     const int prow = piece * p.piece_rows + half * kTile + row;
                     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
                     if (whole) fa *= inv, fb *= inv;
@@ -1021,11 +1007,12 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
     if (bar.abort && tid == 0) {
         // a wait was abandoned: copies in flight land before the CTA exits
         // (otherwise every copy was waited for by its reader)
-        for (uint32_t i = 0; i < kStages; ++i) {
+        constexpr uint32_t kRingStages = kQ4 ? kCodeStages : kStages;
+        for (uint32_t i = 0; i < kRingStages; ++i) {
             int last = -1;
-            for (uint32_t f = i; f < max(bar.fills[0], bar.fills[1]); f += kStages)
+            for (uint32_t f = i; f < max(bar.fills[0], bar.fills[1]); f += kRingStages)
                 if (f < bar.fills[f & 1]) last = f;
-            if (last >= 0) mbar_drain(&bar.full[i], last / kStages & 1);
+            if (last >= 0) mbar_drain(kQ4 ? &bar.codes_full[i] : &bar.full[i], last / kRingStages & 1);
         }
         for (uint32_t f = max(bar.q_fills, (uint32_t)L::kQTiles) - L::kQTiles; f < bar.q_fills; ++f)
             mbar_drain(&bar.q_full[f % L::kQTiles], f / L::kQTiles & 1);
@@ -1037,13 +1024,14 @@ template <int D>
 __global__ void __launch_bounds__(Roles<false>::kThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Params p) {
-    attend<D>(qmap, &kmap, &vmap, p);
+    attend<D>(qmap, kmap, vmap, p);
 }
 
 template <int D>
 __global__ void __launch_bounds__(Roles<true>::kThreads, 1)
-    attention_q4_wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ ParamsQ4 p) {
-    attend<D>(qmap, nullptr, nullptr, p);
+    attention_q4_wide_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                             const __grid_constant__ CUtensorMap vmap, const __grid_constant__ ParamsQ4 p) {
+    attend<D>(qmap, kmap, vmap, p);
 }
 
 // Adds the pieces of the items that a share's boundary cut.  blockIdx.x: the
@@ -1148,6 +1136,20 @@ bool make_map(EncodeTiledFn enc, CUtensorMap *map, const void *base, const int64
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Codes as {byte, token of the page, key head, page}, rows swizzled over their
+// own length.
+bool make_codes_map(EncodeTiledFn enc, CUtensorMap *map, const uint8_t *base, const int64_t (&stride)[3],
+                    const KvQ4View &c, int box1) {
+    const int row = c.head_dim / 2;
+    const cuuint64_t dims[4] = {(cuuint64_t)row, (cuuint64_t)c.page_size, (cuuint64_t)c.kv_heads, (cuuint64_t)c.pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)stride[2], (cuuint64_t)stride[1], (cuuint64_t)stride[0]};
+    const cuuint32_t box[4] = {(cuuint32_t)row, (cuuint32_t)box1, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
 // Rows of an item that has at most max_q_len tokens.
@@ -1242,12 +1244,14 @@ cudaError_t launch_q4_d(const AttentionArgs &a, const KvQ4View &c, int least, vo
     fill_params<D>(p, a, c, workspace, ctas, err);
     p.cache = cache_q4(c);
     p.least = least;
-    CUtensorMap qmap;
-    if (!make_q_map<D>(enc, &qmap, a, p)) return cudaErrorInvalidValue;
+    CUtensorMap qmap, kmap, vmap;
+    if (!make_q_map<D>(enc, &qmap, a, p) || !make_codes_map(enc, &kmap, c.k, c.k_stride, c, p.box) ||
+        !make_codes_map(enc, &vmap, c.v, c.v_stride, c, p.box))
+        return cudaErrorInvalidValue;
     constexpr int kSmem = Layout<D, true>::kSmem;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(attention_q4_wide_kernel<D>), kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(attention_q4_wide_kernel<D>, dim3(ctas), dim3(Roles<true>::kThreads), kSmem, s, qmap, p);
+    e = launch_pdl(attention_q4_wide_kernel<D>, dim3(ctas), dim3(Roles<true>::kThreads), kSmem, s, qmap, kmap, vmap, p);
     if (e != cudaSuccess) return e;
     return launch_join<D>(p, ctas, s);
 }
