@@ -11,8 +11,9 @@
 // certain key has p = 1 exactly.
 //
 // Operands of the tensor cores are binary16:
-// * a key's codes less 8, exactly; its blocks' scales multiply the blocks' dot
-//   products in fp32;
+// * a key's codes, exactly, as the numbers below binary16's normal range that
+//   their bits are where they lie; its blocks' scales multiply the blocks' dot
+//   products in fp32, and one more product takes the codes' 8 too many off;
 // * a value d (code - 8), rounded (2^-11): the format holds elements up to
 //   65504;
 // * a query row times a power of two that brings its largest element to
@@ -38,6 +39,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;  // log2 of the growth of a row's maximum that moves its reference
 constexpr int kStep = 32;     // keys a warp takes at a time
+// A nibble that is left where it is, in the low bits of a binary16, is a
+// number below its normal range: code / kCodeUnit, exactly.
+constexpr float kCodeUnit = 16777216.f;
 
 struct Params {
     CacheQ4 cache;
@@ -225,6 +229,7 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
         // q as the second operand: column g of tile n, for block j and half x
         // of it elements 4t + x, 4t + x + 2 and 16 further
         uint32_t qf[NT][NB][2][2];
+        uint32_t less[NT];
         float cs[NT][2];  // c of columns 2t and 2t + 1
         int pos[NT][2];  // their positions
 #pragma unroll
@@ -261,15 +266,37 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
             const int up = top > 0.f && top < INFINITY ? min(14 - exponent, 100) : 0;
             const float f = __uint_as_float((uint32_t)(127 + up) << 23);
             const float down = __uint_as_float((uint32_t)(127 - up) << 23);
-            const float row_c = fminf(p.scale_log2 * down, 3e38f);
+            const float row_c = fminf(p.scale_log2 * (down * kCodeUnit), 3e38f);
 #pragma unroll
             for (int x = 0; x < 2; ++x) cs[n][x] = __shfl_sync(0xffffffffu, row_c, (2 * t + x) * 4);
-            auto pair = [&](float a, float z) { return as_bits(__floats2half2_rn(a * f, z * f)); };
+            auto pair = [&](float a, float z, float f) { return pack_f16(a * f, z * f); };
+            uint32_t less_hi[NB / 2], less_lo[NB / 2];
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
-                qf[n][j][0][0] = pair(low(lo[j].x), low(lo[j].y)), qf[n][j][1][0] = pair(high(lo[j].x), high(lo[j].y));
-                qf[n][j][0][1] = pair(low(hi[j].x), low(hi[j].y)), qf[n][j][1][1] = pair(high(hi[j].x), high(hi[j].y));
+                // a high nibble is read as 16 codes
+                const float f16 = f * 0.0625f;
+                qf[n][j][0][0] = pair(low(lo[j].x), low(lo[j].y), f), qf[n][j][1][0] = pair(high(lo[j].x), high(lo[j].y), f);
+                qf[n][j][0][1] = pair(low(hi[j].x), low(hi[j].y), f16);
+                qf[n][j][1][1] = pair(high(hi[j].x), high(hi[j].y), f16);
+                // what the codes' 8 too many come to, in two binary16 parts
+                float sum = 0.f;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float2 u = __half22float2(as_half2(qf[n][j][x][0])), v = __half22float2(as_half2(qf[n][j][x][1]));
+                    sum += (u.x + u.y) + 16.f * (v.x + v.y);
+                }
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                sum *= -8.f / kCodeUnit;
+                const __half top_part = __float2half_rn(sum), rest = __float2half_rn(sum - __half2float(top_part));
+                const uint32_t at = j & 1 ? 16 : 0;
+                if (at == 0) less_hi[j / 2] = less_lo[j / 2] = 0;
+                less_hi[j / 2] |= (uint32_t)__half_as_ushort(top_part) << at;
+                less_lo[j / 2] |= (uint32_t)__half_as_ushort(rest) << at;
             }
+            // lanes t: blocks 0 and 1, then 2 and 3 (none at D = 64), of both parts
+            less[n] = t < 2 ? less_hi[t & (NB / 2 - 1)] : less_lo[t & (NB / 2 - 1)];
+            if (D == 64 && (t & 1)) less[n] = 0;
 #pragma unroll
             for (int x = 0; x < 2; ++x) pos[n][x] = s.kv - s.len + (r.row0 + n * 8 + 2 * t + x) / p.group;
         }
@@ -299,8 +326,13 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
                 } else {
                     d0[0] = lds32(st + S::kKScale + r0 * 4), d1[0] = lds32(st + S::kKScale + r1 * 4);
                 }
+                // the scales times what the codes' 8 come to
+                const uint32_t e0 = t & 1 ? d0[NB / 2 - 1] : d0[0], e1 = t & 1 ? d1[NB / 2 - 1] : d1[0];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) sc[h][n][0] = sc[h][n][1] = sc[h][n][2] = sc[h][n][3] = 0.f;
+                for (int n = 0; n < NT; ++n) {
+                    sc[h][n][0] = sc[h][n][1] = sc[h][n][2] = sc[h][n][3] = 0.f;
+                    mma16816(sc[h][n], e0, e1, 0u, 0u, less[n], 0u);
+                }
 #pragma unroll
                 for (int j = 0; j < NB; ++j) {
                     const uint32_t w0 = lds32(st + r0 * S::kRow + S::chunk(r0, j) * 16 + t * 4);
@@ -309,8 +341,8 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const uint32_t u0 = w0 >> 8 * x, u1 = w1 >> 8 * x;
-                        const uint32_t a0 = low_codes(u0, bias), a1 = low_codes(u1, bias);
-                        const uint32_t a2 = high_codes(u0, bias), a3 = high_codes(u1, bias);
+                        const uint32_t a0 = u0 & 0x000F000Fu, a1 = u1 & 0x000F000Fu;
+                        const uint32_t a2 = u0 & 0x00F000F0u, a3 = u1 & 0x00F000F0u;
 #pragma unroll
                         for (int n = 0; n < NT; ++n) mma16816(acc[n], a0, a1, a2, a3, qf[n][j][x][0], qf[n][j][x][1]);
                     }
