@@ -1136,22 +1136,6 @@ bool make_map(EncodeTiledFn enc, CUtensorMap *map, const void *base, const int64
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Codes as {byte, token of the page, key head, page}, rows swizzled over their
-// own length.
-bool make_codes_map(EncodeTiledFn enc, CUtensorMap *map, const uint8_t *base, const int64_t (&stride)[3],
-                    const KvQ4View &c, int box1) {
-    const int row = c.head_dim / 2;
-    const cuuint64_t dims[4] = {(cuuint64_t)row, (cuuint64_t)c.page_size, (cuuint64_t)c.kv_heads, (cuuint64_t)c.pages};
-    const cuuint64_t strides[3] = {(cuuint64_t)stride[2], (cuuint64_t)stride[1], (cuuint64_t)stride[0]};
-    const cuuint32_t box[4] = {(cuuint32_t)row, (cuuint32_t)box1, 1, 1};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t *>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
-
 // Rows of an item that has at most max_q_len tokens.
 int item_rows(int group, int max_q_len) {
     const int tokens = kTile / group;

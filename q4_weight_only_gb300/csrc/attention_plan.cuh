@@ -208,6 +208,8 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
+int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
+
 int current_sms() {
     int dev = 0;
     return cudaGetDevice(&dev) == cudaSuccess ? device_sm_count(dev) : 0;

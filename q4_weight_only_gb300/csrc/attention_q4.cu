@@ -25,6 +25,7 @@
 #include <cuda_fp16.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "attention_plan.cuh"
 #include "cache_q4.cuh"
@@ -38,7 +39,8 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;  // log2 of the growth of a row's maximum that moves its reference
-constexpr int kStep = 32;     // keys a warp takes at a time
+constexpr int kTile = 128;    // tokens of a key tile
+constexpr int kStep = 32;     // keys of a warp's part of one
 // A nibble that is left where it is, in the low bits of a binary16, is a
 // number below its normal range: code / kCodeUnit, exactly.
 constexpr float kCodeUnit = 16777216.f;
@@ -51,6 +53,7 @@ struct Params {
     int sequences, table_width, pages, page_size, rows, max_q_len;
     int q_heads, kv_heads, group, window, sinks;
     int most_rows;  // of a sequence; longer ones are another kernel's
+    int box;        // token rows of one copy of codes
     int item_rows;  // rows of an item: (token, head of the group) pairs of a sequence, in order
     const __nv_bfloat16 *q;
     int64_t q_row_stride, q_head_stride;
@@ -68,14 +71,13 @@ __device__ __forceinline__ int items_of(const Params &p, const Sequence &s) {
     return s.len * p.group > p.most_rows ? 0 : (s.len * p.group + p.item_rows - 1) / p.item_rows;
 }
 
-// The tokens the rows of an item see: [0, sink_end) and [lo, hi), and the
-// steps that hold them: `sink_steps` from token 0, then from step `wstep`.
+// The tokens the rows of an item see, [0, sink_end) and [lo, hi), and the key
+// tiles that hold them: `sink_tiles` from token 0, then from tile `wtile`.
 struct Range {
     int row0, rows;   // the item's first row within the sequence, and its rows
     int first, last;  // positions of its first and last row
     int lo, hi, sink_end;
-    int sink_steps, wstep, n;
-    __device__ __forceinline__ int step(int t) const { return t < sink_steps ? t : wstep + t - sink_steps; }
+    int sink_tiles, wtile, n;
 };
 
 __device__ __forceinline__ Range item_range(const Params &p, const Sequence &s, int item) {
@@ -87,10 +89,10 @@ __device__ __forceinline__ Range item_range(const Params &p, const Sequence &s, 
     r.hi = max(r.last + 1, 0);
     r.lo = p.window ? min(max(r.first - p.window + 1, 0), r.hi) : 0;
     r.sink_end = min(p.sinks, r.lo);
-    r.wstep = r.lo / kStep;
-    r.sink_steps = min((r.sink_end + kStep - 1) / kStep, r.wstep);
-    // rows that see nothing still need their output: one empty step
-    r.n = max(r.sink_steps + (r.hi + kStep - 1) / kStep - r.wstep, 1);
+    r.wtile = r.lo / kTile;
+    r.sink_tiles = min((r.sink_end + kTile - 1) / kTile, r.wtile);
+    // rows that see nothing still need their output: one empty tile
+    r.n = max(r.sink_tiles + (r.hi + kTile - 1) / kTile - r.wtile, 1);
     return r;
 }
 
@@ -99,6 +101,15 @@ __device__ __forceinline__ int largest_cost(const Params &) { return 1; }
 __device__ __forceinline__ int64_t item_cost(const Params &p, const Sequence &s, int item) {
     return item_range(p, s, item).n;
 }
+
+// A CTA's part of an item.
+struct Item {
+    int t0, t1, n;    // its key tiles [t0, t1) of the item's n; t0 == t1: the share has ended
+    int head, b;      // key head and sequence
+    int q_row, before;  // first row of q of the sequence, and the position of its first new token
+    Range r;
+    __device__ __forceinline__ int key_tile(int t) const { return t < r.sink_tiles ? t : r.wtile + t - r.sink_tiles; }
+};
 
 // ------------------------------------------------------------- instructions
 
@@ -120,110 +131,257 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 
 // --------------------------------------------------------------- the kernel
 
-// Shared memory of a warp's step: codes of 32 keys and of their values, then
-// the scales of both.
-template <int D>
-struct Stage {
-    static constexpr int kRow = D / 2;           // bytes of a token's codes
-    static constexpr int kScales = D / 16;       // bytes of its scales
-    static constexpr int kV = kStep * kRow, kKScale = 2 * kV, kVScale = kKScale + kStep * kScales;
-    static constexpr int kBytes = kVScale + kStep * kScales;
-    // Where 16-byte chunk `c` of a token's row is: tokens that a load reads
-    // at once, eight consecutive ones of a key's word, or four consecutive
-    // ones of a value's eight bytes (of which half a warp reads two chunks),
-    // are then in different banks.
+// Threads and their registers: the launch gives 168 each, the four warps that
+// copy give theirs up to the eight that compute (128 * 56 + 256 * 224 = 384 *
+// 168).
+constexpr int kThreads = 384, kComputeWarps = 8;
+constexpr int kRoleRegs = 56, kComputeRegs = 224;
+constexpr int kItems = 4;  // items handed out ahead
+
+template <int D, int NT>
+struct Layout {
+    static constexpr int kRows = NT * 8, kBlocks = D / 32, kTiles = D / 16;
+    static constexpr int kRow = D / 2, kScales = D / 16;  // bytes of a token's codes, and of its scales
+    // a tile's codes of keys and values, then the scales of both
+    static constexpr int kV = kTile * kRow, kKScale = 2 * kV, kVScale = kKScale + kTile * kScales;
+    static constexpr int kStageBytes = kVScale + kTile * kScales;
+    // each warp's O, element by element as its lanes hold it, and the merged rows
+    static constexpr int kOne = NT * kTiles * 4 * 32 * 4;
+    static constexpr int kStages = D == 128 ? (NT == 1 ? 10 : 8) : (NT == 1 ? 20 : 16);
+    static constexpr int kO = kStages * kStageBytes, kOut = kO + kComputeWarps * kOne;
+    static constexpr int kBars = kOut + kRows * D * 4, kStatBytes = 4096;
+    static constexpr int kSmem = kBars + kStatBytes + 1024;  // + alignment
+    // Where 16-byte chunk `c` of a token's row is: the swizzle of a copy whose
+    // rows are 64 (32) bytes.
     static __device__ __forceinline__ int chunk(int token, int c) {
-        if (D == 128) return c ^ ((token >> 2 & 1) | (token & 2));
-        return c ^ (token >> 2 & 1);
+        return c ^ (D == 128 ? token >> 1 & 3 : token >> 2 & 1);
+    }
+    // Token number `i` of a tile of 16 keys, by its place in the MMAs' rows: the
+    // four lanes that read two neighbouring values' words at once then read
+    // different banks, whatever the swizzle.
+    static __device__ __forceinline__ int token(int i) {
+        return D == 128 ? (i & 8) | (i & 4) | (i & 1) << 1 | (i >> 1 & 1) : (i & 8) | (i & 1) << 2 | (i >> 1 & 3);
     }
 };
 
-template <int D, int NT, int W>
-struct Narrow {
-    static constexpr int kThreads = W * 32, kRows = NT * 8, kBlocks = D / 32, kTiles = D / 16;
-    static constexpr int kStages = W == 16 ? 3 : 5;
-    static constexpr int kOut = W * kStages * Stage<D>::kBytes;  // offset of the merged rows
-    static constexpr int kSmem = kOut + kRows * D * 4;
-    static_assert(kStages * Stage<D>::kBytes >= NT * kTiles * 4 * 32 * 4, "a warp's O fits its ring");
+template <int D, int NT>
+struct Bars {
+    using L = Layout<D, NT>;
+    uint64_t full[2][L::kStages], empty[L::kStages];  // keys, values; both have been used
+    uint64_t item_full[kItems], item_empty[kItems];
+    Item item[kItems];
+    float2 warp_ml[kComputeWarps][L::kRows];  // a warp's m and l, then its factor in the merge
+    float4 row_mlc[L::kRows];
+    uint32_t fills[2];
+    int abort;
+    Start<kThreads> start;
 };
 
-// Token number `i` of a tile of 16 keys, by its place in the MMAs' rows: a
-// lane's two neighbouring keys are then four tokens apart, and the four lanes
-// that read a value's word at once read consecutive tokens.
-__device__ __forceinline__ int tile_token(int i) { return (i & 8) + (i >> 1 & 3) + (i & 1) * 4; }
-
-// W warps; rows of an item: NT tiles of 8.  A warp takes every W-th step of 32
-// keys of an item's piece with a reference, sum and O of its own, through a
-// ring of its own: no barrier but the merge at the piece's end.
-template <int D, int NT, int W>
-__global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_constant__ Params p) {
-    using N = Narrow<D, NT, W>;
-    using S = Stage<D>;
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ Start<N::kThreads> start;
-    __shared__ float2 warp_ml[W][N::kRows];   // a warp's m and l, then its factor in the merge
-    __shared__ float4 row_mlc[N::kRows];
-    constexpr int NB = N::kBlocks, MT = N::kTiles, kStages = N::kStages;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const uint32_t bias = p.cache.bias, ring = smem_u32(smem) + warp * (kStages * S::kBytes);
-    float *merged = reinterpret_cast<float *>(smem + N::kOut);
-
+// Warps: 0 copies keys and 2 values into one ring of key tiles (TMA, the
+// scales by asynchronous copies), 3 hands out the items, 4 to 11 compute.  Four
+// of these share a tile, 32 keys each, and the two fours take the tiles in
+// turn; each warp has a reference, a sum and an O of its own, which are merged
+// at the end of an item's piece.
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_q4_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                        const __grid_constant__ Params p) {
+    using L = Layout<D, NT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    Bars<D, NT> &bar = *reinterpret_cast<Bars<D, NT> *>(smem + L::kBars);
+    static_assert(sizeof(Bars<D, NT>) <= L::kStatBytes, "");
+    constexpr int NB = L::kBlocks, MT = L::kTiles, kStages = L::kStages;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile int *abort_flag = &bar.abort;
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&bar.full[0][i], 1 + 32);  // the codes' bytes, and each lane's scales
+            mbar_init(&bar.full[1][i], 1 + 32);
+            mbar_init(&bar.empty[i], kTile / kStep);
+        }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&bar.item_full[i], 1);
+            mbar_init(&bar.item_empty[i], 2 + kComputeWarps);
+        }
+        bar.abort = 0;
+        mbar_fence_init();
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
+    }
     pdl_launch_dependents();
     pdl_wait();
-    locate<N::kThreads>(p, start, blockIdx.x, gridDim.x);
-    int flags = 0;
-    int4 tail = make_int4(0, 0, 0, 0);
-    int64_t left = start.left;
-    int head = start.head, b = start.b, it = start.item, t0 = start.t0;
-    Sequence s = start.s;
-    int n_items = items_of(p, s);
+    locate<kThreads>(p, bar.start, blockIdx.x, gridDim.x);
+    __syncthreads();
 
-    while (left > 0) {
-        const Range r = item_range(p, s, it);
-        const int t1 = left >= r.n ? r.n : (int)left;
-        const int steps = t1 - t0;
-        if (t0 > 0) flags |= kHeadPiece | (t1 < r.n ? kHeadGoesOn : 0);
-        if (t0 == 0 && t1 < r.n)
-            flags |= kTailPiece, tail = make_int4(0, s.row0 * p.group + r.row0, r.rows, head);
+    uint32_t items = 0;
+    auto item = [&]() -> const Item & { return bar.item[items % kItems]; };
+    // Whether the item's record is there (false: a wait was abandoned).
+    auto item_there = [&]() {
+        return __all_sync(0xffffffffu, mbar_wait(&bar.item_full[items % kItems], items / kItems & 1, abort_flag, p.err));
+    };
+    auto done_item = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.item_empty[items % kItems]);
+        ++items;
+    };
 
-        // ------------------------------------------------------ copies
-        const KvQ4View &c = p.cache.c;
-        const uint8_t *k_base = c.k + head * c.k_stride[1], *v_base = c.v + head * c.v_stride[1];
-        const uint16_t *ks_base = c.k_scale + head * c.k_scale_stride[1];
-        const uint16_t *vs_base = c.v_scale + head * c.v_scale_stride[1];
-        const int32_t *table = p.page_table + (int64_t)b * p.table_stride;
-        // Step t0 + i of the piece into stage i / W of the warp's ring; a
-        // token no row of the item sees, or without a page, becomes zeros.
-        auto copy_step = [&](int i) {
-            if (i < steps) {
-                const uint32_t st = ring + (i / W) % kStages * S::kBytes;
-                const int token = r.step(t0 + i) * kStep + lane;
-                bool seen = token < r.sink_end || (token >= r.lo && token < r.hi);
-                const Slot at = slot_of(p.cache, table, token, seen, p.err);
-                const uint32_t all_seen = __ballot_sync(0xffffffffu, seen);
-                const uint64_t k = reinterpret_cast<uint64_t>(k_base + at.page * c.k_stride[0] + at.off * c.k_stride[2]);
-                const uint64_t v = reinterpret_cast<uint64_t>(v_base + at.page * c.v_stride[0] + at.off * c.v_stride[2]);
-                constexpr int kChunks = S::kRow / 16, kAtOnce = 32 / kChunks;
-                const int chunk = lane % kChunks;
-#pragma unroll
-                for (int j = 0; j < kStep / kAtOnce; ++j) {
-                    const int tok = j * kAtOnce + lane / kChunks;
-                    const uint64_t ka = __shfl_sync(0xffffffffu, k, tok), va = __shfl_sync(0xffffffffu, v, tok);
-                    const uint32_t to = st + tok * S::kRow + S::chunk(tok, chunk) * 16;
-                    const int bytes = all_seen >> tok & 1 ? 16 : 0;
-                    copy16(to, reinterpret_cast<const void *>(ka + chunk * 16), bytes);
-                    copy16(to + S::kV, reinterpret_cast<const void *>(va + chunk * 16), bytes);
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
+        if (warp == 0 || warp == 2) {
+            // ------------------------------------------------ copies
+            const int kv = warp >> 1;
+            const CUtensorMap *map = kv ? &vmap : &kmap;
+            const KvQ4View &c = p.cache.c;
+            const int64_t *st = kv ? c.v_scale_stride : c.k_scale_stride;
+            uint32_t fill = 0, slot = 0, phase = 1;
+            bool ok = true, open = false;
+            int t = 0;
+            const int boxes = kTile / p.box, per_load = 32 / boxes, shift = __ffs(p.box) - 1;
+            // Page numbers are loaded for 32 boxes at a time (lane i: box
+            // i % boxes of tile i / boxes) and one load ahead of the copies,
+            // across items.
+            struct Group {
+                int tiles;      // 0: the share has ended
+                int page, off;  // off < 0: a box that no row sees
+                int head;
+                int clip;       // tokens [0, a) and [b, e) of the box are seen, 7 bits each
+            };
+            auto fetch = [&]() {
+                Group o{};
+                if (!open) {
+                    if (!item_there() || item().t0 >= item().t1) return o;
+                    open = true;
+                    t = item().t0;
                 }
-                const int bytes = seen ? S::kScales : 0;
-                copy_small<S::kScales>(st + S::kKScale + lane * S::kScales,
-                                       ks_base + at.page * c.k_scale_stride[0] + at.off * c.k_scale_stride[2], bytes);
-                copy_small<S::kScales>(st + S::kVScale + lane * S::kScales,
-                                       vs_base + at.page * c.v_scale_stride[0] + at.off * c.v_scale_stride[2], bytes);
-            }
-            copy_commit();
-        };
+                const Item &i = item();
+                o.head = i.head;
+                o.tiles = min(per_load, i.t1 - t);
+                o.off = -1;
+                const int mine = lane / boxes;
+                if (mine < o.tiles) {
+                    const int tok = i.key_tile(t + mine) * kTile + (lane - mine * boxes) * p.box;
+                    if (tok < i.r.sink_end || (tok < i.r.hi && tok + p.box > i.r.lo)) {
+                        const int index = tok / p.page_size;
+                        o.page = p.page_table[(int64_t)i.b * p.table_stride + index];
+                        o.off = tok - index * p.page_size;
+                        const int a = min(max(i.r.sink_end - tok, 0), p.box);
+                        const int b = max(i.r.lo - tok, 0), e = min(i.r.hi - tok, p.box);
+                        o.clip = a | min(b, p.box) << 7 | e << 14;
+                    }
+                }
+                t += o.tiles;
+                if (t == i.t1) {
+                    open = false;
+                    done_item();
+                }
+                return o;
+            };
+            Group now = fetch();
+            while (ok && now.tiles) {
+                const Group then = fetch();
+                if (now.off < 0 || now.page < 0 || now.page >= p.pages) {
+                    // a page coordinate past the end reads zeros
+                    if (now.off >= 0) report_index(p.err);
+                    now.page = p.pages, now.off = 0;
+                }
+                const uint16_t *base = (kv ? c.v_scale : c.k_scale) + now.head * st[1];
+                for (int j = 0; j < now.tiles; ++j) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bar.empty[slot], phase, abort_flag, p.err));
+                    if (!ok) break;
+                    const bool issue = elect_one();
+                    uint8_t *dst = smem + slot * L::kStageBytes + (kv ? L::kV : 0);
+                    if (issue) mbar_arrive_expect_tx(&bar.full[kv][slot], kTile * L::kRow);
+                    for (int i = 0; i < boxes; ++i, dst += p.box * L::kRow) {
+                        const int page = __shfl_sync(0xffffffffu, now.page, j * boxes + i);
+                        const int off = __shfl_sync(0xffffffffu, now.off, j * boxes + i);
+                        if (issue) tma_load_4d(dst, map, 0, off, now.head, page, &bar.full[kv][slot]);
+                    }
+                    // Scales of the tokens that some row sees.  Others' become
+                    // zeros: their values may be anything (0 * NaN).
+                    const uint32_t to = smem_u32(smem + slot * L::kStageBytes + (kv ? L::kVScale : L::kKScale));
 #pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) copy_step(warp + i * W);
+                    for (int i = 0; i < kTile / 32; ++i) {
+                        const int tok = i * 32 + lane, box = tok >> shift, in_box = tok & (p.box - 1);
+                        const int page = __shfl_sync(0xffffffffu, now.page, j * boxes + box);
+                        const int off = __shfl_sync(0xffffffffu, now.off, j * boxes + box) + in_box;
+                        const int clip = __shfl_sync(0xffffffffu, now.clip, j * boxes + box);
+                        const bool seen = page < p.pages && (in_box < (clip & 127) || (in_box >= (clip >> 7 & 127) &&
+                                                                                       in_box < clip >> 14));
+                        copy_small<L::kScales>(to + tok * L::kScales,
+                                               base + (seen ? page * st[0] + off * st[2] : 0), seen ? L::kScales : 0);
+                    }
+                    copy_arrive(&bar.full[kv][slot]);
+                    ++fill;
+                    if (++slot == kStages) slot = 0, phase ^= 1;
+                }
+                now = then;
+            }
+            if (lane == 0) bar.fills[kv] = fill;
+        } else if (warp == 3) {
+            // ------------------------------------------------- items
+            int flags = 0;
+            int4 tail = make_int4(0, 0, 0, 0);
+            int64_t left = bar.start.left;
+            int head = bar.start.head, b = bar.start.b, it = bar.start.item, t0 = bar.start.t0;
+            Sequence s = bar.start.s;
+            int n_items = items_of(p, s);
+            for (;; ++items) {
+                Item o{};
+                if (left > 0) {
+                    o.r = item_range(p, s, it);
+                    o.t0 = t0, o.t1 = left >= o.r.n ? o.r.n : (int)left, o.n = o.r.n;
+                    o.head = head, o.b = b, o.q_row = s.row0, o.before = s.kv - s.len;
+                    if (o.t0 > 0) flags |= kHeadPiece | (o.t1 < o.n ? kHeadGoesOn : 0);
+                    if (o.t0 == 0 && o.t1 < o.n)
+                        flags |= kTailPiece, tail = make_int4(0, s.row0 * p.group + o.r.row0, o.r.rows, head);
+                }
+                const int i = items % kItems;
+                if (!__all_sync(0xffffffffu,
+                                mbar_wait(&bar.item_empty[i], (items / kItems & 1) ^ 1, abort_flag, p.err)))
+                    break;
+                if (lane == 0) {
+                    bar.item[i] = o;
+                    mbar_arrive(&bar.item_full[i]);
+                }
+                __syncwarp();
+                if (o.t0 == o.t1) break;
+                left -= o.n;
+                t0 = 0;
+                if (left > 0 && ++it >= n_items) {
+                    it = 0;
+                    int scanned = 0;
+                    do {
+                        if (++b >= p.sequences) {
+                            b = 0;
+                            ++head;
+                        }
+                        s = sequence(p, b);
+                        n_items = items_of(p, s);
+                    } while (n_items == 0 && ++scanned <= p.sequences);
+                }
+            }
+            tail.x = flags;
+            if (lane == 0) p.record[blockIdx.x] = tail;
+        }
+    } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
+    const int g = lane >> 2, t = lane & 3, ctid = tid - 128, cwarp = warp - 4;
+    const int part = cwarp & 3, turn = cwarp >> 2;  // keys of a tile, and which of two tiles
+    const uint32_t bias = p.cache.bias, ring = smem_u32(smem);
+    float *merged = reinterpret_cast<float *>(smem + L::kOut);
+    uint32_t fill = 0;       // tiles of earlier items
+    uint32_t slot = turn, phase = 0;  // of the warp's next tile
+    // Every warp takes part in an item's barriers, also one whose wait was
+    // given up: it only leaves its sums as they are.
+    for (;; done_item()) {
+        if (named_bar_or(1, kComputeWarps * 32, !item_there())) break;
+        const Item &i = item();
+        const int t0 = i.t0, t1 = i.t1, tiles = t1 - t0, head = i.head;
+        if (tiles <= 0) break;
+        const Range r = i.r;
+        const int q_row = i.q_row, before = i.before;
 
         // ---------------------------------------------------- queries
         // q as the second operand: column g of tile n, for block j and half x
@@ -242,7 +400,7 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
             if (row < r.rows) {
                 const int token = (r.row0 + row) / p.group, in_group = r.row0 + row - token * p.group;
                 const __nv_bfloat16 *src =
-                    p.q + (s.row0 + token) * p.q_row_stride + (head * p.group + in_group) * p.q_head_stride;
+                    p.q + (q_row + token) * p.q_row_stride + (head * p.group + in_group) * p.q_head_stride;
 #pragma unroll
                 for (int j = 0; j < NB; ++j) {
                     lo[j] = *reinterpret_cast<const uint2 *>(src + 32 * j + 4 * t);
@@ -298,7 +456,7 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
             less[n] = t < 2 ? less_hi[t & (NB / 2 - 1)] : less_lo[t & (NB / 2 - 1)];
             if (D == 64 && (t & 1)) less[n] = 0;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) pos[n][x] = s.kv - s.len + (r.row0 + n * 8 + 2 * t + x) / p.group;
+            for (int x = 0; x < 2; ++x) pos[n][x] = before + (r.row0 + n * 8 + 2 * t + x) / p.group;
         }
 
         // -------------------------------------------------------- keys
@@ -309,22 +467,23 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
         }
-        for (int i = warp; i < steps; i += W) {
-            copy_step(i + (kStages - 1) * W);
-            copy_wait<kStages - 1>();
-            __syncwarp();
-            const uint32_t st = ring + (i / W) % kStages * S::kBytes;
+        for (int tile = (fill & 1) == (uint32_t)turn ? 0 : 1; tile < tiles; tile += 2) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&bar.full[0][slot], phase, abort_flag, p.err))) break;
+            const uint32_t st = ring + slot * L::kStageBytes;
+            const uint32_t k_codes = st + part * kStep * L::kRow, v_codes = k_codes + L::kV;
+            const uint32_t k_scales = st + L::kKScale + part * kStep * L::kScales;
+            const uint32_t v_scales = st + L::kVScale + part * kStep * L::kScales;
             // scores: keys by queries, two tiles of 16 keys
             float sc[2][NT][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int r0 = h * 16 + tile_token(g), r1 = r0 + 8;
+                const int r0 = h * 16 + L::token(g), r1 = r0 + 8;
                 uint32_t d0[NB / 2], d1[NB / 2];
                 if (D == 128) {
-                    const uint2 x = lds64(st + S::kKScale + r0 * 8), y = lds64(st + S::kKScale + r1 * 8);
+                    const uint2 x = lds64(k_scales + r0 * 8), y = lds64(k_scales + r1 * 8);
                     d0[0] = x.x, d0[NB / 2 - 1] = x.y, d1[0] = y.x, d1[NB / 2 - 1] = y.y;
                 } else {
-                    d0[0] = lds32(st + S::kKScale + r0 * 4), d1[0] = lds32(st + S::kKScale + r1 * 4);
+                    d0[0] = lds32(k_scales + r0 * 4), d1[0] = lds32(k_scales + r1 * 4);
                 }
                 // the scales times what the codes' 8 come to
                 const uint32_t e0 = t & 1 ? d0[NB / 2 - 1] : d0[0], e1 = t & 1 ? d1[NB / 2 - 1] : d1[0];
@@ -335,8 +494,8 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
                 }
 #pragma unroll
                 for (int j = 0; j < NB; ++j) {
-                    const uint32_t w0 = lds32(st + r0 * S::kRow + S::chunk(r0, j) * 16 + t * 4);
-                    const uint32_t w1 = lds32(st + r1 * S::kRow + S::chunk(r1, j) * 16 + t * 4);
+                    const uint32_t w0 = lds32(k_codes + r0 * L::kRow + L::chunk(r0, j) * 16 + t * 4);
+                    const uint32_t w1 = lds32(k_codes + r1 * L::kRow + L::chunk(r1, j) * 16 + t * 4);
                     float acc[NT][4] = {};
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
@@ -356,7 +515,7 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
                     }
                 }
             }
-            const int tok0 = r.step(t0 + i) * kStep;
+            const int tok0 = i.key_tile(t0 + tile) * kTile + part * kStep;
             if (tok0 + kStep - 1 > r.first || (p.window && tok0 <= r.last - p.window && tok0 + kStep > p.sinks)) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -364,7 +523,7 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            const int tok = tok0 + h * 16 + tile_token(g) + (x >> 1) * 8, at = pos[n][x & 1];
+                            const int tok = tok0 + h * 16 + L::token(g) + (x >> 1) * 8, at = pos[n][x & 1];
                             if (tok > at || (p.window && tok <= at - p.window && tok >= p.sinks)) sc[h][n][x] = -INFINITY;
                         }
             }
@@ -417,19 +576,20 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
             }
             // values: a lane's 16 (D = 64: 8) elements of a token are 8 (4)
             // bytes, all of one block
+            if (!__all_sync(0xffffffffu, mbar_wait(&bar.full[1][slot], phase, abort_flag, p.err))) break;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t w[4][D / 64], d[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int tok = h * 16 + t + 4 * k;
+                    const int tok = h * 16 + L::token(2 * t + (k & 1)) + (k >> 1) * 8;
                     if (D == 128) {
-                        const uint2 x = lds64(st + S::kV + tok * S::kRow + S::chunk(tok, g >> 1) * 16 + (g & 1) * 8);
+                        const uint2 x = lds64(v_codes + tok * L::kRow + L::chunk(tok, g >> 1) * 16 + (g & 1) * 8);
                         w[k][0] = x.x, w[k][D / 64 - 1] = x.y;
-                        d[k] = lds16(st + S::kVScale + tok * 8 + (g >> 1) * 2);
+                        d[k] = lds16(v_scales + tok * 8 + (g >> 1) * 2);
                     } else {
-                        w[k][0] = lds32(st + S::kV + tok * S::kRow + S::chunk(tok, g >> 2) * 16 + (g & 3) * 4);
-                        d[k] = lds16(st + S::kVScale + tok * 4 + (g >> 2) * 2);
+                        w[k][0] = lds32(v_codes + tok * L::kRow + L::chunk(tok, g >> 2) * 16 + (g & 3) * 4);
+                        d[k] = lds16(v_scales + tok * 4 + (g >> 2) * 2);
                     }
                 }
                 const __half2 d01 = as_half2(__byte_perm(d[0], d[1], 0x5410)), d23 = as_half2(__byte_perm(d[2], d[3], 0x5410));
@@ -450,15 +610,16 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
                         }
                     }
             }
+            // (the stage's words have all been used)
             __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.empty[slot]);
+            slot += 2;
+            if (slot >= kStages) slot -= kStages, phase ^= 1;
         }
-        copy_wait<0>();
+        fill += tiles;
 
         // ------------------------------------------------------- merge
-        // the warps' O into their rings, element by element as the lanes
-        // hold them
-        float *mine = reinterpret_cast<float *>(smem + warp * (kStages * S::kBytes));
-        __syncwarp();
+        float *mine = reinterpret_cast<float *>(smem + L::kO + cwarp * L::kOne);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -470,50 +631,53 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
 #pragma unroll
                 for (int d = 4; d <= 16; d <<= 1) l[n][x] += __shfl_xor_sync(0xffffffffu, l[n][x], d);
                 if (g == 0) {
-                    warp_ml[warp][n * 8 + 2 * t + x] = make_float2(m[n][x], l[n][x]);
-                    if (warp == 0) row_mlc[n * 8 + 2 * t + x].z = cs[n][x];
+                    bar.warp_ml[cwarp][n * 8 + 2 * t + x] = make_float2(m[n][x], l[n][x]);
+                    if (cwarp == 0) bar.row_mlc[n * 8 + 2 * t + x].z = cs[n][x];
                 }
             }
         }
-        __syncthreads();
-        const bool whole = t0 == 0 && t1 == r.n;
-        if (tid < N::kRows) {
-            const float row_c = row_mlc[tid].z;
+        named_bar_sync(1, kComputeWarps * 32);
+        const bool whole = t0 == 0 && t1 == i.n;
+        if (ctid < L::kRows) {
+            const float row_c = bar.row_mlc[ctid].z;
             float top = -INFINITY, sum = 0.f;
-            for (int w = 0; w < W; ++w) top = fmaxf(top, warp_ml[w][tid].x);
-            for (int w = 0; w < W; ++w) {
-                const float2 ml = warp_ml[w][tid];
-                // a warp without a step has no reference, and a sum of 0
+#pragma unroll
+            for (int w = 0; w < kComputeWarps; ++w) top = fmaxf(top, bar.warp_ml[w][ctid].x);
+#pragma unroll
+            for (int w = 0; w < kComputeWarps; ++w) {
+                const float2 ml = bar.warp_ml[w][ctid];
+                // a warp without a tile has no reference, and a sum of 0
                 const float f = ml.x == top ? 1.f : ex2((ml.x - top) * row_c);
                 sum += ml.y * f;
-                warp_ml[w][tid].x = f;
+                bar.warp_ml[w][ctid].x = f;
             }
             const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
             if (whole)
-                for (int w = 0; w < W; ++w) warp_ml[w][tid].x *= inv;
-            row_mlc[tid].x = top, row_mlc[tid].y = sum;
+                for (int w = 0; w < kComputeWarps; ++w) bar.warp_ml[w][ctid].x *= inv;
+            bar.row_mlc[ctid].x = top, bar.row_mlc[ctid].y = sum;
         }
-        __syncthreads();
-        const float *rings = reinterpret_cast<const float *>(smem);
-        for (int e = tid; e < N::kRows * D; e += N::kThreads) {
+        named_bar_sync(1, kComputeWarps * 32);
+        const float *parts = reinterpret_cast<const float *>(smem + L::kO);
+        for (int e = ctid; e < L::kRows * D; e += kComputeWarps * 32) {
             const int le = e & 31, x = e >> 5 & 3, j = (e >> 7) % MT, n = (e >> 7) / MT, gg = le >> 2;
             const int row = n * 8 + 2 * (le & 3) + (x & 1);
             float v = 0.f;
-            for (int w = 0; w < W; ++w) v = fmaf(warp_ml[w][row].x, rings[w * (kStages * S::kBytes / 4) + e], v);
+#pragma unroll
+            for (int w = 0; w < kComputeWarps; ++w) v = fmaf(bar.warp_ml[w][row].x, parts[w * (L::kOne / 4) + e], v);
             // the lane's byte of its block, and the element it holds
             const int byte = (D == 128 ? 8 * (gg & 1) : 4 * (gg & 3)) + j;
             const int d = (D == 128 ? 32 * (gg >> 1) : 32 * (gg >> 2)) + byte + (x >> 1) * 16;
             merged[row * D + d] = v;
         }
-        __syncthreads();
-        const int f0 = s.row0 * p.group + r.row0;
+        named_bar_sync(1, kComputeWarps * 32);
+        const int f0 = q_row * p.group + r.row0;
         const int piece = (blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * p.item_rows;
         // place of a row of the item in [rows][q_heads]
         auto place = [&](int row) {
             const int token = (f0 + row) / p.group;
             return (int64_t)token * p.q_heads + head * p.group + (f0 + row - token * p.group);
         };
-        for (int e = tid * 4; e < r.rows * D; e += N::kThreads * 4) {
+        for (int e = ctid * 4; e < r.rows * D; e += kComputeWarps * 32 * 4) {
             const int row = e / D, d = e - row * D;
             const float4 v = *reinterpret_cast<const float4 *>(merged + e);
             const int64_t at = place(row) * D + d;
@@ -525,43 +689,35 @@ __global__ void __launch_bounds__(W * 32, 1) attention_q4_kernel(const __grid_co
             else
                 *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = v;
         }
-        if (tid < r.rows) {
-            const float4 mlc = row_mlc[tid];
+        if (ctid < r.rows) {
+            const float4 mlc = bar.row_mlc[ctid];
             if (!whole)
-                p.part_mlc[piece + tid] = mlc;
+                p.part_mlc[piece + ctid] = mlc;
             else if (p.lse)
-                p.lse[place(tid)] = (mlc.x * mlc.z + __log2f(mlc.y)) * kLn2;
-        }
-        __syncthreads();
-
-        // -------------------------------------------------- next item
-        left -= r.n;
-        t0 = 0;
-        if (left > 0 && ++it >= n_items) {
-            it = 0;
-            int scanned = 0;
-            do {
-                if (++b >= p.sequences) {
-                    b = 0;
-                    ++head;
-                }
-                s = sequence(p, b);
-            } while (items_of(p, s) == 0 && ++scanned <= p.sequences);
-            n_items = items_of(p, s);
+                p.lse[place(ctid)] = (mlc.x * mlc.z + __log2f(mlc.y)) * kLn2;
         }
     }
-    tail.x = flags;
-    if (tid == 0) p.record[blockIdx.x] = tail;
+    }
+    __syncthreads();
+    if (bar.abort && tid == 0) {
+        // a wait was abandoned: copies in flight land before the CTA exits
+        // (otherwise every copy was waited for by its readers)
+        for (int kv = 0; kv < 2; ++kv)
+            for (uint32_t f = max(bar.fills[kv], (uint32_t)kStages) - kStages; f < bar.fills[kv]; ++f)
+                mbar_drain(&bar.full[kv][f % kStages], f / kStages & 1);
+    }
 }
 
 // Adds the pieces of the items that a share's boundary cut.  blockIdx.x: the
-// CTA whose tail piece starts the item; a warp takes every (gridDim.y * 8)-th
-// of its rows.
+// CTA whose tail piece starts the item, blockIdx.y: a row of it; its warps take
+// the pieces in turn.  Latency bounds it: the records, then a row's (m, l, c)
+// and pieces of O at once.
 template <int D>
 __global__ void __launch_bounds__(256) attention_q4_join_kernel(const __grid_constant__ Params p, int ctas) {
+    __shared__ float sums[8][D];
     pdl_launch_dependents();
     pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y;
     const int4 rec = p.record[blockIdx.x];
     // pieces: this CTA's tail, then the heads of the next ones
     int n = 1;
@@ -578,58 +734,62 @@ __global__ void __launch_bounds__(256) attention_q4_join_kernel(const __grid_con
             more = false;
         }
     }
-    if (!(rec.x & kTailPiece)) return;
+    if (!(rec.x & kTailPiece) || row >= rec.z) return;
     constexpr int kOwn = D / 32;
-    auto place = [&](int i, int r) { return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * p.item_rows + r; };
-    for (int row = blockIdx.y * 8 + warp; row < rec.z; row += gridDim.y * 8) {
-        float m = -INFINITY;
-        for (int i = lane; i < n; i += 32) m = fmaxf(m, p.part_mlc[place(i, row)].x);
+    using Own = typename std::conditional<kOwn == 4, float4, float2>::type;
+    auto place = [&](int i) { return (int64_t)((blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * p.item_rows + row; };
+    auto piece = [&](int i) { return *reinterpret_cast<const Own *>(p.part + place(i) * D + lane * kOwn); };
+    // the warp's first pieces are read with the statistics
+    Own first[4];
 #pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        float acc[kOwn] = {}, l = 0.f, c = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float4 mlc = p.part_mlc[place(i, row)];
-            const float *src = p.part + place(i, row) * D + lane * kOwn;
-            float v[kOwn];
+    for (int k = 0; k < 4; ++k) first[k] = piece(min(warp + 8 * k, n - 1));
+    float m = -INFINITY;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, p.part_mlc[place(i)].x);
 #pragma unroll
-            for (int e = 0; e < kOwn; e += 2) {
-                const float2 x = *reinterpret_cast<const float2 *>(src + e);
-                v[e] = x.x, v[e + 1] = x.y;
-            }
-            c = mlc.z;
-            const float f = mlc.x == m ? 1.f : ex2((mlc.x - m) * c);
-            l += mlc.y * f;
-#pragma unroll
-            for (int e = 0; e < kOwn; ++e) acc[e] = fmaf(v[e], f, acc[e]);
-        }
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-        const int token = (rec.y + row) / p.group;
-        const int64_t at = (int64_t)token * p.q_heads + rec.w * p.group + (rec.y + row - token * p.group);
-#pragma unroll
-        for (int e = 0; e < kOwn; e += 2) {
-            const int64_t to = at * D + lane * kOwn + e;
-            if (p.out_bf16)
-                *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.out) + to) =
-                    pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-            else
-                *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + to) = make_float2(acc[e] * inv, acc[e + 1] * inv);
-        }
-        if (p.lse && lane == 0) p.lse[at] = (m * c + __log2f(l)) * kLn2;
+    for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    float l = 0.f;
+    const float c = p.part_mlc[place(0)].z;
+    auto factor = [&](float x) { return x == m ? 1.f : ex2((x - m) * c); };
+    for (int i = lane; i < n; i += 32) {
+        const float4 mlc = p.part_mlc[place(i)];
+        l += mlc.y * factor(mlc.x);
     }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    float acc[kOwn] = {};
+    auto add = [&](const Own &v, int i) {
+        const float *o = reinterpret_cast<const float *>(&v), f = factor(p.part_mlc[place(i)].x);
+#pragma unroll
+        for (int e = 0; e < kOwn; ++e) acc[e] = fmaf(o[e], f, acc[e]);
+    };
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (warp + 8 * k < n) add(first[k], warp + 8 * k);
+    for (int i = warp + 32; i < n; i += 8) add(piece(i), i);
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) sums[warp][lane * kOwn + e] = acc[e];
+    __syncthreads();
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    const int token = (rec.y + row) / p.group;
+    const int64_t at = (int64_t)token * p.q_heads + rec.w * p.group + (rec.y + row - token * p.group);
+    const int d = threadIdx.x;
+    if (d < D) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) v += sums[w][d];
+        store_y(static_cast<float *>(p.out), at * D + d, v * inv, p.out_bf16);
+    }
+    if (p.lse && d == 0) p.lse[at] = (m * c + __log2f(l)) * kLn2;
 }
 
 // -------------------------------------------------------------------- host
 
-// Rows (tokens times heads of the group) of the sequences that these kernels
-// take; those of longer ones fill tcgen05's tiles (attention.cu).
-constexpr int kMostRows = 32;
+// Rows (tokens times heads of the group) of the sequences that this kernel
+// takes; those of longer ones fill tcgen05's tiles (attention.cu).
+constexpr int kMostRows = 16;
 
 // Rows of an item: tiles of 8, as few as hold the rows of a sequence.
-int item_rows(int group, int max_q_len) {
-    const int64_t rows = (int64_t)group * max_q_len;
-    return rows <= 8 ? 8 : rows <= 16 ? 16 : kMostRows;
-}
+int item_rows(int group, int max_q_len) { return (int64_t)group * max_q_len <= 8 ? 8 : kMostRows; }
 
 struct WorkspaceLayout {
     size_t mlc_off, rec_off, bytes;
@@ -641,12 +801,12 @@ struct WorkspaceLayout {
     }
 };
 
-template <int D, int NT, int W>
-cudaError_t launch_narrow(const Params &p, int ctas, cudaStream_t s) {
-    using N = Narrow<D, NT, W>;
-    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(attention_q4_kernel<D, NT, W>), N::kSmem);
+template <int D, int NT>
+cudaError_t launch_narrow(const CUtensorMap &kmap, const CUtensorMap &vmap, const Params &p, int ctas, cudaStream_t s) {
+    constexpr int kSmem = Layout<D, NT>::kSmem;
+    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(attention_q4_kernel<D, NT>), kSmem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attention_q4_kernel<D, NT, W>, dim3(ctas), dim3(N::kThreads), N::kSmem, s, p);
+    return launch_pdl(attention_q4_kernel<D, NT>, dim3(ctas), dim3(kThreads), kSmem, s, kmap, vmap, p);
 }
 
 template <int D>
@@ -669,11 +829,16 @@ cudaError_t launch_d(const AttentionArgs &a, const KvQ4View &c, void *workspace,
     p.part_mlc = reinterpret_cast<float4 *>(ws + w.mlc_off);
     p.record = reinterpret_cast<int4 *>(ws + w.rec_off);
     p.err = err;
-    cudaError_t e = p.item_rows == 8    ? launch_narrow<D, 1, 16>(p, ctas, s)
-                    : p.item_rows == 16 ? launch_narrow<D, 2, 8>(p, ctas, s)
-                                        : launch_narrow<D, 4, 8>(p, ctas, s);
+    p.box = gcd(c.page_size, 64);
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    CUtensorMap kmap, vmap;
+    if (!make_codes_map(enc, &kmap, c.k, c.k_stride, c, p.box) || !make_codes_map(enc, &vmap, c.v, c.v_stride, c, p.box))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = p.item_rows == 8 ? launch_narrow<D, 1>(kmap, vmap, p, ctas, s)
+                                           : launch_narrow<D, 2>(kmap, vmap, p, ctas, s);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attention_q4_join_kernel<D>, dim3(ctas, p.item_rows / 8), dim3(256), 0, s, p, ctas);
+    return launch_pdl(attention_q4_join_kernel<D>, dim3(ctas, p.item_rows), dim3(256), 0, s, p, ctas);
 }
 
 }  // namespace

@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include "attention_plan.cuh"
 #include "q4_0_internal.h"
 #include "q4_0_ptx.cuh"
 
@@ -12,61 +13,38 @@ namespace q4_0 {
 
 namespace {
 
-// The cache with what divides a token's number by the page size: t /
-// page_size = umulhi(t, magic) >> shift for t < 2^31.
+// The cache as the attention kernels take it.
 struct CacheQ4 {
     KvQ4View c;
-    uint32_t page_magic, page_shift;
     uint32_t bias;  // kNibbleBias
 };
+inline CacheQ4 cache_q4(const KvQ4View &c) { return CacheQ4{c, kNibbleBias}; }
 
-inline CacheQ4 cache_q4(const KvQ4View &c) {
-    CacheQ4 r{c, 0, 0, kNibbleBias};
-    // with 2^s < page_size <= 2^(s + 1), floor(t m / 2^(32 + s)) for m the next
-    // whole number from 2^(32 + s) / page_size; page_size is at least 8
-    while ((2 << r.page_shift) < c.page_size) ++r.page_shift;
-    r.page_magic = (uint32_t)(((1ull << (32 + r.page_shift)) + c.page_size - 1) / c.page_size);
-    return r;
+// Codes as {byte, token of the page, key head, page}, rows swizzled over their
+// own length.
+bool make_codes_map(EncodeTiledFn enc, CUtensorMap *map, const uint8_t *base, const int64_t (&stride)[3],
+                    const KvQ4View &c, int box1) {
+    const int row = c.head_dim / 2;
+    const cuuint64_t dims[4] = {(cuuint64_t)row, (cuuint64_t)c.page_size, (cuuint64_t)c.kv_heads, (cuuint64_t)c.pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)stride[2], (cuuint64_t)stride[1], (cuuint64_t)stride[0]};
+    const cuuint32_t box[4] = {(cuuint32_t)row, (cuuint32_t)box1, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Page and slot of a token of a sequence; a page out of range is reported and
-// `ok` is cleared.
-struct Slot {
-    int page, off;
-};
-__device__ __forceinline__ Slot slot_of(const CacheQ4 &c, const int32_t *table, int token, bool &ok, unsigned int *err) {
-    Slot s{0, 0};
-    if (!ok) return s;
-    const int index = __umulhi((uint32_t)token, c.page_magic) >> c.page_shift;
-    s.page = table[index], s.off = token - index * c.c.page_size;
-    if (s.page < 0 || s.page >= c.c.pages) {
-        report_index(err);
-        ok = false;
-        s = Slot{0, 0};
-    }
-    return s;
-}
-
-// Asynchronous copies of 16, 8 or 4 bytes; nothing is read and zeros are
-// written where `bytes` is 0.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
+// An asynchronous copy of 8 or 4 bytes; nothing is read and zeros are written
+// where `bytes` is 0.
 template <int kBytes>
 __device__ __forceinline__ void copy_small(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // An arrival on `bar` once the thread's copies so far have landed (one of the
 // arrivals that the barrier counts).
 __device__ __forceinline__ void copy_arrive(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-template <int kLeft>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
-}
-
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
