@@ -53,7 +53,6 @@ struct Params {
     int sequences, table_width, pages, page_size, rows, max_q_len;
     int q_heads, kv_heads, group, window, sinks;
     int most_rows;  // of a sequence; longer ones are another kernel's
-    int box;        // token rows of one copy of codes
     int item_rows;  // rows of an item: (token, head of the group) pairs of a sequence, in order
     const __nv_bfloat16 *q;
     int64_t q_row_stride, q_head_stride;
@@ -132,10 +131,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 // --------------------------------------------------------------- the kernel
 
 // Threads and their registers: the launch gives 168 each, the four warps that
-// copy give theirs up to the eight that compute (128 * 56 + 256 * 224 = 384 *
+// copy give theirs up to the eight that compute (128 * 72 + 256 * 216 = 384 *
 // 168).
 constexpr int kThreads = 384, kComputeWarps = 8;
-constexpr int kRoleRegs = 56, kComputeRegs = 224;
+constexpr int kCopyRegs = 72, kComputeRegs = 216;
+constexpr int kParts = kTile / kStep;  // of a tile: one copying warp's and one computing warp's
 constexpr int kItems = 4;  // items handed out ahead
 
 template <int D, int NT>
@@ -167,25 +167,26 @@ struct Layout {
 template <int D, int NT>
 struct Bars {
     using L = Layout<D, NT>;
-    uint64_t full[2][L::kStages], empty[L::kStages];  // keys, values; both have been used
+    uint64_t full[kParts][L::kStages], empty[kParts][L::kStages];
     uint64_t item_full[kItems], item_empty[kItems];
     Item item[kItems];
     float2 warp_ml[kComputeWarps][L::kRows];  // a warp's m and l, then its factor in the merge
     float4 row_mlc[L::kRows];
-    uint32_t fills[2];
     int abort;
     Start<kThreads> start;
 };
 
-// Warps: 0 copies keys and 2 values into one ring of key tiles (TMA, the
-// scales by asynchronous copies), 3 hands out the items, 4 to 11 compute.  Four
-// of these share a tile, 32 keys each, and the two fours take the tiles in
-// turn; each warp has a reference, a sum and an O of its own, which are merged
-// at the end of an item's piece.
+// Warps: 0 to 3 copy, each 32 tokens of every key tile, into one ring; 0 hands
+// out the items too.  4 to 11 compute: four share a tile, 32 keys each, and the
+// two fours take the tiles in turn.  Each has a reference, a sum and an O of
+// its own, which are merged at the end of an item's piece.
+//
+// The copies are asynchronous ones of 16 bytes a lane: a row of codes is 64
+// (32) bytes, and tensor copies took 4.6 cycles a row whatever its length (64
+// requests of up to 32768 tokens: copies alone 300 us against 234).
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
-    attention_q4_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                        const __grid_constant__ Params p) {
+    attention_q4_kernel(const __grid_constant__ Params p) {
     using L = Layout<D, NT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -196,19 +197,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int *abort_flag = &bar.abort;
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(&bar.full[0][i], 1 + 32);  // the codes' bytes, and each lane's scales
-            mbar_init(&bar.full[1][i], 1 + 32);
-            mbar_init(&bar.empty[i], kTile / kStep);
+        for (int i = 0; i < kParts * kStages; ++i) {
+            mbar_init(&bar.full[0][i], 32);  // each lane's copies
+            mbar_init(&bar.empty[0][i], 1);
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&bar.item_full[i], 1);
-            mbar_init(&bar.item_empty[i], 2 + kComputeWarps);
+            mbar_init(&bar.item_empty[i], kParts + kComputeWarps);
         }
         bar.abort = 0;
         mbar_fence_init();
-        tma_prefetch_desc(&kmap);
-        tma_prefetch_desc(&vmap);
     }
     pdl_launch_dependents();
     pdl_wait();
@@ -227,141 +225,122 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++items;
     };
 
-    if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
-        if (warp == 0 || warp == 2) {
-            // ------------------------------------------------ copies
-            const int kv = warp >> 1;
-            const CUtensorMap *map = kv ? &vmap : &kmap;
-            const KvQ4View &c = p.cache.c;
-            const int64_t *st = kv ? c.v_scale_stride : c.k_scale_stride;
-            uint32_t fill = 0, slot = 0, phase = 1;
-            bool ok = true, open = false;
-            int t = 0;
-            const int boxes = kTile / p.box, per_load = 32 / boxes, shift = __ffs(p.box) - 1;
-            // Page numbers are loaded for 32 boxes at a time (lane i: box
-            // i % boxes of tile i / boxes) and one load ahead of the copies,
-            // across items.
-            struct Group {
-                int tiles;      // 0: the share has ended
-                int page, off;  // off < 0: a box that no row sees
-                int head;
-                int clip;       // tokens [0, a) and [b, e) of the box are seen, 7 bits each
-            };
-            auto fetch = [&]() {
-                Group o{};
-                if (!open) {
-                    if (!item_there() || item().t0 >= item().t1) return o;
-                    open = true;
-                    t = item().t0;
-                }
-                const Item &i = item();
-                o.head = i.head;
-                o.tiles = min(per_load, i.t1 - t);
-                o.off = -1;
-                const int mine = lane / boxes;
-                if (mine < o.tiles) {
-                    const int tok = i.key_tile(t + mine) * kTile + (lane - mine * boxes) * p.box;
-                    if (tok < i.r.sink_end || (tok < i.r.hi && tok + p.box > i.r.lo)) {
-                        const int index = tok / p.page_size;
-                        o.page = p.page_table[(int64_t)i.b * p.table_stride + index];
-                        o.off = tok - index * p.page_size;
-                        const int a = min(max(i.r.sink_end - tok, 0), p.box);
-                        const int b = max(i.r.lo - tok, 0), e = min(i.r.hi - tok, p.box);
-                        o.clip = a | min(b, p.box) << 7 | e << 14;
+    if (warp < kParts) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
+        // ------------------------------------------------------ items
+        int flags = 0;
+        int4 tail = make_int4(0, 0, 0, 0);
+        int64_t left = bar.start.left;
+        int head = bar.start.head, b = bar.start.b, it = bar.start.item, t0 = bar.start.t0;
+        Sequence s = bar.start.s;
+        int n_items = items_of(p, s);
+        uint32_t handed = 0;
+        // Hands out the next item, or one without tiles at the share's end;
+        // false after that and when a wait was abandoned.
+        auto publish = [&]() {
+            Item o{};
+            if (left > 0) {
+                o.r = item_range(p, s, it);
+                o.t0 = t0, o.t1 = left >= o.r.n ? o.r.n : (int)left, o.n = o.r.n;
+                o.head = head, o.b = b, o.q_row = s.row0, o.before = s.kv - s.len;
+                if (o.t0 > 0) flags |= kHeadPiece | (o.t1 < o.n ? kHeadGoesOn : 0);
+                if (o.t0 == 0 && o.t1 < o.n)
+                    flags |= kTailPiece, tail = make_int4(0, s.row0 * p.group + o.r.row0, o.r.rows, head);
+            }
+            const int i = handed % kItems;
+            if (!__all_sync(0xffffffffu, mbar_wait(&bar.item_empty[i], (handed / kItems & 1) ^ 1, abort_flag, p.err)))
+                return false;
+            if (lane == 0) {
+                bar.item[i] = o;
+                mbar_arrive(&bar.item_full[i]);
+            }
+            __syncwarp();
+            ++handed;
+            if (o.t0 == o.t1) return false;
+            left -= o.n;
+            t0 = 0;
+            if (left > 0 && ++it >= n_items) {
+                it = 0;
+                int scanned = 0;
+                do {
+                    if (++b >= p.sequences) {
+                        b = 0;
+                        ++head;
                     }
-                }
-                t += o.tiles;
-                if (t == i.t1) {
-                    open = false;
-                    done_item();
-                }
-                return o;
-            };
-            Group now = fetch();
-            while (ok && now.tiles) {
-                const Group then = fetch();
-                if (now.off < 0 || now.page < 0 || now.page >= p.pages) {
-                    // a page coordinate past the end reads zeros
-                    if (now.off >= 0) report_index(p.err);
-                    now.page = p.pages, now.off = 0;
-                }
-                const uint16_t *base = (kv ? c.v_scale : c.k_scale) + now.head * st[1];
-                for (int j = 0; j < now.tiles; ++j) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&bar.empty[slot], phase, abort_flag, p.err));
-                    if (!ok) break;
-                    const bool issue = elect_one();
-                    uint8_t *dst = smem + slot * L::kStageBytes + (kv ? L::kV : 0);
-                    if (issue) mbar_arrive_expect_tx(&bar.full[kv][slot], kTile * L::kRow);
-                    for (int i = 0; i < boxes; ++i, dst += p.box * L::kRow) {
-                        const int page = __shfl_sync(0xffffffffu, now.page, j * boxes + i);
-                        const int off = __shfl_sync(0xffffffffu, now.off, j * boxes + i);
-                        if (issue) tma_load_4d(dst, map, 0, off, now.head, page, &bar.full[kv][slot]);
-                    }
-                    // Scales of the tokens that some row sees.  Others' become
-                    // zeros: their values may be anything (0 * NaN).
-                    const uint32_t to = smem_u32(smem + slot * L::kStageBytes + (kv ? L::kVScale : L::kKScale));
+                    s = sequence(p, b);
+                    n_items = items_of(p, s);
+                } while (n_items == 0 && ++scanned <= p.sequences);
+            }
+            return true;
+        };
+        bool more = warp == 0 && publish();
+        // ----------------------------------------------------- copies
+        const KvQ4View &c = p.cache.c;
+        const uint32_t ring = smem_u32(smem);
+        // The key tile to be copied next, and the lane's token of it (off < 0:
+        // no row sees it): page numbers are loaded a tile ahead.  Warp 0 hands
+        // out an item when it comes to the one before.
+        int t = 0, t1 = 0, page = 0, off = -1, kv_head = 0;
+        bool ended = false;
+        auto look = [&]() {
+            if (++t >= t1) {
+                if (t1) done_item();
+                ended = !item_there() || item().t0 >= item().t1;
+                if (ended) return;
+                t = item().t0, t1 = item().t1;
+                if (more) more = publish();
+            }
+            const Item &i = item();
+            kv_head = i.head;
+            const int token = i.key_tile(t) * kTile + warp * kStep + lane;
+            off = -1;
+            if (token < i.r.sink_end || (token >= i.r.lo && token < i.r.hi)) {
+                const int index = token / p.page_size;
+                page = p.page_table[(int64_t)i.b * p.table_stride + index];
+                off = token - index * p.page_size;
+            }
+        };
+        look();
+        for (uint32_t slot = 0, phase = 1; !ended;) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&bar.empty[warp][slot], phase, abort_flag, p.err))) break;
+            if (off >= 0 && (page < 0 || page >= p.pages)) {
+                report_index(p.err);
+                off = -1;
+            }
+            // a token that no row sees, or without a page, becomes zeros
+            const bool seen = off >= 0;
+            const uint32_t all_seen = __ballot_sync(0xffffffffu, seen);
+            const int64_t at_page = seen ? page : 0, at = seen ? off : 0;
+            const uint64_t k = reinterpret_cast<uint64_t>(c.k) + at_page * c.k_stride[0] + kv_head * c.k_stride[1] +
+                               at * c.k_stride[2];
+            const uint64_t v = reinterpret_cast<uint64_t>(c.v) + at_page * c.v_stride[0] + kv_head * c.v_stride[1] +
+                               at * c.v_stride[2];
+            const uint32_t st = ring + slot * L::kStageBytes;
+            constexpr int kChunks = L::kRow / 16, kAtOnce = 32 / kChunks;
+            const int chunk = lane % kChunks;
 #pragma unroll
-                    for (int i = 0; i < kTile / 32; ++i) {
-                        const int tok = i * 32 + lane, box = tok >> shift, in_box = tok & (p.box - 1);
-                        const int page = __shfl_sync(0xffffffffu, now.page, j * boxes + box);
-                        const int off = __shfl_sync(0xffffffffu, now.off, j * boxes + box) + in_box;
-                        const int clip = __shfl_sync(0xffffffffu, now.clip, j * boxes + box);
-                        const bool seen = page < p.pages && (in_box < (clip & 127) || (in_box >= (clip >> 7 & 127) &&
-                                                                                       in_box < clip >> 14));
-                        copy_small<L::kScales>(to + tok * L::kScales,
-                                               base + (seen ? page * st[0] + off * st[2] : 0), seen ? L::kScales : 0);
-                    }
-                    copy_arrive(&bar.full[kv][slot]);
-                    ++fill;
-                    if (++slot == kStages) slot = 0, phase ^= 1;
-                }
-                now = then;
+            for (int j = 0; j < kStep / kAtOnce; ++j) {
+                const int tok = j * kAtOnce + lane / kChunks, row = warp * kStep + tok;
+                const uint64_t ka = __shfl_sync(0xffffffffu, k, tok), va = __shfl_sync(0xffffffffu, v, tok);
+                const uint32_t to = st + row * L::kRow + L::chunk(row, chunk) * 16;
+                const int bytes = all_seen >> tok & 1 ? 16 : 0;
+                copy16(to, reinterpret_cast<const void *>(ka + chunk * 16), bytes);
+                copy16(to + L::kV, reinterpret_cast<const void *>(va + chunk * 16), bytes);
             }
-            if (lane == 0) bar.fills[kv] = fill;
-        } else if (warp == 3) {
-            // ------------------------------------------------- items
-            int flags = 0;
-            int4 tail = make_int4(0, 0, 0, 0);
-            int64_t left = bar.start.left;
-            int head = bar.start.head, b = bar.start.b, it = bar.start.item, t0 = bar.start.t0;
-            Sequence s = bar.start.s;
-            int n_items = items_of(p, s);
-            for (;; ++items) {
-                Item o{};
-                if (left > 0) {
-                    o.r = item_range(p, s, it);
-                    o.t0 = t0, o.t1 = left >= o.r.n ? o.r.n : (int)left, o.n = o.r.n;
-                    o.head = head, o.b = b, o.q_row = s.row0, o.before = s.kv - s.len;
-                    if (o.t0 > 0) flags |= kHeadPiece | (o.t1 < o.n ? kHeadGoesOn : 0);
-                    if (o.t0 == 0 && o.t1 < o.n)
-                        flags |= kTailPiece, tail = make_int4(0, s.row0 * p.group + o.r.row0, o.r.rows, head);
-                }
-                const int i = items % kItems;
-                if (!__all_sync(0xffffffffu,
-                                mbar_wait(&bar.item_empty[i], (items / kItems & 1) ^ 1, abort_flag, p.err)))
-                    break;
-                if (lane == 0) {
-                    bar.item[i] = o;
-                    mbar_arrive(&bar.item_full[i]);
-                }
-                __syncwarp();
-                if (o.t0 == o.t1) break;
-                left -= o.n;
-                t0 = 0;
-                if (left > 0 && ++it >= n_items) {
-                    it = 0;
-                    int scanned = 0;
-                    do {
-                        if (++b >= p.sequences) {
-                            b = 0;
-                            ++head;
-                        }
-                        s = sequence(p, b);
-                        n_items = items_of(p, s);
-                    } while (n_items == 0 && ++scanned <= p.sequences);
-                }
-            }
+            const int bytes = seen ? L::kScales : 0;
+            const uint32_t to = st + (warp * kStep + lane) * L::kScales;
+            copy_small<L::kScales>(to + L::kKScale,
+                                   c.k_scale + at_page * c.k_scale_stride[0] + kv_head * c.k_scale_stride[1] +
+                                       at * c.k_scale_stride[2], bytes);
+            copy_small<L::kScales>(to + L::kVScale,
+                                   c.v_scale + at_page * c.v_scale_stride[0] + kv_head * c.v_scale_stride[1] +
+                                       at * c.v_scale_stride[2], bytes);
+            copy_arrive(&bar.full[warp][slot]);
+            if (++slot == kStages) slot = 0, phase ^= 1;
+            look();
+        }
+        copy_wait_all();
+        if (warp == 0) {
             tail.x = flags;
             if (lane == 0) p.record[blockIdx.x] = tail;
         }
@@ -468,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
         }
         for (int tile = (fill & 1) == (uint32_t)turn ? 0 : 1; tile < tiles; tile += 2) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&bar.full[0][slot], phase, abort_flag, p.err))) break;
+            if (!__all_sync(0xffffffffu, mbar_wait(&bar.full[part][slot], phase, abort_flag, p.err))) break;
             const uint32_t st = ring + slot * L::kStageBytes;
             const uint32_t k_codes = st + part * kStep * L::kRow, v_codes = k_codes + L::kV;
             const uint32_t k_scales = st + L::kKScale + part * kStep * L::kScales;
@@ -576,7 +555,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // values: a lane's 16 (D = 64: 8) elements of a token are 8 (4)
             // bytes, all of one block
-            if (!__all_sync(0xffffffffu, mbar_wait(&bar.full[1][slot], phase, abort_flag, p.err))) break;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t w[4][D / 64], d[4];
@@ -612,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // (the stage's words have all been used)
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.empty[slot]);
+            if (lane == 0) mbar_arrive(&bar.empty[part][slot]);
             slot += 2;
             if (slot >= kStages) slot -= kStages, phase ^= 1;
         }
@@ -697,14 +675,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 p.lse[place(ctid)] = (mlc.x * mlc.z + __log2f(mlc.y)) * kLn2;
         }
     }
-    }
-    __syncthreads();
-    if (bar.abort && tid == 0) {
-        // a wait was abandoned: copies in flight land before the CTA exits
-        // (otherwise every copy was waited for by its readers)
-        for (int kv = 0; kv < 2; ++kv)
-            for (uint32_t f = max(bar.fills[kv], (uint32_t)kStages) - kStages; f < bar.fills[kv]; ++f)
-                mbar_drain(&bar.full[kv][f % kStages], f / kStages & 1);
     }
 }
 
@@ -802,11 +772,11 @@ struct WorkspaceLayout {
 };
 
 template <int D, int NT>
-cudaError_t launch_narrow(const CUtensorMap &kmap, const CUtensorMap &vmap, const Params &p, int ctas, cudaStream_t s) {
+cudaError_t launch_narrow(const Params &p, int ctas, cudaStream_t s) {
     constexpr int kSmem = Layout<D, NT>::kSmem;
     const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(attention_q4_kernel<D, NT>), kSmem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attention_q4_kernel<D, NT>, dim3(ctas), dim3(kThreads), kSmem, s, kmap, vmap, p);
+    return launch_pdl(attention_q4_kernel<D, NT>, dim3(ctas), dim3(kThreads), kSmem, s, p);
 }
 
 template <int D>
@@ -829,14 +799,7 @@ cudaError_t launch_d(const AttentionArgs &a, const KvQ4View &c, void *workspace,
     p.part_mlc = reinterpret_cast<float4 *>(ws + w.mlc_off);
     p.record = reinterpret_cast<int4 *>(ws + w.rec_off);
     p.err = err;
-    p.box = gcd(c.page_size, 64);
-    EncodeTiledFn enc = encode_fn();
-    if (!enc) return cudaErrorNotSupported;
-    CUtensorMap kmap, vmap;
-    if (!make_codes_map(enc, &kmap, c.k, c.k_stride, c, p.box) || !make_codes_map(enc, &vmap, c.v, c.v_stride, c, p.box))
-        return cudaErrorInvalidValue;
-    const cudaError_t e = p.item_rows == 8 ? launch_narrow<D, 1>(kmap, vmap, p, ctas, s)
-                                           : launch_narrow<D, 2>(kmap, vmap, p, ctas, s);
+    const cudaError_t e = p.item_rows == 8 ? launch_narrow<D, 1>(p, ctas, s) : launch_narrow<D, 2>(p, ctas, s);
     if (e != cudaSuccess) return e;
     return launch_pdl(attention_q4_join_kernel<D>, dim3(ctas, p.item_rows), dim3(256), 0, s, p, ctas);
 }

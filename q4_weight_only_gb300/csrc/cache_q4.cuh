@@ -34,8 +34,11 @@ bool make_codes_map(EncodeTiledFn enc, CUtensorMap *map, const uint8_t *base, co
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// An asynchronous copy of 8 or 4 bytes; nothing is read and zeros are written
-// where `bytes` is 0.
+// Asynchronous copies of 16, 8 or 4 bytes; nothing is read and zeros are
+// written where `bytes` is 0.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 template <int kBytes>
 __device__ __forceinline__ void copy_small(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(bytes) : "memory");
@@ -45,6 +48,8 @@ __device__ __forceinline__ void copy_small(uint32_t dst, const void *src, int by
 __device__ __forceinline__ void copy_arrive(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// The thread's copies have landed.
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
