@@ -53,6 +53,7 @@ struct Params {
     int sequences, table_width, pages, page_size, rows, max_q_len;
     int q_heads, kv_heads, group, window, sinks;
     int most_rows;  // of a sequence; longer ones are another kernel's
+    int tile_pages, tile_rest;  // kTile by page_size
     int item_rows;  // rows of an item: (token, head of the group) pairs of a sequence, in order
     const __nv_bfloat16 *q;
     int64_t q_row_stride, q_head_stride;
@@ -277,43 +278,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ----------------------------------------------------- copies
         const KvQ4View &c = p.cache.c;
         const uint32_t ring = smem_u32(smem);
-        // The key tile to be copied next, and the lane's token of it (off < 0:
-        // no row sees it): page numbers are loaded a tile ahead.  Warp 0 hands
-        // out an item when it comes to the one before.
-        int t = 0, t1 = 0, page = 0, off = -1, kv_head = 0;
-        bool ended = false;
+        // The lane's token of a key tile.  Page numbers are loaded a tile
+        // ahead of the copies, across items; within a run of tiles the page
+        // table's index moves by the same step, without a division.
+        struct Token {
+            int page, off;  // off < 0: no row sees it
+            int head;       // < 0: the share has ended
+        };
+        int t = 0, t1 = 0, index = 0, off = 0;
         auto look = [&]() {
+            Token k{0, -1, -1};
+            const int last = t;
             if (++t >= t1) {
                 if (t1) done_item();
-                ended = !item_there() || item().t0 >= item().t1;
-                if (ended) return;
+                if (!item_there() || item().t0 >= item().t1) return k;
                 t = item().t0, t1 = item().t1;
+                // warp 0 hands out an item when it comes to the one before
                 if (more) more = publish();
             }
             const Item &i = item();
-            kv_head = i.head;
             const int token = i.key_tile(t) * kTile + warp * kStep + lane;
-            off = -1;
-            if (token < i.r.sink_end || (token >= i.r.lo && token < i.r.hi)) {
-                const int index = token / p.page_size;
-                page = p.page_table[(int64_t)i.b * p.table_stride + index];
-                off = token - index * p.page_size;
+            if (t == i.t0 || i.key_tile(t) != i.key_tile(last) + 1) {
+                index = token / p.page_size, off = token - index * p.page_size;
+            } else {
+                index += p.tile_pages, off += p.tile_rest;
+                if (off >= p.page_size) off -= p.page_size, ++index;
             }
+            k.head = i.head;
+            if (token < i.r.sink_end || (token >= i.r.lo && token < i.r.hi)) {
+                k.page = p.page_table[(int64_t)i.b * p.table_stride + index];
+                k.off = off;
+            }
+            return k;
         };
-        look();
-        for (uint32_t slot = 0, phase = 1; !ended;) {
+        Token now = look();
+        for (uint32_t slot = 0, phase = 1; now.head >= 0;) {
+            const Token then = look();
             if (!__all_sync(0xffffffffu, mbar_wait(&bar.empty[warp][slot], phase, abort_flag, p.err))) break;
-            if (off >= 0 && (page < 0 || page >= p.pages)) {
+            bool seen = now.off >= 0;
+            if (seen && (now.page < 0 || now.page >= p.pages)) {
                 report_index(p.err);
-                off = -1;
+                seen = false;
             }
             // a token that no row sees, or without a page, becomes zeros
-            const bool seen = off >= 0;
             const uint32_t all_seen = __ballot_sync(0xffffffffu, seen);
-            const int64_t at_page = seen ? page : 0, at = seen ? off : 0;
-            const uint64_t k = reinterpret_cast<uint64_t>(c.k) + at_page * c.k_stride[0] + kv_head * c.k_stride[1] +
+            const int64_t at_page = seen ? now.page : 0, at = seen ? now.off : 0;
+            const uint64_t k = reinterpret_cast<uint64_t>(c.k) + at_page * c.k_stride[0] + now.head * c.k_stride[1] +
                                at * c.k_stride[2];
-            const uint64_t v = reinterpret_cast<uint64_t>(c.v) + at_page * c.v_stride[0] + kv_head * c.v_stride[1] +
+            const uint64_t v = reinterpret_cast<uint64_t>(c.v) + at_page * c.v_stride[0] + now.head * c.v_stride[1] +
                                at * c.v_stride[2];
             const uint32_t st = ring + slot * L::kStageBytes;
             constexpr int kChunks = L::kRow / 16, kAtOnce = 32 / kChunks;
@@ -330,14 +342,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int bytes = seen ? L::kScales : 0;
             const uint32_t to = st + (warp * kStep + lane) * L::kScales;
             copy_small<L::kScales>(to + L::kKScale,
-                                   c.k_scale + at_page * c.k_scale_stride[0] + kv_head * c.k_scale_stride[1] +
+                                   c.k_scale + at_page * c.k_scale_stride[0] + now.head * c.k_scale_stride[1] +
                                        at * c.k_scale_stride[2], bytes);
             copy_small<L::kScales>(to + L::kVScale,
-                                   c.v_scale + at_page * c.v_scale_stride[0] + kv_head * c.v_scale_stride[1] +
+                                   c.v_scale + at_page * c.v_scale_stride[0] + now.head * c.v_scale_stride[1] +
                                        at * c.v_scale_stride[2], bytes);
             copy_arrive(&bar.full[warp][slot]);
             if (++slot == kStages) slot = 0, phase ^= 1;
-            look();
+            now = then;
         }
         copy_wait_all();
         if (warp == 0) {
@@ -787,6 +799,7 @@ cudaError_t launch_d(const AttentionArgs &a, const KvQ4View &c, void *workspace,
     p.page_table = c.page_table, p.q_start = c.q_start, p.kv_len = c.kv_len, p.table_stride = c.table_stride;
     p.sequences = c.sequences, p.table_width = c.table_width, p.pages = c.pages, p.page_size = c.page_size;
     p.rows = a.rows, p.max_q_len = a.max_q_len;
+    p.tile_pages = kTile / c.page_size, p.tile_rest = kTile % c.page_size;
     p.q_heads = a.q_heads, p.kv_heads = c.kv_heads, p.group = a.q_heads / c.kv_heads;
     p.window = a.window, p.sinks = a.sinks;
     p.item_rows = item_rows(p.group, a.max_q_len), p.most_rows = kMostRows;
