@@ -53,7 +53,7 @@ struct Params {
     int sequences, table_width, pages, page_size, rows, max_q_len;
     int q_heads, kv_heads, group, window, sinks;
     int most_rows;  // of a sequence; longer ones are another kernel's
-    int tile_pages, tile_rest;  // kTile by page_size
+    int step_pages, step_rest;  // two tiles by page_size
     int item_rows;  // rows of an item: (token, head of the group) pairs of a sequence, in order
     const __nv_bfloat16 *q;
     int64_t q_row_stride, q_head_stride;
@@ -131,12 +131,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 
 // --------------------------------------------------------------- the kernel
 
-// Threads and their registers: the launch gives 168 each, the four warps that
-// copy give theirs up to the eight that compute (128 * 72 + 256 * 216 = 384 *
-// 168).
-constexpr int kThreads = 384, kComputeWarps = 8;
-constexpr int kCopyRegs = 72, kComputeRegs = 216;
+// Threads and their registers: the launch gives 128 each, the eight warps that
+// copy give theirs up to the eight that compute (256 * 64 + 256 * 192 = 512 *
+// 128).
+constexpr int kThreads = 512, kCopyWarps = 8, kComputeWarps = 8;
+constexpr int kCopyRegs = 64, kComputeRegs = 192;
 constexpr int kParts = kTile / kStep;  // of a tile: one copying warp's and one computing warp's
+constexpr int kTurns = kCopyWarps / kParts;  // tiles that are under way at once
+static_assert(kCopyWarps == kComputeWarps, "both take every second tile");
 constexpr int kItems = 4;  // items handed out ahead
 
 template <int D, int NT>
@@ -177,10 +179,10 @@ struct Bars {
     Start<kThreads> start;
 };
 
-// Warps: 0 to 3 copy, each 32 tokens of every key tile, into one ring; 0 hands
-// out the items too.  4 to 11 compute: four share a tile, 32 keys each, and the
-// two fours take the tiles in turn.  Each has a reference, a sum and an O of
-// its own, which are merged at the end of an item's piece.
+// Warps: 0 to 7 copy key tiles into one ring, 8 to 15 compute.  Four of a kind
+// share a tile, 32 tokens each, and the two fours take the tiles in turn.  Each
+// computing warp has a reference, a sum and an O of its own, which are merged
+// at the end of an item's piece.  Warp 0 hands out the items too.
 //
 // The copies are asynchronous ones of 16 bytes a lane: a row of codes is 64
 // (32) bytes, and tensor copies took 4.6 cycles a row whatever its length (64
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&bar.item_full[i], 1);
-            mbar_init(&bar.item_empty[i], kParts + kComputeWarps);
+            mbar_init(&bar.item_empty[i], kCopyWarps + kComputeWarps);
         }
         bar.abort = 0;
         mbar_fence_init();
@@ -226,7 +228,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++items;
     };
 
-    if (warp < kParts) {
+    // the warp's part of a tile, and which of two tiles are its
+    const int part = warp & (kParts - 1), turn = warp / kParts & 1;
+    if (warp < kCopyWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
         // ------------------------------------------------------ items
         int flags = 0;
@@ -286,22 +290,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             int head;       // < 0: the share has ended
         };
         int t = 0, t1 = 0, index = 0, off = 0;
+        uint32_t fill = turn;  // of the ring: tile t is fill number `fill`, tile t1 of the item `end`
+        uint32_t end = 0;
         auto look = [&]() {
             Token k{0, -1, -1};
-            const int last = t;
-            if (++t >= t1) {
+            int last = t;
+            t += kTurns;
+            while (t >= t1) {
                 if (t1) done_item();
                 if (!item_there() || item().t0 >= item().t1) return k;
-                t = item().t0, t1 = item().t1;
+                // the item's first tile is fill number `end`
+                t = item().t0 + (int)(fill - end), t1 = item().t1, last = -1;
+                end += t1 - item().t0;
                 // warp 0 hands out an item when it comes to the one before
                 if (more) more = publish();
             }
+            fill += kTurns;
             const Item &i = item();
-            const int token = i.key_tile(t) * kTile + warp * kStep + lane;
-            if (t == i.t0 || i.key_tile(t) != i.key_tile(last) + 1) {
+            const int token = i.key_tile(t) * kTile + part * kStep + lane;
+            if (last < 0 || i.key_tile(t) != i.key_tile(last) + kTurns) {
                 index = token / p.page_size, off = token - index * p.page_size;
             } else {
-                index += p.tile_pages, off += p.tile_rest;
+                index += p.step_pages, off += p.step_rest;
                 if (off >= p.page_size) off -= p.page_size, ++index;
             }
             k.head = i.head;
@@ -312,9 +322,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             return k;
         };
         Token now = look();
-        for (uint32_t slot = 0, phase = 1; now.head >= 0;) {
+        for (uint32_t slot = turn, phase = 1; now.head >= 0;) {
             const Token then = look();
-            if (!__all_sync(0xffffffffu, mbar_wait(&bar.empty[warp][slot], phase, abort_flag, p.err))) break;
+            if (!__all_sync(0xffffffffu, mbar_wait(&bar.empty[part][slot], phase, abort_flag, p.err))) break;
             bool seen = now.off >= 0;
             if (seen && (now.page < 0 || now.page >= p.pages)) {
                 report_index(p.err);
@@ -332,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int chunk = lane % kChunks;
 #pragma unroll
             for (int j = 0; j < kStep / kAtOnce; ++j) {
-                const int tok = j * kAtOnce + lane / kChunks, row = warp * kStep + tok;
+                const int tok = j * kAtOnce + lane / kChunks, row = part * kStep + tok;
                 const uint64_t ka = __shfl_sync(0xffffffffu, k, tok), va = __shfl_sync(0xffffffffu, v, tok);
                 const uint32_t to = st + row * L::kRow + L::chunk(row, chunk) * 16;
                 const int bytes = all_seen >> tok & 1 ? 16 : 0;
@@ -340,15 +350,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 copy16(to + L::kV, reinterpret_cast<const void *>(va + chunk * 16), bytes);
             }
             const int bytes = seen ? L::kScales : 0;
-            const uint32_t to = st + (warp * kStep + lane) * L::kScales;
+            const uint32_t to = st + (part * kStep + lane) * L::kScales;
             copy_small<L::kScales>(to + L::kKScale,
                                    c.k_scale + at_page * c.k_scale_stride[0] + now.head * c.k_scale_stride[1] +
                                        at * c.k_scale_stride[2], bytes);
             copy_small<L::kScales>(to + L::kVScale,
                                    c.v_scale + at_page * c.v_scale_stride[0] + now.head * c.v_scale_stride[1] +
                                        at * c.v_scale_stride[2], bytes);
-            copy_arrive(&bar.full[warp][slot]);
-            if (++slot == kStages) slot = 0, phase ^= 1;
+            copy_arrive(&bar.full[part][slot]);
+            slot += kTurns;
+            if (slot >= kStages) slot -= kStages, phase ^= 1;
             now = then;
         }
         copy_wait_all();
@@ -358,8 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
-    const int g = lane >> 2, t = lane & 3, ctid = tid - 128, cwarp = warp - 4;
-    const int part = cwarp & 3, turn = cwarp >> 2;  // keys of a tile, and which of two tiles
+    const int g = lane >> 2, t = lane & 3, ctid = tid - kCopyWarps * 32, cwarp = warp - kCopyWarps;
     const uint32_t bias = p.cache.bias, ring = smem_u32(smem);
     float *merged = reinterpret_cast<float *>(smem + L::kOut);
     uint32_t fill = 0;       // tiles of earlier items
@@ -458,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
         }
-        for (int tile = (fill & 1) == (uint32_t)turn ? 0 : 1; tile < tiles; tile += 2) {
+        for (int tile = (fill & 1) == (uint32_t)turn ? 0 : 1; tile < tiles; tile += kTurns) {
             if (!__all_sync(0xffffffffu, mbar_wait(&bar.full[part][slot], phase, abort_flag, p.err))) break;
             const uint32_t st = ring + slot * L::kStageBytes;
             const uint32_t k_codes = st + part * kStep * L::kRow, v_codes = k_codes + L::kV;
@@ -603,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (the stage's words have all been used)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.empty[part][slot]);
-            slot += 2;
+            slot += kTurns;
             if (slot >= kStages) slot -= kStages, phase ^= 1;
         }
         fill += tiles;
@@ -799,7 +809,7 @@ cudaError_t launch_d(const AttentionArgs &a, const KvQ4View &c, void *workspace,
     p.page_table = c.page_table, p.q_start = c.q_start, p.kv_len = c.kv_len, p.table_stride = c.table_stride;
     p.sequences = c.sequences, p.table_width = c.table_width, p.pages = c.pages, p.page_size = c.page_size;
     p.rows = a.rows, p.max_q_len = a.max_q_len;
-    p.tile_pages = kTile / c.page_size, p.tile_rest = kTile % c.page_size;
+    p.step_pages = kTurns * kTile / c.page_size, p.step_rest = kTurns * kTile % c.page_size;
     p.q_heads = a.q_heads, p.kv_heads = c.kv_heads, p.group = a.q_heads / c.kv_heads;
     p.window = a.window, p.sinks = a.sinks;
     p.item_rows = item_rows(p.group, a.max_q_len), p.most_rows = kMostRows;
