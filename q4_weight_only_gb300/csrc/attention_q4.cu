@@ -53,7 +53,7 @@ struct Params {
     int sequences, table_width, pages, page_size, rows, max_q_len;
     int q_heads, kv_heads, group, window, sinks;
     int most_rows;  // of a sequence; longer ones are another kernel's
-    int step_pages, step_rest;  // two tiles by page_size
+    int step_pages, step_rest;  // kCopyTurns tiles by page_size
     int item_rows;  // rows of an item: (token, head of the group) pairs of a sequence, in order
     const __nv_bfloat16 *q;
     int64_t q_row_stride, q_head_stride;
@@ -132,13 +132,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 // --------------------------------------------------------------- the kernel
 
 // Threads and their registers: the launch gives 128 each, the eight warps that
-// copy give theirs up to the eight that compute (256 * 64 + 256 * 192 = 512 *
+// copy give theirs up to the eight that compute (256 * 88 + 256 * 168 = 512 *
 // 128).
 constexpr int kThreads = 512, kCopyWarps = 8, kComputeWarps = 8;
-constexpr int kCopyRegs = 64, kComputeRegs = 192;
-constexpr int kParts = kTile / kStep;  // of a tile: one copying warp's and one computing warp's
-constexpr int kTurns = kCopyWarps / kParts;  // tiles that are under way at once
-static_assert(kCopyWarps == kComputeWarps, "both take every second tile");
+constexpr int kCopyRegs = 88, kComputeRegs = 168;
+constexpr int kTurns = kComputeWarps / (kTile / kStep);  // tiles computed at once
+constexpr int kCopyTurns = kCopyWarps / 2;               // and copied at once
 constexpr int kItems = 4;  // items handed out ahead
 
 template <int D, int NT>
@@ -170,7 +169,7 @@ struct Layout {
 template <int D, int NT>
 struct Bars {
     using L = Layout<D, NT>;
-    uint64_t full[kParts][L::kStages], empty[kParts][L::kStages];
+    uint64_t full[2][L::kStages], empty[L::kStages];  // keys and values; both have been used
     uint64_t item_full[kItems], item_empty[kItems];
     Item item[kItems];
     float2 warp_ml[kComputeWarps][L::kRows];  // a warp's m and l, then its factor in the merge
@@ -179,10 +178,11 @@ struct Bars {
     Start<kThreads> start;
 };
 
-// Warps: 0 to 7 copy key tiles into one ring, 8 to 15 compute.  Four of a kind
-// share a tile, 32 tokens each, and the two fours take the tiles in turn.  Each
-// computing warp has a reference, a sum and an O of its own, which are merged
-// at the end of an item's piece.  Warp 0 hands out the items too.
+// Warps: 0 to 7 copy key tiles into one ring, even ones keys and odd ones
+// values, each pair every fourth tile; warp 0 hands out the items too.  8 to 15
+// compute: four share a tile, 32 tokens each, and the two fours take the tiles
+// in turn.  Each has a reference, a sum and an O of its own, which are merged
+// at the end of an item's piece.
 //
 // The copies are asynchronous ones of 16 bytes a lane: a row of codes is 64
 // (32) bytes, and tensor copies took 4.6 cycles a row whatever its length (64
@@ -200,9 +200,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int *abort_flag = &bar.abort;
     if (tid == 0) {
-        for (int i = 0; i < kParts * kStages; ++i) {
+        for (int i = 0; i < kStages; ++i) {
             mbar_init(&bar.full[0][i], 32);  // each lane's copies
-            mbar_init(&bar.empty[0][i], 1);
+            mbar_init(&bar.full[1][i], 32);
+            mbar_init(&bar.empty[i], kTile / kStep);
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&bar.item_full[i], 1);
@@ -228,8 +229,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++items;
     };
 
-    // the warp's part of a tile, and which of two tiles are its
-    const int part = warp & (kParts - 1), turn = warp / kParts & 1;
     if (warp < kCopyWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
         // ------------------------------------------------------ items
@@ -280,22 +279,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         bool more = warp == 0 && publish();
         // ----------------------------------------------------- copies
+        const int kv = warp & 1, turn = warp >> 1;  // keys or values, and which of four tiles
         const KvQ4View &c = p.cache.c;
-        const uint32_t ring = smem_u32(smem);
-        // The lane's token of a key tile.  Page numbers are loaded a tile
-        // ahead of the copies, across items; within a run of tiles the page
-        // table's index moves by the same step, without a division.
-        struct Token {
-            int page, off;  // off < 0: no row sees it
+        // Lane i < 16 has group i of a tile, 8 tokens, which are in one page.
+        // Page numbers are loaded a tile ahead of the copies, across items;
+        // within a run of tiles the page table's index moves by the same
+        // step, without a division.
+        struct Tile {
+            int page, off;  // of the lane's group; off < 0: no row sees any of it
             int head;       // < 0: the share has ended
+            uint32_t seen;  // whether some row sees the lane's tokens 32 i + lane, bit i
         };
         int t = 0, t1 = 0, index = 0, off = 0;
         uint32_t fill = turn;  // of the ring: tile t is fill number `fill`, tile t1 of the item `end`
         uint32_t end = 0;
         auto look = [&]() {
-            Token k{0, -1, -1};
+            Tile k{0, -1, -1, 0};
             int last = t;
-            t += kTurns;
+            t += kCopyTurns;
             while (t >= t1) {
                 if (t1) done_item();
                 if (!item_there() || item().t0 >= item().t1) return k;
@@ -305,60 +306,76 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // warp 0 hands out an item when it comes to the one before
                 if (more) more = publish();
             }
-            fill += kTurns;
+            fill += kCopyTurns;
             const Item &i = item();
-            const int token = i.key_tile(t) * kTile + part * kStep + lane;
-            if (last < 0 || i.key_tile(t) != i.key_tile(last) + kTurns) {
+            const int tile = i.key_tile(t), first = tile * kTile, token = first + (lane & 15) * 8;
+            if (last < 0 || tile != i.key_tile(last) + kCopyTurns) {
                 index = token / p.page_size, off = token - index * p.page_size;
             } else {
                 index += p.step_pages, off += p.step_rest;
                 if (off >= p.page_size) off -= p.page_size, ++index;
             }
             k.head = i.head;
-            if (token < i.r.sink_end || (token >= i.r.lo && token < i.r.hi)) {
+            const int sink_end = i.r.sink_end, lo = i.r.lo, hi = i.r.hi;
+            k.seen = 15;
+            if (first < lo || first + kTile > hi) {
+                k.seen = 0;
+#pragma unroll
+                for (int x = 0; x < kTile / 32; ++x) {
+                    const int tok = first + x * 32 + lane;
+                    if (tok < sink_end || (tok >= lo && tok < hi)) k.seen |= 1u << x;
+                }
+            }
+            if (lane < 16 && (token < sink_end || (token + 8 > lo && token < hi))) {
                 k.page = p.page_table[(int64_t)i.b * p.table_stride + index];
                 k.off = off;
             }
             return k;
         };
-        Token now = look();
+        const uint8_t *base = kv ? c.v : c.k;
+        const uint16_t *scale_base = kv ? c.v_scale : c.k_scale;
+        const int64_t *cs = kv ? c.v_stride : c.k_stride, *ss = kv ? c.v_scale_stride : c.k_scale_stride;
+        // the lane's place within the tokens of one copy: a row's chunk, and a
+        // scale's token of eight
+        constexpr int kChunks = L::kRow / 16, kAtOnce = 32 / kChunks;
+        const int row = lane / kChunks, chunk = lane % kChunks;
+        const int64_t lane_bytes = (row & 7) * cs[2] + chunk * 16, lane_scale = (lane & 7) * ss[2];
+        const uint32_t lane_to = smem_u32(smem) + (kv ? L::kV : 0) + row * L::kRow + L::chunk(row, chunk) * 16;
+        const uint32_t lane_scale_to = smem_u32(smem) + (kv ? L::kVScale : L::kKScale) + lane * L::kScales;
+        Tile now = look();
         for (uint32_t slot = turn, phase = 1; now.head >= 0;) {
-            const Token then = look();
-            if (!__all_sync(0xffffffffu, mbar_wait(&bar.empty[part][slot], phase, abort_flag, p.err))) break;
-            bool seen = now.off >= 0;
-            if (seen && (now.page < 0 || now.page >= p.pages)) {
-                report_index(p.err);
-                seen = false;
+            const Tile then = look();
+            bool some = now.off >= 0;
+            if (some && (now.page < 0 || now.page >= p.pages)) {
+                if (kv == 0) report_index(p.err);
+                some = false;
             }
-            // a token that no row sees, or without a page, becomes zeros
-            const uint32_t all_seen = __ballot_sync(0xffffffffu, seen);
-            const int64_t at_page = seen ? now.page : 0, at = seen ? now.off : 0;
-            const uint64_t k = reinterpret_cast<uint64_t>(c.k) + at_page * c.k_stride[0] + now.head * c.k_stride[1] +
-                               at * c.k_stride[2];
-            const uint64_t v = reinterpret_cast<uint64_t>(c.v) + at_page * c.v_stride[0] + now.head * c.v_stride[1] +
-                               at * c.v_stride[2];
-            const uint32_t st = ring + slot * L::kStageBytes;
-            constexpr int kChunks = L::kRow / 16, kAtOnce = 32 / kChunks;
-            const int chunk = lane % kChunks;
+            // tokens that no row sees, or without a page, become zeros
+            const uint32_t groups = __ballot_sync(0xffffffffu, some);
+            const int64_t page = some ? now.page : 0, at = some ? now.off : 0;
+            const uint64_t codes =
+                reinterpret_cast<uint64_t>(base + page * cs[0] + now.head * cs[1] + at * cs[2]);
+            const uint64_t scales =
+                reinterpret_cast<uint64_t>(scale_base + page * ss[0] + now.head * ss[1] + at * ss[2]);
+            if (!__all_sync(0xffffffffu, mbar_wait(&bar.empty[slot], phase, abort_flag, p.err))) break;
+            const uint32_t to = lane_to + slot * L::kStageBytes;
 #pragma unroll
-            for (int j = 0; j < kStep / kAtOnce; ++j) {
-                const int tok = j * kAtOnce + lane / kChunks, row = part * kStep + tok;
-                const uint64_t ka = __shfl_sync(0xffffffffu, k, tok), va = __shfl_sync(0xffffffffu, v, tok);
-                const uint32_t to = st + row * L::kRow + L::chunk(row, chunk) * 16;
-                const int bytes = all_seen >> tok & 1 ? 16 : 0;
-                copy16(to, reinterpret_cast<const void *>(ka + chunk * 16), bytes);
-                copy16(to + L::kV, reinterpret_cast<const void *>(va + chunk * 16), bytes);
+            for (int j = 0; j < kTile / kAtOnce; ++j) {
+                const int group = D == 128 ? j : 2 * j + (lane >> 4);
+                const uint64_t from = __shfl_sync(0xffffffffu, codes, group) + lane_bytes;
+                copy16(to + j * kAtOnce * L::kRow, reinterpret_cast<const void *>(from), groups >> group & 1 ? 16 : 0);
             }
-            const int bytes = seen ? L::kScales : 0;
-            const uint32_t to = st + (part * kStep + lane) * L::kScales;
-            copy_small<L::kScales>(to + L::kKScale,
-                                   c.k_scale + at_page * c.k_scale_stride[0] + now.head * c.k_scale_stride[1] +
-                                       at * c.k_scale_stride[2], bytes);
-            copy_small<L::kScales>(to + L::kVScale,
-                                   c.v_scale + at_page * c.v_scale_stride[0] + now.head * c.v_scale_stride[1] +
-                                       at * c.v_scale_stride[2], bytes);
-            copy_arrive(&bar.full[part][slot]);
-            slot += kTurns;
+            const uint32_t scale_to = lane_scale_to + slot * L::kStageBytes;
+#pragma unroll
+            for (int x = 0; x < kTile / 32; ++x) {
+                const int group = 4 * x + (lane >> 3);
+                const uint64_t from = __shfl_sync(0xffffffffu, scales, group) + 2 * lane_scale;
+                const bool seen = (groups >> group & 1) && (now.seen >> x & 1);
+                copy_small<L::kScales>(scale_to + x * 32 * L::kScales, reinterpret_cast<const void *>(from),
+                                       seen ? L::kScales : 0);
+            }
+            copy_arrive(&bar.full[kv][slot]);
+            slot += kCopyTurns;
             if (slot >= kStages) slot -= kStages, phase ^= 1;
             now = then;
         }
@@ -370,6 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
     const int g = lane >> 2, t = lane & 3, ctid = tid - kCopyWarps * 32, cwarp = warp - kCopyWarps;
+    const int part = cwarp & 3, turn = cwarp >> 2;  // of a tile, and which of two tiles
     const uint32_t bias = p.cache.bias, ring = smem_u32(smem);
     float *merged = reinterpret_cast<float *>(smem + L::kOut);
     uint32_t fill = 0;       // tiles of earlier items
@@ -469,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
         }
         for (int tile = (fill & 1) == (uint32_t)turn ? 0 : 1; tile < tiles; tile += kTurns) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&bar.full[part][slot], phase, abort_flag, p.err))) break;
+            if (!__all_sync(0xffffffffu, mbar_wait(&bar.full[0][slot], phase, abort_flag, p.err))) break;
             const uint32_t st = ring + slot * L::kStageBytes;
             const uint32_t k_codes = st + part * kStep * L::kRow, v_codes = k_codes + L::kV;
             const uint32_t k_scales = st + L::kKScale + part * kStep * L::kScales;
@@ -577,6 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // values: a lane's 16 (D = 64: 8) elements of a token are 8 (4)
             // bytes, all of one block
+            if (!__all_sync(0xffffffffu, mbar_wait(&bar.full[1][slot], phase, abort_flag, p.err))) break;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t w[4][D / 64], d[4];
@@ -612,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // (the stage's words have all been used)
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.empty[part][slot]);
+            if (lane == 0) mbar_arrive(&bar.empty[slot]);
             slot += kTurns;
             if (slot >= kStages) slot -= kStages, phase ^= 1;
         }
@@ -780,8 +799,13 @@ __global__ void __launch_bounds__(256) attention_q4_join_kernel(const __grid_con
 // takes; those of longer ones fill tcgen05's tiles (attention.cu).
 constexpr int kMostRows = 16;
 
-// Rows of an item: tiles of 8, as few as hold the rows of a sequence.
-int item_rows(int group, int max_q_len) { return (int64_t)group * max_q_len <= 8 ? 8 : kMostRows; }
+// Rows of an item, and the most of a sequence that this kernel takes: one tile
+// of 8 where single tokens need no more and no sequence brings 9 to 16, which
+// two tiles serve best.
+int item_rows(int group, int max_q_len) {
+    const int64_t most = (int64_t)group * max_q_len;
+    return most <= 8 || (most > kMostRows && group <= 8) ? 8 : kMostRows;
+}
 
 struct WorkspaceLayout {
     size_t mlc_off, rec_off, bytes;
@@ -809,10 +833,10 @@ cudaError_t launch_d(const AttentionArgs &a, const KvQ4View &c, void *workspace,
     p.page_table = c.page_table, p.q_start = c.q_start, p.kv_len = c.kv_len, p.table_stride = c.table_stride;
     p.sequences = c.sequences, p.table_width = c.table_width, p.pages = c.pages, p.page_size = c.page_size;
     p.rows = a.rows, p.max_q_len = a.max_q_len;
-    p.step_pages = kTurns * kTile / c.page_size, p.step_rest = kTurns * kTile % c.page_size;
+    p.step_pages = kCopyTurns * kTile / c.page_size, p.step_rest = kCopyTurns * kTile % c.page_size;
     p.q_heads = a.q_heads, p.kv_heads = c.kv_heads, p.group = a.q_heads / c.kv_heads;
     p.window = a.window, p.sinks = a.sinks;
-    p.item_rows = item_rows(p.group, a.max_q_len), p.most_rows = kMostRows;
+    p.item_rows = p.most_rows = item_rows(p.group, a.max_q_len);
     p.q = a.q, p.q_row_stride = a.q_row_stride, p.q_head_stride = a.q_head_stride;
     p.scale_log2 = a.scale * kLog2e;
     p.out = a.out, p.lse = a.lse, p.out_bf16 = a.out_bf16;
@@ -846,7 +870,7 @@ cudaError_t launch_attention_q4(const AttentionArgs &a, const KvQ4View &c, void 
         e = c.head_dim == 128 ? launch_d<128>(a, c, workspace, sms, s, err) : launch_d<64>(a, c, workspace, sms, s, err);
     if (e != cudaSuccess || (int64_t)group * a.max_q_len <= kMostRows) return e;
     const size_t narrow = WorkspaceLayout(sms, c.head_dim, item_rows(group, a.max_q_len)).bytes;
-    return launch_attention_q4_wide(a, c, kMostRows + 1, static_cast<uint8_t *>(workspace) + narrow, s, err);
+    return launch_attention_q4_wide(a, c, item_rows(group, a.max_q_len) + 1, static_cast<uint8_t *>(workspace) + narrow, s, err);
 }
 
 }  // namespace q4_0
