@@ -32,6 +32,14 @@ constexpr int kThreads = 256;
 constexpr int kPieceBytes = 32 * 1024;  // most of a row that one CTA holds
 constexpr float kLargest = 65504.f;     // of an element: what binary16 holds, and what attention reads
 
+// Division of whole numbers below 2^24 by one below 2^8: floor(a / b) =
+// umulhi(a, ceil(2^32 / b)), since a b < 2^32; b = 1 has no such factor.
+struct Divisor {
+    uint32_t by, magic;
+    explicit Divisor(int b) : by(b), magic(b == 1 ? 0 : (uint32_t)(((1ull << 32) + b - 1) / b)) {}
+    __device__ __forceinline__ int operator()(int a) const { return by == 1 ? a : (int)__umulhi((uint32_t)a, magic); }
+};
+
 // Four consecutive elements as fp32.
 __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
@@ -47,10 +55,15 @@ __device__ __forceinline__ void turn(float &a, float &b, float cosv, float sinv)
     b = __fadd_rn(__fmul_rn(b, cosv), __fmul_rn(a0, sinv));
 }
 
-__device__ __forceinline__ uint32_t code_of(float w, float d) {
-    // w / d is within half a step of [-8, 8]; 0 / 0 and a d that became 0
-    // give codes that its scale of 0 makes no difference of
-    return (uint32_t)(int)(fminf(fmaxf(roundf(__fdiv_rn(w, d)), -8.f), 7.f) + 8.f);
+// clamp(round(w / d), -8, 7) + 8, halves away from zero, with `inv` the
+// reciprocal of d.  w inv is within 3 2^-24 |w / d| <= 2^-19 of the quotient:
+// only where it is that near to a half does the quotient itself decide (0 / 0
+// and a d that became 0 give codes that its scale of 0 makes no difference of).
+__device__ __forceinline__ uint32_t code_of(float w, float d, float inv) {
+    float q = w * inv;
+    const float half = fabsf(fabsf(q) - floorf(fabsf(q)) - 0.5f);
+    if (!(half > 0x1p-19f)) q = __fdiv_rn(w, d);
+    return (uint32_t)(int)(fminf(fmaxf(roundf(q), -8.f), 7.f) + 8.f);
 }
 
 // The largest element of a block so far.
@@ -84,8 +97,10 @@ __device__ __forceinline__ void quantise_quad(float4 u, float4 v, int j, uint32_
     } else if (m.size > 0.f) {
         const float d = __fmul_rn(m.value, -0.125f);
         s = __half_as_ushort(__float2half_rn(d));
-        w = code_of(u.x, d) | code_of(v.x, d) << 4 | code_of(u.y, d) << 8 | code_of(v.y, d) << 12 |
-            code_of(u.z, d) << 16 | code_of(v.z, d) << 20 | code_of(u.w, d) << 24 | code_of(v.w, d) << 28;
+        const float inv = __frcp_rn(d);
+        w = code_of(u.x, d, inv) | code_of(v.x, d, inv) << 4 | code_of(u.y, d, inv) << 8 | code_of(v.y, d, inv) << 12 |
+            code_of(u.z, d, inv) << 16 | code_of(v.z, d, inv) << 20 | code_of(u.w, d, inv) << 24 |
+            code_of(v.w, d, inv) << 28;
     }
     *reinterpret_cast<uint32_t *>(codes + 4 * j) = w;
     if (j == 0) *scale = s;
@@ -115,8 +130,9 @@ __device__ __forceinline__ Place place_of(const KvQ4View &c, int row, int ended)
 // (in the piece itself for fp32, beside it for bfloat16), and four lanes then
 // quantise a block.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 6) kv_append_q4_kernel(const KvAppendArgs a, const KvQ4View c, int heads,
-                                                                   unsigned int *err) {
+__global__ void __launch_bounds__(kThreads, 5)
+    kv_append_q4_kernel(const KvAppendArgs a, const KvQ4View c, int heads, Divisor per_head, Divisor blocks,
+                        unsigned int *err) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t full;
     __shared__ int abort_flag;
@@ -166,9 +182,9 @@ __global__ void __launch_bounds__(kThreads, 6) kv_append_q4_kernel(const KvAppen
     }
     const float *cs = a.cos_sin + (int64_t)turn_row * a.rot;
     __nv_bfloat16 *q_row = a.q_out + (int64_t)row * a.q_heads * c.head_dim;
-    const int per_head = c.head_dim / kVec, half = a.rot / 2;
-    for (int it = threadIdx.x; it < value0 * per_head; it += kThreads) {
-        const int in_piece = it / per_head, i = it - in_piece * per_head;
+    const int items = c.head_dim / kVec, half = a.rot / 2;  // of a head
+    for (int it = threadIdx.x; it < value0 * items; it += kThreads) {
+        const int in_piece = per_head(it), i = it - in_piece * items;
         const bool turned = i * kVec < a.rot, query = in_piece < key0;
         if (kInPlace && !turned && !query) continue;
         // first elements of the item's two halves
@@ -198,10 +214,10 @@ __global__ void __launch_bounds__(kThreads, 6) kv_append_q4_kernel(const KvAppen
     }
     if (key0 == n_heads) return;
     __syncthreads();
-    const int blocks = c.head_dim / 32, j = threadIdx.x & 3;
+    const int j = threadIdx.x & 3, per_token = c.head_dim / 32;
     const uint32_t quad = 15u << (threadIdx.x & 28);
-    for (int it = threadIdx.x >> 2; it < (n_heads - key0) * blocks; it += kThreads / 4) {
-        const int in_piece = key0 + it / blocks, block = it % blocks, e = block * 32 + 4 * j;
+    for (int it = threadIdx.x >> 2; it < (n_heads - key0) * per_token; it += kThreads / 4) {
+        const int of = blocks(it), in_piece = key0 + of, block = it - of * per_token, e = block * 32 + 4 * j;
         const bool key = in_piece < value0;
         float4 u, v;
         if (key) {
@@ -229,7 +245,8 @@ cudaError_t launch_append(const KvAppendArgs &a, const KvQ4View &c, int64_t rows
         const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kv_append_q4_kernel<T>), smem);
         if (e != cudaSuccess) return e;
     }
-    return launch_pdl(kv_append_q4_kernel<T>, dim3((unsigned)rows, pieces), dim3(kThreads), smem, s, a, c, heads, err);
+    return launch_pdl(kv_append_q4_kernel<T>, dim3((unsigned)rows, pieces), dim3(kThreads), smem, s, a, c, heads,
+                      Divisor(c.head_dim / kVec), Divisor(c.head_dim / 32), err);
 }
 
 // The values of four nibbles (the low ones, or after a shift the high ones, of
@@ -251,19 +268,24 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, float4 a, float4 b) {
         make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
 }
 
-constexpr int kReadRows = 8;  // rows of a CTA, each warp finds the place of one
+// Rows of a CTA, of whose places each warp finds one or two: 16 where there are
+// enough of them to fill the SMs (73 thousand rows take 77 us, with 8 rows 80;
+// 515 rows 3.6 us with 8, with 16 rows 5.4).
+constexpr int kReadRows = 8, kMostReadRows = 16, kManyRows = 16384;
 
-// blockIdx.x: kReadRows rows of the batch.  A thread reads half a block (8
-// bytes of codes) and writes its 16 values.  Bound by the writes.
+// blockIdx.x: `per_cta` rows of the batch.  A thread reads half a block (8
+// bytes of codes) of every few rows and writes its 16 values: `width` threads
+// have a row at once (a row's half blocks, kThreads at most).  Bound by the
+// writes.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) kv_read_q4_kernel(const KvQ4View c, int rows, T *k_out, T *v_out,
-                                                              unsigned int *err) {
-    __shared__ int2 at[kReadRows];  // page (-1: none) and token of each row
+__global__ void __launch_bounds__(kThreads) kv_read_q4_kernel(const KvQ4View c, int rows, int per_cta, int width,
+                                                              T *k_out, T *v_out, unsigned int *err) {
+    __shared__ int2 at[kMostReadRows];  // page (-1: none) and token of each row
     pdl_launch_dependents();
     pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row0 = blockIdx.x * kReadRows;
-    {
-        const int row = row0 + warp;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row0 = blockIdx.x * per_cta;
+    for (int r = warp; r < per_cta; r += kThreads / 32) {
+        const int row = row0 + r;
         int ended = 0;
         for (int base = 0; base < c.sequences; base += 32) {
             const int b = base + lane;
@@ -272,26 +294,45 @@ __global__ void __launch_bounds__(kThreads) kv_read_q4_kernel(const KvQ4View c, 
         if (lane == 0) {
             const Place p = row < rows ? place_of(c, row, ended) : Place{};
             if (p.in_sequence && !p.ok) report_index(err);
-            at[warp] = make_int2(p.ok ? p.page : -1, p.off);
+            at[r] = make_int2(p.ok ? p.page : -1, p.off);
         }
     }
     __syncthreads();
-    const int halves = c.head_dim / 16, per_side = c.kv_heads * halves, per_row = 2 * per_side;
-    for (int it = threadIdx.x; it < kReadRows * per_row; it += kThreads) {
-        const int r = it / per_row, i = it - r * per_row;
-        const int2 place = at[r];
-        if (place.x < 0) continue;
+    const int halves = c.head_dim / 16, per_side = c.kv_heads * halves;
+    const int at_once = kThreads / width, first = threadIdx.x / width;
+    if (first >= at_once) return;
+    for (int i = threadIdx.x - first * width; i < 2 * per_side; i += width) {
         const bool key = i < per_side;
         const int in_side = key ? i : i - per_side, head = in_side / halves, h = in_side - head * halves;
         const int64_t *st = key ? c.k_stride : c.v_stride, *ss = key ? c.k_scale_stride : c.v_scale_stride;
-        const uint2 w = *reinterpret_cast<const uint2 *>((key ? c.k : c.v) + place.x * st[0] + head * st[1] +
-                                                         place.y * st[2] + h * 8);
-        const float d = __half2float(__ushort_as_half(
-            (key ? c.k_scale : c.v_scale)[place.x * ss[0] + head * ss[1] + place.y * ss[2] + (h >> 1)]));
-        T *dst = (key ? k_out : v_out) + ((int64_t)(row0 + r) * c.kv_heads + head) * c.head_dim + (h >> 1) * 32 +
-                 (h & 1) * 8;
-        store8(dst, values4(w.x, d), values4(w.y, d));
-        store8(dst + 16, values4(w.x >> 4, d), values4(w.y >> 4, d));
+        const uint8_t *codes = (key ? c.k : c.v) + head * st[1] + h * 8;
+        const uint16_t *scales = (key ? c.k_scale : c.v_scale) + head * ss[1] + (h >> 1);
+        T *out = (key ? k_out : v_out) + ((int64_t)row0 * c.kv_heads + head) * c.head_dim + (h >> 1) * 32 + (h & 1) * 8;
+        const int row_step = c.kv_heads * c.head_dim;
+        // several rows' reads are under way at once
+        constexpr int kAtOnce = 4;
+        for (int r0 = first; r0 < per_cta; r0 += kAtOnce * at_once) {
+            uint2 w[kAtOnce];
+            uint16_t d[kAtOnce];
+            bool ok[kAtOnce];
+#pragma unroll
+            for (int x = 0; x < kAtOnce; ++x) {
+                const int r = r0 + x * at_once;
+                const int2 place = r < per_cta ? at[r] : make_int2(-1, 0);
+                ok[x] = place.x >= 0;
+                if (!ok[x]) continue;
+                w[x] = *reinterpret_cast<const uint2 *>(codes + place.x * st[0] + place.y * st[2]);
+                d[x] = scales[place.x * ss[0] + place.y * ss[2]];
+            }
+#pragma unroll
+            for (int x = 0; x < kAtOnce; ++x) {
+                if (!ok[x]) continue;
+                const float f = __half2float(__ushort_as_half(d[x]));
+                T *dst = out + (int64_t)(r0 + x * at_once) * row_step;
+                store8(dst, values4(w[x].x, f), values4(w[x].y, f));
+                store8(dst + 16, values4(w[x].x >> 4, f), values4(w[x].y >> 4, f));
+            }
+        }
     }
 }
 
@@ -304,12 +345,14 @@ cudaError_t launch_kv_append_q4(const KvAppendArgs &a, const KvQ4View &c, int64_
 
 cudaError_t launch_kv_read_q4(const KvQ4View &c, int64_t rows, void *k_out, void *v_out, bool bf16, cudaStream_t s,
                               unsigned int *err) {
-    const dim3 grid((unsigned)((rows + kReadRows - 1) / kReadRows));
+    const int per_cta = rows < kManyRows ? kReadRows : kMostReadRows;
+    const dim3 grid((unsigned)((rows + per_cta - 1) / per_cta));
+    const int halves = 2 * c.kv_heads * (c.head_dim / 16), width = halves < kThreads ? halves : kThreads;
     if (bf16)
-        return launch_pdl(kv_read_q4_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, s, c, (int)rows,
+        return launch_pdl(kv_read_q4_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, s, c, (int)rows, per_cta, width,
                           static_cast<__nv_bfloat16 *>(k_out), static_cast<__nv_bfloat16 *>(v_out), err);
-    return launch_pdl(kv_read_q4_kernel<float>, grid, dim3(kThreads), 0, s, c, (int)rows, static_cast<float *>(k_out),
-                      static_cast<float *>(v_out), err);
+    return launch_pdl(kv_read_q4_kernel<float>, grid, dim3(kThreads), 0, s, c, (int)rows, per_cta, width,
+                      static_cast<float *>(k_out), static_cast<float *>(v_out), err);
 }
 
 }  // namespace q4_0
