@@ -567,7 +567,7 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                                                                                            in_box < clip >> 14));
                             copy_small<L::kScaleRow>(to + t * L::kScaleRow,
                                                      base + (seen ? page * st[0] + off * st[2] : 0),
-                                                     seen ? L::kScaleRow : 0);
+                                                     !seen);
                         }
                         copy_arrive(&full[slot]);
                     }

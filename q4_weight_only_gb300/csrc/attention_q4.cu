@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < kTile / kAtOnce; ++j) {
                 const int group = D == 128 ? j : 2 * j + (lane >> 4);
                 const uint64_t from = __shfl_sync(0xffffffffu, codes, group) + lane_bytes;
-                copy16(to + j * kAtOnce * L::kRow, reinterpret_cast<const void *>(from), groups >> group & 1 ? 16 : 0);
+                copy16(to + j * kAtOnce * L::kRow, reinterpret_cast<const void *>(from), !(groups >> group & 1));
             }
             const uint32_t scale_to = lane_scale_to + slot * L::kStageBytes;
 #pragma unroll
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t from = __shfl_sync(0xffffffffu, scales, group) + 2 * lane_scale;
                 const bool seen = (groups >> group & 1) && (now.seen >> x & 1);
                 copy_small<L::kScales>(scale_to + x * 32 * L::kScales, reinterpret_cast<const void *>(from),
-                                       seen ? L::kScales : 0);
+                                       !seen);
             }
             copy_arrive(&bar.full[kv][slot]);
             slot += kCopyTurns;

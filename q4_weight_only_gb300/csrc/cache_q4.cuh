@@ -34,14 +34,23 @@ bool make_codes_map(EncodeTiledFn enc, CUtensorMap *map, const uint8_t *base, co
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Asynchronous copies of 16, 8 or 4 bytes; nothing is read and zeros are
-// written where `bytes` is 0.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// Asynchronous copies of 16, 8 or 4 bytes; where `skip`, nothing is read and
+// zeros are written.  (A predicate, not a size of 0: the compiler makes one
+// instruction of it.)
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool skip) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+        "cp.async.cg.shared.global [%0], [%1], 16, p;\n\t}" ::"r"(dst),
+        "l"(src), "r"((uint32_t)skip)
+        : "memory");
 }
 template <int kBytes>
-__device__ __forceinline__ void copy_small(uint32_t dst, const void *src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(bytes) : "memory");
+__device__ __forceinline__ void copy_small(uint32_t dst, const void *src, bool skip) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+        "cp.async.ca.shared.global [%0], [%1], %2, p;\n\t}" ::"r"(dst),
+        "l"(src), "n"(kBytes), "r"((uint32_t)skip)
+        : "memory");
 }
 // An arrival on `bar` once the thread's copies so far have landed (one of the
 // arrivals that the barrier counts).
