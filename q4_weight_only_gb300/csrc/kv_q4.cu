@@ -55,15 +55,31 @@ __device__ __forceinline__ void turn(float &a, float &b, float cosv, float sinv)
     b = __fadd_rn(__fmul_rn(b, cosv), __fmul_rn(a0, sinv));
 }
 
-// clamp(round(w / d), -8, 7) + 8, halves away from zero, with `inv` the
-// reciprocal of d.  w inv is within 3 2^-24 |w / d| <= 2^-19 of the quotient:
-// only where it is that near to a half does the quotient itself decide (0 / 0
-// and a d that became 0 give codes that its scale of 0 makes no difference of).
-__device__ __forceinline__ uint32_t code_of(float w, float d, float inv) {
-    float q = w * inv;
-    const float half = fabsf(fabsf(q) - floorf(fabsf(q)) - 0.5f);
-    if (!(half > 0x1p-19f)) q = __fdiv_rn(w, d);
-    return (uint32_t)(int)(fminf(fmaxf(roundf(q), -8.f), 7.f) + 8.f);
+// clamp(round(w / d), -8, 7) + 8, halves away from zero (0 / 0 and a d that
+// became 0 give codes that its scale of 0 makes no difference of).
+__device__ __forceinline__ uint32_t code_of(float w, float d) {
+    return (uint32_t)(int)(fminf(fmaxf(roundf(__fdiv_rn(w, d)), -8.f), 7.f) + 8.f);
+}
+
+// The codes of eight elements, w[0] in the lowest four bits.  q = w / d rounded
+// twice, by the reciprocal and the product, is within 3 2^-24 |w / d| < 2^-19
+// of the quotient that code_of rounds: they round to the same whole number
+// unless q is next to a half, and then the quotients decide.
+__device__ __forceinline__ uint32_t codes_of(const float (&w)[8], float d) {
+    const float inv = __frcp_rn(d), base = 12582920.f;  // 1.5 2^23 + 8: whole numbers are its last bits
+    uint32_t codes = 0;
+    bool sure = true;
+#pragma unroll
+    for (int i = 7; i >= 0; --i) {
+        const float q = w[i] * inv, t = __fadd_rn(q, base);
+        sure &= fabsf(q - __fsub_rn(t, base)) < 0.5f - 0x1p-19f;  // (false for NaN)
+        codes = codes * 16 + min(__float_as_uint(t) & 31u, 15u);
+    }
+    if (!sure) {
+        codes = 0;
+        for (int i = 7; i >= 0; --i) codes = codes * 16 + code_of(w[i], d);
+    }
+    return codes;
 }
 
 // The largest element of a block so far.
@@ -97,10 +113,8 @@ __device__ __forceinline__ void quantise_quad(float4 u, float4 v, int j, uint32_
     } else if (m.size > 0.f) {
         const float d = __fmul_rn(m.value, -0.125f);
         s = __half_as_ushort(__float2half_rn(d));
-        const float inv = __frcp_rn(d);
-        w = code_of(u.x, d, inv) | code_of(v.x, d, inv) << 4 | code_of(u.y, d, inv) << 8 | code_of(v.y, d, inv) << 12 |
-            code_of(u.z, d, inv) << 16 | code_of(v.z, d, inv) << 20 | code_of(u.w, d, inv) << 24 |
-            code_of(v.w, d, inv) << 28;
+        const float e[8] = {u.x, v.x, u.y, v.y, u.z, v.z, u.w, v.w};
+        w = codes_of(e, d);
     }
     *reinterpret_cast<uint32_t *>(codes + 4 * j) = w;
     if (j == 0) *scale = s;
@@ -249,14 +263,12 @@ cudaError_t launch_append(const KvAppendArgs &a, const KvQ4View &c, int64_t rows
                       Divisor(c.head_dim / kVec), Divisor(c.head_dim / 32), err);
 }
 
-// The values of four nibbles (the low ones, or after a shift the high ones, of
-// a word's bytes) times d.
+// What the four bytes of `w`, codes, stand for: a byte in the upper mantissa of
+// 2^23 is 2^16 (128 + code), and (128 + code) d - 136 d is exact.
 __device__ __forceinline__ float4 values4(uint32_t w, float d) {
-    // 2^23 + code less 2^23 + 8: exact
-    const float base = 8388616.f;
-    const uint32_t m = 0x4B000000u;
-    return make_float4((__uint_as_float((w & 15u) | m) - base) * d, (__uint_as_float((w >> 8 & 15u) | m) - base) * d,
-                       (__uint_as_float((w >> 16 & 15u) | m) - base) * d, (__uint_as_float((w >> 24 & 15u) | m) - base) * d);
+    const float unit = d * 0x1p-16f, less = -136.f * d;
+    auto value = [&](uint32_t sel) { return fmaf(__uint_as_float(__byte_perm(w, 0x4B000000u, sel)), unit, less); };
+    return make_float4(value(0x7044), value(0x7144), value(0x7244), value(0x7344));
 }
 
 __device__ __forceinline__ void store8(float *p, float4 a, float4 b) {
@@ -321,16 +333,19 @@ __global__ void __launch_bounds__(kThreads) kv_read_q4_kernel(const KvQ4View c, 
                 const int2 place = r < per_cta ? at[r] : make_int2(-1, 0);
                 ok[x] = place.x >= 0;
                 if (!ok[x]) continue;
-                w[x] = *reinterpret_cast<const uint2 *>(codes + place.x * st[0] + place.y * st[2]);
-                d[x] = scales[place.x * ss[0] + place.y * ss[2]];
+                // (32 by 64 bits: two instructions a product)
+                const uint64_t page = (uint32_t)place.x, off = (uint32_t)place.y;
+                w[x] = *reinterpret_cast<const uint2 *>(codes + page * st[0] + off * st[2]);
+                d[x] = scales[page * ss[0] + off * ss[2]];
             }
 #pragma unroll
             for (int x = 0; x < kAtOnce; ++x) {
                 if (!ok[x]) continue;
                 const float f = __half2float(__ushort_as_half(d[x]));
                 T *dst = out + (int64_t)(r0 + x * at_once) * row_step;
-                store8(dst, values4(w[x].x, f), values4(w[x].y, f));
-                store8(dst + 16, values4(w[x].x >> 4, f), values4(w[x].y >> 4, f));
+                const uint32_t low = 0x0F0F0F0Fu;
+                store8(dst, values4(w[x].x & low, f), values4(w[x].y & low, f));
+                store8(dst + 16, values4(w[x].x >> 4 & low, f), values4(w[x].y >> 4 & low, f));
             }
         }
     }
