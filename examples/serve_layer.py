@@ -1,12 +1,13 @@
 """One served decoder layer end to end: Q4_0 matmuls with the operators
 between and after them.
 
-    python examples/serve_layer.py [--steps 8] [--window 0] [--sinks 0]
+    python examples/serve_layer.py [--steps 8] [--window 0] [--sinks 0] [--cache bf16|q4]
 
 A batch of prompts goes through the layer in one call each of
   matmul(QKV) -> kv_append -> attention -> matmul(O) -> matmul(vocabulary)
   -> token_logprobs,
-then every sequence decodes token by token on the same calls.  Weights and
+then every sequence decodes token by token on the same calls.  The cache is in
+bfloat16, or in 4 bits (kv_append_q4 and attention_q4).  Weights and
 prompts are random (no checkpoint is needed); the layer has 40 query and 8 key
 heads of 128 on a hidden size of 5120, the QKV 7168 x 5120 and O 5120 x 5120
 matrices of the benchmark.  The last step's log probabilities are compared
@@ -27,13 +28,19 @@ HIDDEN, Q_HEADS, KV_HEADS, DIM, VOCAB, PAGE = 5120, 40, 8, 128, 32000, 16
 
 
 class Cache:
-    """Pages of a key and a value cache, handed out as sequences grow."""
+    """Pages of a key and a value cache (bf16 or q4), handed out as sequences
+    grow."""
 
-    def __init__(self, sequences, tokens):
+    def __init__(self, sequences, tokens, kind):
         per_sequence = -(-tokens // PAGE)
         pages = sequences * per_sequence
-        self.k = torch.empty(pages, KV_HEADS, PAGE, DIM, dtype=torch.bfloat16, device="cuda")
-        self.v = torch.empty_like(self.k)
+        if kind == "q4":
+            self.append, self.attention = q4.kv_append_q4, q4.attention_q4
+            self.tensors = (q4.kv_cache_q4(pages, KV_HEADS, PAGE, DIM),)
+        else:
+            self.append, self.attention = q4.kv_append, q4.attention
+            k = torch.empty(pages, KV_HEADS, PAGE, DIM, dtype=torch.bfloat16, device="cuda")
+            self.tensors = (k, torch.empty_like(k))
         order = torch.randperm(pages, generator=torch.Generator().manual_seed(0))
         self.table = order.to(torch.int32).view(sequences, per_sequence).cuda()
         self.length = torch.zeros(sequences, dtype=torch.int32, device="cuda")
@@ -60,21 +67,21 @@ class Layer:
         `lengths` of them new in each."""
         starts = torch.tensor([0] + lengths).cumsum(0).to(torch.int32).cuda()
         cache.length += torch.tensor(lengths, dtype=torch.int32, device="cuda")
-        batch = (cache.k, cache.v, cache.table, starts, cache.length)
+        batch = (*cache.tensors, cache.table, starts, cache.length)
         x = self.embedding[tokens]
         qkv = q4.matmul(x, self.qkv, self.width, HIDDEN)
-        q = q4.kv_append(qkv, self.cos_sin, *batch, q_heads=Q_HEADS)
-        a = q4.attention(q, *batch, max_q_len=max(lengths), window=self.window, sinks=self.sinks)
+        q = cache.append(qkv, self.cos_sin, *batch, q_heads=Q_HEADS)
+        a = cache.attention(q, *batch, max_q_len=max(lengths), window=self.window, sinks=self.sinks)
         y = q4.matmul(a.view(len(tokens), Q_HEADS * DIM), self.o, HIDDEN, Q_HEADS * DIM, out_dtype=torch.bfloat16)
         return q4.matmul(x + y, self.vocab, VOCAB, HIDDEN)
 
 
-def main(steps=8, window=0, sinks=0, verbose=True):
+def main(steps=8, window=0, sinks=0, verbose=True, cache_kind="bf16"):
     lengths = [37, 5, 300, 128]
     layer = Layer(max(lengths) + steps + 1, window, sinks)
     g = torch.Generator(device="cuda").manual_seed(2)
     texts = [torch.randint(0, VOCAB, (n,), generator=g, device="cuda") for n in lengths]
-    cache = Cache(len(texts), max(lengths) + steps + 1)
+    cache = Cache(len(texts), max(lengths) + steps + 1, cache_kind)
 
     # the prompts: each token's log probability after the ones before it
     logits = layer(torch.cat(texts), lengths, cache)
@@ -98,7 +105,7 @@ def main(steps=8, window=0, sinks=0, verbose=True):
         last = layer(ids[:, 0], [1] * len(texts), cache)
 
     # the same sequences at once, in a fresh cache
-    whole = Cache(len(texts), max(lengths) + steps + 1)
+    whole = Cache(len(texts), max(lengths) + steps + 1, cache_kind)
     counts = [len(t) for t in texts]
     logits = layer(torch.cat(texts), counts, whole)[(torch.tensor(counts).cumsum(0) - 1).cuda()]
     tokens = torch.zeros(len(texts), dtype=torch.int64, device="cuda")
@@ -116,5 +123,6 @@ if __name__ == "__main__":
     p.add_argument("--steps", type=int, default=8)
     p.add_argument("--window", type=int, default=0)
     p.add_argument("--sinks", type=int, default=0)
+    p.add_argument("--cache", choices=["bf16", "q4"], default="bf16")
     a = p.parse_args()
-    main(a.steps, a.window, a.sinks)
+    main(a.steps, a.window, a.sinks, cache_kind=a.cache)

@@ -531,8 +531,8 @@ int q4_0_kv_append(const void *qkv, int qkv_type, int64_t qkv_stride, int64_t ro
     KvCacheView c;
     int st = cache_view(cache, &c);
     if (st != Q4_0_OK) return st;
-    st = append_fits(qkv, qkv_type, qkv_stride, rows, q_heads, cos_sin, positions, rot, row_positions, q_out, c.kv_heads,
-                     c.head_dim);
+    st = append_fits(qkv, qkv_type, qkv_stride, rows, q_heads, cos_sin, positions, rot, row_positions, q_out,
+                     c.kv_heads, c.head_dim);
     if (st != Q4_0_OK) return st;
     if (rows == 0 || c.sequences == 0) return Q4_0_OK;
     unsigned int *err = device_error_word();
@@ -548,8 +548,8 @@ int q4_0_kv_append_q4(const void *qkv, int qkv_type, int64_t qkv_stride, int64_t
     KvQ4View c;
     int st = cache_q4_view(cache, &c);
     if (st != Q4_0_OK) return st;
-    st = append_fits(qkv, qkv_type, qkv_stride, rows, q_heads, cos_sin, positions, rot, row_positions, q_out, c.kv_heads,
-                     c.head_dim);
+    st = append_fits(qkv, qkv_type, qkv_stride, rows, q_heads, cos_sin, positions, rot, row_positions, q_out,
+                     c.kv_heads, c.head_dim);
     if (st != Q4_0_OK) return st;
     if (rows == 0 || c.sequences == 0) return Q4_0_OK;
     unsigned int *err = device_error_word();
@@ -569,8 +569,8 @@ int q4_0_kv_read_q4(void *k_out, void *v_out, int out_type, int64_t rows, const 
     if (rows == 0 || c.sequences == 0) return Q4_0_OK;
     unsigned int *err = device_error_word();
     if (!err) return Q4_0_ERR_CUDA;
-    return from_cuda(launch_kv_read_q4(c, rows, k_out, v_out, out_type == Q4_0_Y_BF16, static_cast<cudaStream_t>(stream),
-                                       err));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return from_cuda(launch_kv_read_q4(c, rows, k_out, v_out, out_type == Q4_0_Y_BF16, s, err));
 }
 
 namespace {
@@ -623,8 +623,8 @@ int q4_0_attention(const uint16_t *q, int64_t q_row_stride, int64_t q_head_strid
     int st = cache_view(cache, &c);
     if (st != Q4_0_OK) return st;
     AttentionArgs a{};
-    st = attention_args(q, q_row_stride, q_head_stride, out, out_type, lse, rows, q_heads, max_q_len, scale, window, sinks,
-                        c.kv_heads, c.head_dim, c.page_size, &a);
+    st = attention_args(q, q_row_stride, q_head_stride, out, out_type, lse, rows, q_heads, max_q_len, scale, window,
+                        sinks, c.kv_heads, c.head_dim, c.page_size, &a);
     if (st != Q4_0_OK) return st;
     if (rows == 0 || c.sequences == 0) return Q4_0_OK;
     const size_t need = q4_0_attention_workspace_bytes(rows, q_heads, c.kv_heads, c.head_dim, max_q_len);
@@ -659,8 +659,8 @@ int q4_0_attention_q4(const uint16_t *q, int64_t q_row_stride, int64_t q_head_st
     int st = cache_q4_view(cache, &c);
     if (st != Q4_0_OK) return st;
     AttentionArgs a{};
-    st = attention_args(q, q_row_stride, q_head_stride, out, out_type, lse, rows, q_heads, max_q_len, scale, window, sinks,
-                        c.kv_heads, c.head_dim, c.page_size, &a);
+    st = attention_args(q, q_row_stride, q_head_stride, out, out_type, lse, rows, q_heads, max_q_len, scale, window,
+                        sinks, c.kv_heads, c.head_dim, c.page_size, &a);
     if (st != Q4_0_OK) return st;
     if (attention_q4_sizes(rows, q_heads, c.kv_heads, c.head_dim, max_q_len) != Q4_0_OK) return Q4_0_ERR_UNSUPPORTED;
     // a token's scales are copied at once

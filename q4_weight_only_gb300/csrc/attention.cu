@@ -55,6 +55,24 @@
 //   take 265 us.
 // * One token after 2047 takes 16.7 us against a floor of 1.2: 4.3 launch, 4
 //   join, the rest reads that wait for one another.
+//
+// A cache in Q4_0 blocks (attention_q4_wide_kernel; sequences of few rows are
+// attention_q4.cu's).  The same warps, and four more: codes and scales come
+// through a ring of their own, warps 12 to 15 unpack tiles of binary16 from it
+// into the ring that the MMAs read, and the softmax warps turn their rows of Q
+// to binary16.  The copies are a quarter of the bytes; what bounds a tile is
+// the unpacking and what it costs the others:
+// * 8192 tokens after 8192 others take 1.61 ms, 1.28 PFLOP/s.  Without the
+//   unpacking's arithmetic it is 1.55, without its reads and stores 1.43: its
+//   warps take 2240 of the 3700 cycles of a pair of tiles, and the stores of
+//   64 KB compete with the MMAs' reads for shared memory.  Three unpacking
+//   warps in the copy warps' places took 3.28 ms; four that copied for
+//   themselves 1.94.
+// * The windowed prompts at D = 64 take 200 us.
+// * 5 drafted tokens of 16 sequences under a window of 4096: 70 us, 3600 cycles
+//   a key tile, of which the unpacking is 1800 (bfloat16: 60 us).
+// * Rings of 3 unpacked tiles and 6 of codes instead of 4 and 3 (D = 64: 6 and
+//   12 instead of 8 and 6): prompts 3 % slower, the others level.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -563,11 +581,10 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                             const int page = __shfl_sync(0xffffffffu, now.page, j * boxes + box);
                             const int off = __shfl_sync(0xffffffffu, now.off, j * boxes + box) + in_box;
                             const int clip = __shfl_sync(0xffffffffu, now.clip, j * boxes + box);
-                            const bool seen = page < p.pages && (in_box < (clip & 127) || (in_box >= (clip >> 7 & 127) &&
-                                                                                           in_box < clip >> 14));
+                            const bool in_window = in_box >= (clip >> 7 & 127) && in_box < clip >> 14;
+                            const bool seen = page < p.pages && (in_box < (clip & 127) || in_window);
                             copy_small<L::kScaleRow>(to + t * L::kScaleRow,
-                                                     base + (seen ? page * st[0] + off * st[2] : 0),
-                                                     !seen);
+                                                     base + (seen ? page * st[0] + off * st[2] : 0), !seen);
                         }
                         copy_arrive(&full[slot]);
                     }
@@ -809,7 +826,8 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                 q_tiles += wide ? 2 : 1;
                 if (wide || g == 0) {
                     if (!wait(&bar.q_full[at], parity)) break;
-                    bar.q_down[half][row] = valid ? q_to_f16<D>(smem + L::kQ + at * L::kTileBytes, L::kBlock, row) : 1.f;
+                    uint8_t *tile = smem + L::kQ + at * L::kTileBytes;
+                    bar.q_down[half][row] = valid ? q_to_f16<D>(tile, L::kBlock, row) : 1.f;
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.q_ready[at]);

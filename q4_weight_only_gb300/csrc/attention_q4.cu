@@ -21,6 +21,35 @@
 //   largest, off by at most 2^-39 of that below;
 // * p, at most 2^8, rounded (2^-11, and 2^-25 where it is below 2^-14); l sums p
 //   before the rounding.
+//
+// Two kernels.  Sequences of at most 16 rows, (token, head of the group) pairs,
+// are this file's: their few rows are the narrow operand of m16n8k16 products
+// with the keys and values as the wide one, which warps unpack straight from
+// the codes into their registers.  Nothing unpacked is written anywhere, and
+// a tcgen05 operand in shared memory is not worth it for codes that so few rows
+// use: 64 sequences' next tokens take twice as long there (351 and 700 us).
+// Longer sequences fill tcgen05's tiles of 128 rows and are attention.cu's
+// 4-bit variant: 16 sequences' 5 drafted tokens by 5 heads, 25 rows each, take
+// 70 us there, and 85 as two items of 16 here.
+//
+// Layout of work: an item is 8 or 16 rows of one sequence and key head, its
+// cost the key tiles it sees; CTAs, one an SM, take equal shares of all cost,
+// and attention_q4_join_kernel adds what a share's boundary cut, in share
+// order.
+//
+// Bounds and measurements (40 query heads on 8 key heads of 128, device time):
+// * 64 sequences' next tokens, 4 to 32 thousand tokens each, 1.29 GB: 351 us,
+//   3.7 TB/s, 0.55 of a copy's rate, where the bfloat16 cache takes 663.  Copies
+//   alone take 241 us and the arithmetic alone 258: 400 warp instructions for
+//   16 keys and values fill 60 % of the issue slots (logic and integers 49 %
+//   of their pipe, multiply-adds 36 %, tensor 20 %, HBM 50 %).
+// * 16 sequences of 1 to 8 thousand, 98 MB: 41 us (bfloat16: 69), of which 12
+//   are the launches, the first reads and the join.
+// * One token after 2047: 11.6 us (bfloat16: 14.7).
+// * Pages that hold a head's tokens in a row are 12 % faster than pages that
+//   hold a token's heads in a row: a token's scales of one head are 8 bytes,
+//   and a sector of 32 holds four tokens' of the head then (605 against 807 MB
+//   into the SMs for 32 sequences of 16384; 155 against 177 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -52,9 +81,9 @@ struct Params {
     int64_t table_stride;
     int sequences, table_width, pages, page_size, rows, max_q_len;
     int q_heads, kv_heads, group, window, sinks;
-    int most_rows;  // of a sequence; longer ones are another kernel's
+    int most_rows;              // of a sequence; longer ones are another kernel's
     int step_pages, step_rest;  // kCopyTurns tiles by page_size
-    int item_rows;  // rows of an item: (token, head of the group) pairs of a sequence, in order
+    int item_rows;              // rows of an item: (token, head of the group) pairs of a sequence, in order
     const __nv_bfloat16 *q;
     int64_t q_row_stride, q_head_stride;
     float scale_log2;
@@ -63,7 +92,9 @@ struct Params {
     int out_bf16;
     float *part;       // [CTA][head piece, tail piece][item_rows][D], unnormalised
     float4 *part_mlc;  // the rows' m, l and c
-    int4 *record;      // per CTA: flags, then first row (token * group + head), rows and key head of the tail piece's item
+    // per CTA: flags, then first row (token * group + head), rows and key head
+    // of the tail piece's item
+    int4 *record;
     unsigned int *err;
 };
 
@@ -221,7 +252,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto item = [&]() -> const Item & { return bar.item[items % kItems]; };
     // Whether the item's record is there (false: a wait was abandoned).
     auto item_there = [&]() {
-        return __all_sync(0xffffffffu, mbar_wait(&bar.item_full[items % kItems], items / kItems & 1, abort_flag, p.err));
+        uint64_t *const full = &bar.item_full[items % kItems];
+        return __all_sync(0xffffffffu, mbar_wait(full, items / kItems & 1, abort_flag, p.err));
     };
     auto done_item = [&]() {
         __syncwarp();
@@ -353,8 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // tokens that no row sees, or without a page, become zeros
             const uint32_t groups = __ballot_sync(0xffffffffu, some);
             const int64_t page = some ? now.page : 0, at = some ? now.off : 0;
-            const uint64_t codes =
-                reinterpret_cast<uint64_t>(base + page * cs[0] + now.head * cs[1] + at * cs[2]);
+            const uint64_t codes = reinterpret_cast<uint64_t>(base + page * cs[0] + now.head * cs[1] + at * cs[2]);
             const uint64_t scales =
                 reinterpret_cast<uint64_t>(scale_base + page * ss[0] + now.head * ss[1] + at * ss[2]);
             if (!__all_sync(0xffffffffu, mbar_wait(&bar.empty[slot], phase, abort_flag, p.err))) break;
@@ -371,8 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int group = 4 * x + (lane >> 3);
                 const uint64_t from = __shfl_sync(0xffffffffu, scales, group) + 2 * lane_scale;
                 const bool seen = (groups >> group & 1) && (now.seen >> x & 1);
-                copy_small<L::kScales>(scale_to + x * 32 * L::kScales, reinterpret_cast<const void *>(from),
-                                       !seen);
+                copy_small<L::kScales>(scale_to + x * 32 * L::kScales, reinterpret_cast<const void *>(from), !seen);
             }
             copy_arrive(&bar.full[kv][slot]);
             slot += kCopyTurns;
@@ -452,14 +482,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < NB; ++j) {
                 // a high nibble is read as 16 codes
                 const float f16 = f * 0.0625f;
-                qf[n][j][0][0] = pair(low(lo[j].x), low(lo[j].y), f), qf[n][j][1][0] = pair(high(lo[j].x), high(lo[j].y), f);
+                qf[n][j][0][0] = pair(low(lo[j].x), low(lo[j].y), f);
+                qf[n][j][1][0] = pair(high(lo[j].x), high(lo[j].y), f);
                 qf[n][j][0][1] = pair(low(hi[j].x), low(hi[j].y), f16);
                 qf[n][j][1][1] = pair(high(hi[j].x), high(hi[j].y), f16);
                 // what the codes' 8 too many come to, in two binary16 parts
                 float sum = 0.f;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const float2 u = __half22float2(as_half2(qf[n][j][x][0])), v = __half22float2(as_half2(qf[n][j][x][1]));
+                    const float2 u = __half22float2(as_half2(qf[n][j][x][0]));
+                    const float2 v = __half22float2(as_half2(qf[n][j][x][1]));
                     sum += (u.x + u.y) + 16.f * (v.x + v.y);
                 }
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
@@ -543,7 +575,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
                             const int tok = tok0 + h * 16 + L::token(g) + (x >> 1) * 8, at = pos[n][x & 1];
-                            if (tok > at || (p.window && tok <= at - p.window && tok >= p.sinks)) sc[h][n][x] = -INFINITY;
+                            if (tok > at || (p.window && tok <= at - p.window && tok >= p.sinks))
+                                sc[h][n][x] = -INFINITY;
                         }
             }
             // references that a score outgrew move, in all lanes of a column
@@ -611,7 +644,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         d[k] = lds16(v_scales + tok * 4 + (g >> 2) * 2);
                     }
                 }
-                const __half2 d01 = as_half2(__byte_perm(d[0], d[1], 0x5410)), d23 = as_half2(__byte_perm(d[2], d[3], 0x5410));
+                const __half2 d01 = as_half2(__byte_perm(d[0], d[1], 0x5410));
+                const __half2 d23 = as_half2(__byte_perm(d[2], d[3], 0x5410));
 #pragma unroll
                 for (int j = 0; j < D / 64; ++j)
 #pragma unroll
@@ -867,10 +901,11 @@ cudaError_t launch_attention_q4(const AttentionArgs &a, const KvQ4View &c, void 
     if (sms < 1) return cudaErrorInvalidDevice;
     cudaError_t e = cudaSuccess;
     if (group <= kMostRows)
-        e = c.head_dim == 128 ? launch_d<128>(a, c, workspace, sms, s, err) : launch_d<64>(a, c, workspace, sms, s, err);
+        e = (c.head_dim == 128 ? launch_d<128> : launch_d<64>)(a, c, workspace, sms, s, err);
     if (e != cudaSuccess || (int64_t)group * a.max_q_len <= kMostRows) return e;
-    const size_t narrow = WorkspaceLayout(sms, c.head_dim, item_rows(group, a.max_q_len)).bytes;
-    return launch_attention_q4_wide(a, c, item_rows(group, a.max_q_len) + 1, static_cast<uint8_t *>(workspace) + narrow, s, err);
+    const int rows = item_rows(group, a.max_q_len);
+    uint8_t *rest = static_cast<uint8_t *>(workspace) + WorkspaceLayout(sms, c.head_dim, rows).bytes;
+    return launch_attention_q4_wide(a, c, rows + 1, rest, s, err);
 }
 
 }  // namespace q4_0
