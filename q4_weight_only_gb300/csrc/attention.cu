@@ -206,6 +206,8 @@ struct Layout {
     static constexpr int kQTiles = D == 128 ? 2 : 4;       // Q tiles held
     static constexpr int kQ = 0;
     static constexpr int kRing = kQTiles * kTileBytes;
+    // 4 bits at D = 128: masks in a pass over S of their own
+    static constexpr bool kMaskPass = kQ4 && D == 128;
     // 4 bits: a ring of tiles' codes and scales
     static constexpr int kCodes = kRing + kStages * kTileBytes;
     static constexpr int kCodeRow = D / 2, kScaleRow = D / 16, kCodeBytes = kTile * (kCodeRow + kScaleRow);
@@ -253,16 +255,15 @@ __device__ __forceinline__ uint32_t col_o(int g) { return 256 + g * 128; }
 // row of zeros or with an infinity or NaN is not scaled.
 template <int D>
 __device__ __forceinline__ float q_to_f16(uint8_t *tile, int block, int row) {
-    uint4 v[D / 8];
     uint32_t top2 = 0;  // as whole numbers, sizes of bfloat16 pairs are ordered
     auto at = [&](int i) {
         return reinterpret_cast<uint4 *>(tile + (i >> 3) * block + row * 128 + (((i & 7) ^ (row & 7)) << 4));
     };
-#pragma unroll
+#pragma unroll 4
     for (int i = 0; i < D / 8; ++i) {
-        v[i] = *at(i);
-        top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
-                                       __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu)));
+        const uint4 v = *at(i);
+        top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                       __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
     }
     const uint32_t top = max(top2 & 0xFFFFu, top2 >> 16);
     const int exponent = (int)(top >> 7);
@@ -271,8 +272,11 @@ __device__ __forceinline__ float q_to_f16(uint8_t *tile, int block, int row) {
     auto turn = [&](uint32_t w) {
         return pack_f16(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
     };
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) *at(i) = make_uint4(turn(v[i].x), turn(v[i].y), turn(v[i].z), turn(v[i].w));
+#pragma unroll 4
+    for (int i = 0; i < D / 8; ++i) {
+        const uint4 v = *at(i);
+        *at(i) = make_uint4(turn(v.x), turn(v.y), turn(v.z), turn(v.w));
+    }
     return __uint_as_float((uint32_t)(127 - up) << 23);
 }
 
@@ -444,6 +448,7 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                                                      mbar_wait(&bar.empty[slot], phase, abort_flag, p.err));
                     if (!ok) break;
                     const uint32_t src = codes + from * L::kCodeBytes;
+                    if constexpr (D == 128) {
                     uint32_t d[2];
                     if (D == 128) {
                         const uint2 x = lds64(src + kTile * L::kCodeRow + row * 8);
@@ -474,6 +479,38 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                             sts128(at + ((first ^ (row & 7)) * 16), lo);
                             sts128(at + (((first + 2) ^ (row & 7)) * 16), hi);
                         }
+                    }
+                    } else {
+                    uint2 d;
+                    if (D == 128)
+                        d = lds64(src + kTile * L::kCodeRow + row * 8);
+                    else
+                        d.x = d.y = lds32(src + kTile * L::kCodeRow + row * 4);
+                    const uint32_t dst = tiles + slot * L::kTileBytes, words = src + row * L::kCodeRow;
+                    // (rolled: straight-line code of all blocks makes the
+                    // softmax warps wait for their instructions)
+                    uint4 next = lds128(words + turn * 16);
+#pragma unroll 1
+                    for (int j = 0; j < D / 32; ++j) {
+                        const uint4 x = next;
+                        // (no load passes the stores below)
+                        if (j + 1 < D / 32) next = lds128(words + ((j + 1) ^ turn) * 16);
+                        const __half2 scale = as_half2(__byte_perm(j & 2 ? d.y : d.x, 0, j & 1 ? 0x3232 : 0x1010));
+                        const uint32_t at = dst + (j >> 1) * L::kBlock, first = (j & 1) * 4;
+                        const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            // eight bytes: elements 8h .. 8h + 7 of the block and 16 further
+                            uint32_t lo[4], hi[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t w = __byte_perm(words[2 * h + i / 2], 0, i & 1 ? 0x4342 : 0x4140);
+                                lo[i] = times(low_codes(w, bias), scale), hi[i] = times(high_codes(w, bias), scale);
+                            }
+                            sts128(at + (((first + h) ^ (row & 7)) * 16), lo);
+                            sts128(at + (((first + h + 2) ^ (row & 7)) * 16), hi);
+                        }
+                    }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -711,10 +748,17 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
             if (!q_full(q)) break;
             if (wide) {
                 uint32_t slot_k = fills % kStages, slot_v = (fills + 1) % kStages;
-                if (!full(fills) || !q_full(q + 1)) break;
+                if (!full(fills) || (!kQ4 && !q_full(q + 1))) break;
                 tc_fence_after();
+                if (elect_one()) scores(0, q, slot_k, n == 1);
+                if constexpr (kQ4) {
+                    // group B turns its Q to binary16 when it is done with the
+                    // last item: A does not wait for that
+                    __syncwarp();
+                    if (!q_full(q + 1)) break;
+                    tc_fence_after();
+                }
                 if (elect_one()) {
-                    scores(0, q, slot_k, n == 1);
                     scores(1, q + 1, slot_k, n == 1);
                     mma_commit(&bar.empty[slot_k]);
                 }
@@ -849,6 +893,32 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                 s_phase ^= 1;
                 tc_fence_after();
                 if (busy) {
+                    // masks in a pass of their own, a quarter of S at a time
+                    if constexpr (L::kMaskPass) {
+                        const int tok0 = item().key_tile(t) * kTile;
+                        const int pos_a = item().pos0 + half * p.tokens;
+                        const int pos_z = item().pos0 + min((half + 1) * p.tokens, item().tokens) - 1;
+                        if (tok0 + kTile - 1 > pos_a ||
+                            (p.window && tok0 <= pos_z - p.window && tok0 + kTile > p.sinks)) {
+                            const int end = pos + 1 - tok0;
+                            const int first = p.window ? end - p.window : 0;
+                            const int sink = p.sinks - tok0;
+#pragma unroll 1
+                            for (int q = 0; q < 4; ++q) {
+                                const uint32_t seen =
+                                    below(end - q * 32) & (~below(first - q * 32) | below(sink - q * 32));
+                                if (__all_sync(0xffffffffu, seen == ~0u)) continue;
+                                uint32_t v[32];
+                                tmem_ld32(ts + q * 32, v);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (!(seen >> e & 1)) v[e] = 0xFF800000u;
+                                tmem_st32(ts + q * 32, v);
+                            }
+                            tmem_wait_st();
+                        }
+                    }
                     uint32_t s[4][32];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) tmem_ld32(ts + q * 32, s[q]);
@@ -857,7 +927,8 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                     // positions of the tile's first and last query
                     const int pos_a = item().pos0 + half * p.tokens;
                     const int pos_z = item().pos0 + min((half + 1) * p.tokens, item().tokens) - 1;
-                    if (tok0 + kTile - 1 > pos_a || (p.window && tok0 <= pos_z - p.window && tok0 + kTile > p.sinks)) {
+                    if constexpr (L::kMaskPass) {
+                    } else if (tok0 + kTile - 1 > pos_a || (p.window && tok0 <= pos_z - p.window && tok0 + kTile > p.sinks)) {
                         const int end = pos + 1 - tok0;
                         const int first = p.window ? end - p.window : 0;
                         const int sink = p.sinks - tok0;
@@ -893,7 +964,7 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                             // O of the earlier tiles is complete: scale it
                             if (!wait(&bar.o_full[g], o_phase ^ 1)) break;
                             tc_fence_after();
-#pragma unroll
+#pragma unroll (kQ4 ? 1 : 4)
                             for (int d = 0; d < D; d += 32) {
                                 uint32_t o[32];
                                 tmem_ld32(to + d, o);
@@ -969,7 +1040,7 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                     const int prow = piece * p.piece_rows + half * kTile + row;
                     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
                     if (whole) fa *= inv, fb *= inv;
-#pragma unroll
+#pragma unroll (kQ4 ? 1 : 4)
                     for (int d = 0; d < D; d += 32) {
                         uint32_t o[32];
                         tmem_ld32(to + d, o);
