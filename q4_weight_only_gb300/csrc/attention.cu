@@ -206,8 +206,13 @@ struct Layout {
     static constexpr int kQTiles = D == 128 ? 2 : 4;       // Q tiles held
     static constexpr int kQ = 0;
     static constexpr int kRing = kQTiles * kTileBytes;
-    // 4 bits at D = 128: masks in a pass over S of their own
+    // 4 bits: the unpacking warps' code and the softmax's keep each other
+    // waiting for instructions, so what can be is rolled.  At D = 128 masks are
+    // a pass over S of their own (windowed prompts 300 -> 283 us; D = 64: 193 ->
+    // 196), and only the unpacking, which bounds it, is straight-line code
+    // (rolled: a prompt of 8192 1556 -> 1640; D = 64: 193 against 196).
     static constexpr bool kMaskPass = kQ4 && D == 128;
+    static constexpr int kColumnsAtOnce = kQ4 ? 1 : 4;  // 32 columns of O
     // 4 bits: a ring of tiles' codes and scales
     static constexpr int kCodes = kRing + kStages * kTileBytes;
     static constexpr int kCodeRow = D / 2, kScaleRow = D / 16, kCodeBytes = kTile * (kCodeRow + kScaleRow);
@@ -440,6 +445,7 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
             const int row = (warp - 12) * 32 + lane;
             const uint32_t bias = p.cache.bias, codes = smem_u32(smem + L::kCodes), tiles = smem_u32(ring) + row * 128;
             const int turn = D == 128 ? row >> 1 & 3 : row >> 2 & 1;  // the swizzle of a row of codes
+            constexpr int kBlocksAtOnce = D == 128 ? 4 : 1;  // of a token
             uint32_t from = 0, from_phase = 0, slot = 0, phase = 1;
             bool ok = true;
             for (; ok && next_item(); done_item()) {
@@ -448,55 +454,20 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                                                      mbar_wait(&bar.empty[slot], phase, abort_flag, p.err));
                     if (!ok) break;
                     const uint32_t src = codes + from * L::kCodeBytes;
-                    if constexpr (D == 128) {
-                    uint32_t d[2];
-                    if (D == 128) {
-                        const uint2 x = lds64(src + kTile * L::kCodeRow + row * 8);
-                        d[0] = x.x, d[1] = x.y;
-                    } else {
-                        d[0] = d[1] = lds32(src + kTile * L::kCodeRow + row * 4);
-                    }
-                    uint4 x[D / 32];  // all before the first store, which no load passes
-#pragma unroll
-                    for (int j = 0; j < D / 32; ++j) x[j] = lds128(src + row * L::kCodeRow + (j ^ turn) * 16);
-                    const uint32_t dst = tiles + slot * L::kTileBytes;
-#pragma unroll
-                    for (int j = 0; j < D / 32; ++j) {
-                        const __half2 e = as_half2(d[j / 2]);
-                        const __half2 scale = j & 1 ? __high2half2(e) : __low2half2(e);
-                        const uint32_t words[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            // eight bytes: elements 8h .. 8h + 7 of the block and 16 further
-                            uint32_t lo[4], hi[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t w = __byte_perm(words[2 * h + i / 2], 0, i & 1 ? 0x4342 : 0x4140);
-                                lo[i] = times(low_codes(w, bias), scale), hi[i] = times(high_codes(w, bias), scale);
-                            }
-                            const uint32_t at = dst + (j >> 1) * L::kBlock;
-                            const int first = (j & 1) * 4 + h;
-                            sts128(at + ((first ^ (row & 7)) * 16), lo);
-                            sts128(at + (((first + 2) ^ (row & 7)) * 16), hi);
-                        }
-                    }
-                    } else {
                     uint2 d;
                     if (D == 128)
                         d = lds64(src + kTile * L::kCodeRow + row * 8);
                     else
                         d.x = d.y = lds32(src + kTile * L::kCodeRow + row * 4);
-                    const uint32_t dst = tiles + slot * L::kTileBytes, words = src + row * L::kCodeRow;
-                    // (rolled: straight-line code of all blocks makes the
-                    // softmax warps wait for their instructions)
-                    uint4 next = lds128(words + turn * 16);
-#pragma unroll 1
+                    const uint32_t dst = tiles + slot * L::kTileBytes, blocks = src + row * L::kCodeRow;
+                    uint4 next = lds128(blocks + turn * 16);
+#pragma unroll kBlocksAtOnce
                     for (int j = 0; j < D / 32; ++j) {
                         const uint4 x = next;
                         // (no load passes the stores below)
-                        if (j + 1 < D / 32) next = lds128(words + ((j + 1) ^ turn) * 16);
+                        if (j + 1 < D / 32) next = lds128(blocks + ((j + 1) ^ turn) * 16);
                         const __half2 scale = as_half2(__byte_perm(j & 2 ? d.y : d.x, 0, j & 1 ? 0x3232 : 0x1010));
-                        const uint32_t at = dst + (j >> 1) * L::kBlock, first = (j & 1) * 4;
+                        const uint32_t at = dst + (j >> 1) * L::kBlock, chunk = (j & 1) * 4;
                         const uint32_t words[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
@@ -507,10 +478,9 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                                 const uint32_t w = __byte_perm(words[2 * h + i / 2], 0, i & 1 ? 0x4342 : 0x4140);
                                 lo[i] = times(low_codes(w, bias), scale), hi[i] = times(high_codes(w, bias), scale);
                             }
-                            sts128(at + (((first + h) ^ (row & 7)) * 16), lo);
-                            sts128(at + (((first + h + 2) ^ (row & 7)) * 16), hi);
+                            sts128(at + (((chunk + h) ^ (row & 7)) * 16), lo);
+                            sts128(at + (((chunk + h + 2) ^ (row & 7)) * 16), hi);
                         }
-                    }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -893,20 +863,27 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                 s_phase ^= 1;
                 tc_fence_after();
                 if (busy) {
-                    // masks in a pass of their own, a quarter of S at a time
-                    if constexpr (L::kMaskPass) {
-                        const int tok0 = item().key_tile(t) * kTile;
+                    // whether some query of the tile does not see some key,
+                    // and which of keys 32 q to 32 q + 31 this row sees
+                    auto cut = [&](int tok0) {
+                        // positions of the tile's first and last query
                         const int pos_a = item().pos0 + half * p.tokens;
                         const int pos_z = item().pos0 + min((half + 1) * p.tokens, item().tokens) - 1;
-                        if (tok0 + kTile - 1 > pos_a ||
-                            (p.window && tok0 <= pos_z - p.window && tok0 + kTile > p.sinks)) {
-                            const int end = pos + 1 - tok0;
-                            const int first = p.window ? end - p.window : 0;
-                            const int sink = p.sinks - tok0;
+                        return tok0 + kTile - 1 > pos_a ||
+                               (p.window && tok0 <= pos_z - p.window && tok0 + kTile > p.sinks);
+                    };
+                    auto seen_of = [&](int tok0, int q) {
+                        const int end = pos + 1 - tok0;
+                        const int first = p.window ? end - p.window : 0;
+                        const int sink = p.sinks - tok0;
+                        return below(end - q * 32) & (~below(first - q * 32) | below(sink - q * 32));
+                    };
+                    if constexpr (L::kMaskPass) {
+                        const int tok0 = item().key_tile(t) * kTile;
+                        if (cut(tok0)) {
 #pragma unroll 1
                             for (int q = 0; q < 4; ++q) {
-                                const uint32_t seen =
-                                    below(end - q * 32) & (~below(first - q * 32) | below(sink - q * 32));
+                                const uint32_t seen = seen_of(tok0, q);
                                 if (__all_sync(0xffffffffu, seen == ~0u)) continue;
                                 uint32_t v[32];
                                 tmem_ld32(ts + q * 32, v);
@@ -923,21 +900,16 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
 #pragma unroll
                     for (int q = 0; q < 4; ++q) tmem_ld32(ts + q * 32, s[q]);
                     tmem_wait_ld();
-                    const int tok0 = item().key_tile(t) * kTile;
-                    // positions of the tile's first and last query
-                    const int pos_a = item().pos0 + half * p.tokens;
-                    const int pos_z = item().pos0 + min((half + 1) * p.tokens, item().tokens) - 1;
-                    if constexpr (L::kMaskPass) {
-                    } else if (tok0 + kTile - 1 > pos_a || (p.window && tok0 <= pos_z - p.window && tok0 + kTile > p.sinks)) {
-                        const int end = pos + 1 - tok0;
-                        const int first = p.window ? end - p.window : 0;
-                        const int sink = p.sinks - tok0;
+                    if constexpr (!L::kMaskPass) {
+                        const int tok0 = item().key_tile(t) * kTile;
+                        if (cut(tok0)) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint32_t seen = below(end - q * 32) & (~below(first - q * 32) | below(sink - q * 32));
+                            for (int q = 0; q < 4; ++q) {
+                                const uint32_t seen = seen_of(tok0, q);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!(seen >> e & 1)) s[q][e] = 0xFF800000u;
+                                for (int e = 0; e < 32; ++e)
+                                    if (!(seen >> e & 1)) s[q][e] = 0xFF800000u;
+                            }
                         }
                     }
                     // four chains each for the maximum and the sum: one
@@ -964,7 +936,7 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                             // O of the earlier tiles is complete: scale it
                             if (!wait(&bar.o_full[g], o_phase ^ 1)) break;
                             tc_fence_after();
-#pragma unroll (kQ4 ? 1 : 4)
+#pragma unroll L::kColumnsAtOnce
                             for (int d = 0; d < D; d += 32) {
                                 uint32_t o[32];
                                 tmem_ld32(to + d, o);
@@ -1040,7 +1012,7 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                     const int prow = piece * p.piece_rows + half * kTile + row;
                     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
                     if (whole) fa *= inv, fb *= inv;
-#pragma unroll (kQ4 ? 1 : 4)
+#pragma unroll L::kColumnsAtOnce
                     for (int d = 0; d < D; d += 32) {
                         uint32_t o[32];
                         tmem_ld32(to + d, o);
