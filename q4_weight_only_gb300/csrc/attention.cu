@@ -62,17 +62,24 @@
 // into the ring that the MMAs read, and the softmax warps turn their rows of Q
 // to binary16.  The copies are a quarter of the bytes; what bounds a tile is
 // the unpacking and what it costs the others:
-// * 8192 tokens after 8192 others take 1.61 ms, 1.28 PFLOP/s.  Without the
-//   unpacking's arithmetic it is 1.55, without its reads and stores 1.43: its
-//   warps take 2240 of the 3700 cycles of a pair of tiles, and the stores of
-//   64 KB compete with the MMAs' reads for shared memory.  Three unpacking
-//   warps in the copy warps' places took 3.28 ms; four that copied for
-//   themselves 1.94.
-// * The windowed prompts at D = 64 take 200 us.
-// * 5 drafted tokens of 16 sequences under a window of 4096: 70 us, 3600 cycles
-//   a key tile, of which the unpacking is 1800 (bfloat16: 60 us).
-// * Rings of 3 unpacked tiles and 6 of codes instead of 4 and 3 (D = 64: 6 and
-//   12 instead of 8 and 6): prompts 3 % slower, the others level.
+// * 8192 tokens after 8192 others take 1.56 ms, 1.32 PFLOP/s; 1.43 with the
+//   unpacking left out, 1.36 without the copies too (timing only).  Its warps
+//   work 2240 of a pair of tiles' 3600 cycles, their stores of 64 KB compete
+//   with the MMAs' reads for shared memory, and their code with the softmax's
+//   for the instruction caches: waits for instructions are 2.1 an issue under a
+//   window, where they are 0.7 with the bfloat16 cache.  Three unpacking warps
+//   in the copy warps' places took 3.28 ms; four that copied for themselves
+//   1.94.
+// * The windowed prompts at D = 64 take 193 us, of which 6 are the launch of
+//   the kernel for few rows; 182 without unpacking and copies.  Turning a Q to
+//   binary16, and its scores waiting for that, take 5000 cycles an item.
+// * 5 drafted tokens of 16 sequences under a window of 4096: 68 us (bfloat16:
+//   60), 46 without unpacking and copies.
+// * Not faster: rings of 3 unpacked tiles and 6 of codes instead of 4 and 3 (D
+//   = 64: 6 and 12 instead of 8 and 6; prompts 3 % slower, the others level); Q
+//   turned by the unpacking warps (windowed prompts 206, a prompt of 8192 1.62
+//   ms) or before the last item's output is written (197, 1.57); more registers
+//   for the copy warps (56 + 40 + 2 * 208; level).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -625,12 +632,11 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
         } else if (warp == 3) {
             // ------------------------------------------------- items
             Publisher w = publisher();
-            bool more = publish(w);
             if constexpr (kQ4) {
                 // and copies each item's Q, with the next item handed out:
                 // the copying warps have no registers for it
                 uint32_t q = 0;
-                bool ok = true;
+                bool ok = true, more = publish(w);
                 for (uint32_t i = 0; ok && bar.item[i % kItems].t0 < bar.item[i % kItems].t1; ++i) {
                     if (more) more = publish(w);
                     const Item &o = bar.item[i % kItems];
@@ -641,7 +647,7 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                 }
                 if (lane == 0) bar.q_fills = q;
             } else {
-                while (more) more = publish(w);
+                while (publish(w)) {}
             }
             publish_end(w);
         } else if (warp == 1) {
@@ -720,15 +726,16 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                 uint32_t slot_k = fills % kStages, slot_v = (fills + 1) % kStages;
                 if (!full(fills) || (!kQ4 && !q_full(q + 1))) break;
                 tc_fence_after();
-                if (elect_one()) scores(0, q, slot_k, n == 1);
                 if constexpr (kQ4) {
                     // group B turns its Q to binary16 when it is done with the
                     // last item: A does not wait for that
+                    if (elect_one()) scores(0, q, slot_k, n == 1);
                     __syncwarp();
                     if (!q_full(q + 1)) break;
                     tc_fence_after();
                 }
                 if (elect_one()) {
+                    if (!kQ4) scores(0, q, slot_k, n == 1);
                     scores(1, q + 1, slot_k, n == 1);
                     mma_commit(&bar.empty[slot_k]);
                 }
@@ -1007,7 +1014,8 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                 const bool both = !wide && item().t1 - item().t0 > 1;
                 if (busy) {
                     const bool whole = item().t0 == 0 && item().t1 == item().n;
-                    const int64_t at = ((int64_t)item().row0 + i) * p.q_heads + item().head * p.group + (row - my_token * p.group);
+                    const int my_head = row - my_token * p.group;
+                    const int64_t at = ((int64_t)item().row0 + i) * p.q_heads + item().head * p.group + my_head;
                     const int piece = blockIdx.x * 2 + (item().t0 == 0 ? 1 : 0);
                     const int prow = piece * p.piece_rows + half * kTile + row;
                     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
