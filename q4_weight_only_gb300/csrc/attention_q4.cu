@@ -27,10 +27,10 @@
 // with the keys and values as the wide one, which warps unpack straight from
 // the codes into their registers.  Nothing unpacked is written anywhere, and
 // a tcgen05 operand in shared memory is not worth it for codes that so few rows
-// use: 64 sequences' next tokens take twice as long there (351 and 700 us).
+// use: 64 sequences' next tokens take twice as long there (353 and 700 us).
 // Longer sequences fill tcgen05's tiles of 128 rows and are attention.cu's
 // 4-bit variant: 16 sequences' 5 drafted tokens by 5 heads, 25 rows each, take
-// 70 us there, and 85 as two items of 16 here.
+// 68 us there, and 85 as two items of 16 here.
 //
 // Layout of work: an item is 8 or 16 rows of one sequence and key head, its
 // cost the key tiles it sees; CTAs, one an SM, take equal shares of all cost,
@@ -38,8 +38,8 @@
 // order.
 //
 // Bounds and measurements (40 query heads on 8 key heads of 128, device time):
-// * 64 sequences' next tokens, 4 to 32 thousand tokens each, 1.29 GB: 351 us,
-//   3.7 TB/s, 0.55 of a copy's rate, where the bfloat16 cache takes 663.  Copies
+// * 64 sequences' next tokens, 4 to 32 thousand tokens each, 1.29 GB: 353 us,
+//   3.6 TB/s, 0.55 of a copy's rate, where the bfloat16 cache takes 662.  Copies
 //   alone take 241 us and the arithmetic alone 258: 400 warp instructions for
 //   16 keys and values fill 60 % of the issue slots (logic and integers 49 %
 //   of their pipe, multiply-adds 36 %, tensor 20 %, HBM 50 %).
