@@ -62,7 +62,7 @@
 // into the ring that the MMAs read, and the softmax warps turn their rows of Q
 // to binary16.  The copies are a quarter of the bytes; what bounds a tile is
 // the unpacking and what it costs the others:
-// * 8192 tokens after 8192 others take 1.56 ms, 1.32 PFLOP/s; 1.43 with the
+// * 8192 tokens after 8192 others take 1.55 ms, 1.33 PFLOP/s; 1.43 with the
 //   unpacking left out, 1.36 without the copies too (timing only).  Its warps
 //   work 2240 of a pair of tiles' 3600 cycles, their stores of 64 KB compete
 //   with the MMAs' reads for shared memory, and their code with the softmax's
@@ -70,16 +70,16 @@
 //   window, where they are 0.7 with the bfloat16 cache.  Three unpacking warps
 //   in the copy warps' places took 3.28 ms; four that copied for themselves
 //   1.94.
-// * The windowed prompts at D = 64 take 193 us, of which 6 are the launch of
-//   the kernel for few rows; 182 without unpacking and copies.  Turning a Q to
-//   binary16, and its scores waiting for that, take 5000 cycles an item.
-// * 5 drafted tokens of 16 sequences under a window of 4096: 68 us (bfloat16:
-//   60), 46 without unpacking and copies.
+// * The windowed prompts at D = 64 take 187 us; 176 without unpacking and
+//   copies.  Turning a Q to binary16, and its scores waiting for that, take 5000
+//   cycles an item.
+// * 5 drafted tokens of 16 sequences under a window of 4096: 61 us (bfloat16:
+//   60), 39 without unpacking and copies.
 // * Not faster: rings of 3 unpacked tiles and 6 of codes instead of 4 and 3 (D
 //   = 64: 6 and 12 instead of 8 and 6; prompts 3 % slower, the others level); Q
-//   turned by the unpacking warps (windowed prompts 206, a prompt of 8192 1.62
-//   ms) or before the last item's output is written (197, 1.57); more registers
-//   for the copy warps (56 + 40 + 2 * 208; level).
+//   turned by the unpacking warps (windowed prompts 193 -> 206 us, a prompt of
+//   8192 1.56 -> 1.62 ms) or before the last item's output is written (197,
+//   1.57); more registers for the copy warps (56 + 40 + 2 * 208; level).
 #include <cuda.h>
 #include <cuda_bf16.h>
 

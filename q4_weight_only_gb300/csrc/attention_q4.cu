@@ -30,7 +30,7 @@
 // use: 64 sequences' next tokens take twice as long there (353 and 700 us).
 // Longer sequences fill tcgen05's tiles of 128 rows and are attention.cu's
 // 4-bit variant: 16 sequences' 5 drafted tokens by 5 heads, 25 rows each, take
-// 68 us there, and 85 as two items of 16 here.
+// 61 us there, and 85 as two items of 16 here.
 //
 // Layout of work: an item is 8 or 16 rows of one sequence and key head, its
 // cost the key tiles it sees; CTAs, one an SM, take equal shares of all cost,
@@ -899,13 +899,20 @@ cudaError_t launch_attention_q4(const AttentionArgs &a, const KvQ4View &c, void 
                                 unsigned int *err) {
     const int sms = current_sms(), group = a.q_heads / c.kv_heads;
     if (sms < 1) return cudaErrorInvalidDevice;
+    const bool both = (int64_t)group * a.max_q_len > kMostRows;
+    // Where all but one sequence can have max_q_len tokens and the last one more
+    // than this kernel's, none has few unless there are rows of no sequence (and
+    // then it is the other kernel's too).  A kernel that finds nothing to do
+    // takes 6 us of a call.
+    const int64_t least = a.rows - (c.sequences - 1ll) * a.max_q_len;
+    const bool all_long = both && least * group > item_rows(group, a.max_q_len);
     cudaError_t e = cudaSuccess;
-    if (group <= kMostRows)
+    if (group <= kMostRows && !all_long)
         e = (c.head_dim == 128 ? launch_d<128> : launch_d<64>)(a, c, workspace, sms, s, err);
-    if (e != cudaSuccess || (int64_t)group * a.max_q_len <= kMostRows) return e;
+    if (e != cudaSuccess || !both) return e;
     const int rows = item_rows(group, a.max_q_len);
     uint8_t *rest = static_cast<uint8_t *>(workspace) + WorkspaceLayout(sms, c.head_dim, rows).bytes;
-    return launch_attention_q4_wide(a, c, rows + 1, rest, s, err);
+    return launch_attention_q4_wide(a, c, all_long ? 1 : rows + 1, rest, s, err);
 }
 
 }  // namespace q4_0

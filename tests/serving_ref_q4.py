@@ -66,6 +66,8 @@ class Batch(ref.Batch):
         return tuple(back)
 
     def cuda(self):
-        keep = lambda t: t.transpose(1, 2).contiguous().cuda().transpose(1, 2) if not t.is_contiguous() else t.cuda()  # noqa: E731
+        def keep(t):
+            return t.cuda() if t.is_contiguous() else t.transpose(1, 2).contiguous().cuda().transpose(1, 2)
+
         self.dev = (tuple(keep(t) for t in self.cache), self.table.cuda(), self.q_start.cuda(), self.kv_len.cuda())
         return self.dev

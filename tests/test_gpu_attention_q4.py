@@ -215,6 +215,30 @@ def test_items_of_one_and_two_tiles_in_turn(dim, window):
     check(b, *run(b, 10, window=window, sinks=2 if window else 0), window, 2 if window else 0)
 
 
+@pytest.mark.parametrize("q_heads,kv_heads", [(10, 2), (40, 2)])
+@pytest.mark.parametrize("max_q_len", [2, 9, 30, 5000])
+def test_a_bound_above_the_batch(q_heads, kv_heads, max_q_len):
+    """max_q_len is a bound: single tokens under one that lets both kernels
+    run, or that is above the number of rows."""
+    b = Batch([1] * 30, [3 + 37 * i for i in range(30)], 16, kv_heads, 64, seed=19).write_tokens()
+    q = torch.randn(b.rows, q_heads, b.dim, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    q4, lse = lib(), torch.full((b.rows, q_heads), 7.0, device="cuda")
+    out = q4.attention_q4(q, *b.cuda(), max_q_len=max_q_len, out_dtype=torch.float32, lse=lse)
+    assert q4.device_error() == q4.OK
+    check(b, q, out, lse)
+
+
+@pytest.mark.parametrize("new,extra", [([5, 5, 5], 0), ([1, 5, 5], 4), ([5, 0, 2], 8), ([40, 40], 0), ([40, 1], 39),
+                                       ([40, 25], 0), ([40, 3], 30), ([30], 0), ([2], 40), ([40, 4], 0), ([5, 3, 5], 1)])
+def test_rows_enough_for_long_sequences_alone(new, extra):
+    """Batches whose rows could all be of sequences too long for the kernel of
+    few rows: in some they are, and in some a shorter sequence leaves rows of
+    none."""
+    b = Batch(new, [300 + 77 * i + n for i, n in enumerate(new)], 16, 2, 128, seed=20, extra_rows=extra).write_tokens()
+    check(b, *run(b, 10))
+    check(b, *run(b, 10, window=60, sinks=3), window=60, sinks=3)
+
+
 def test_strided_queries():
     """Queries inside fused rows: row and head strides of their own."""
     b = Batch([1, 30], [100, 200], 16, 2, 64, seed=16).write_tokens()
@@ -323,7 +347,9 @@ def test_refusals():
     b = Batch([1], [20], 16, 2, 64, seed=22).write_tokens()
     dev = b.cuda()
     q = torch.zeros(1, 4, 64, dtype=torch.bfloat16, device="cuda")
-    good = lambda **k: q4.attention_q4(k.pop("q", q), *k.pop("dev", dev), max_q_len=k.pop("max_q_len", 1), **k)  # noqa: E731
+    def good(**k):
+        return q4.attention_q4(k.pop("q", q), *k.pop("dev", dev), max_q_len=k.pop("max_q_len", 1), **k)
+
     good()
     with pytest.raises(TypeError):
         good(q=q.float())

@@ -135,6 +135,30 @@ def test_blocks_of_equals_zeros_and_halves():
     assert q4.device_error() == q4.OK
 
 
+@pytest.mark.parametrize("size", [1.0, 3e-6, 8000.0])
+def test_elements_next_to_half_a_code(size):
+    """Every element within two units in the last place of the border of two
+    codes, where the rounding of a quotient decides."""
+    q4 = lib()
+    b = Batch([40], [40], 16, 2, 128, seed=8)
+    g = np.random.default_rng(8)
+    top = (g.uniform(1, 8, (40, 5, 4, 1)) * g.choice([-1, 1], (40, 5, 4, 1)) * size).astype(np.float32)
+    d = top * np.float32(-0.125)
+    x = ((g.integers(-8, 8, (40, 5, 4, 32)) + 0.5).astype(np.float32) * d).astype(np.float32)
+    for _ in range(2):
+        away = g.integers(-1, 2, x.shape)
+        x = np.where(away == 0, x, np.nextafter(x, np.where(away > 0, np.inf, -np.inf).astype(np.float32)))
+    x = np.clip(x, -np.abs(top), np.abs(top))
+    x[..., 7:8] = top
+    qkv = torch.from_numpy(x.reshape(40, -1).astype(np.float32)).cuda()
+    b.cuda()
+    q4.kv_append_q4(qkv, torch.zeros(64, 0, device="cuda"), *b.dev, q_heads=1)
+    _, cache = expected(b, qkv, 1, 0, False, None)
+    for t, w in zip(b.dev[0], cache):
+        assert torch.equal(t.cpu(), w)
+    assert q4.device_error() == q4.OK
+
+
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf, 65520.0, 1e30])
 def test_elements_a_block_cannot_hold(bad):
     q4 = lib()

@@ -90,7 +90,9 @@ def test_two_captured_graphs_with_workspaces_of_their_own_and_one_shared():
             dev = b.cuda()
             ws = one if shared else torch.empty(need, dtype=torch.uint8, device="cuda")
             out = torch.empty(4, 10, 128, device="cuda")
-            call = lambda: q4.attention_q4(q, *dev, max_q_len=1, out=out, out_dtype=torch.float32, workspace=ws)  # noqa: E731
+            def call():
+                q4.attention_q4(q, *dev, max_q_len=1, out=out, out_dtype=torch.float32, workspace=ws)
+
             side = torch.cuda.Stream()
             with torch.cuda.stream(side):
                 call()

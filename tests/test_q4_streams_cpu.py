@@ -24,7 +24,8 @@ def calls():
     batch = ((codes, scales, codes.clone(), scales.clone()), ints(1)[None], ints(0, 1), ints(1))
     q = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
     return {
-        "append": lambda s: serving.kv_append_q4(torch.zeros(1, 4 * 64), torch.zeros(8, 64), *batch, q_heads=2, stream=s),
+        "append": lambda s: serving.kv_append_q4(torch.zeros(1, 4 * 64), torch.zeros(8, 64), *batch, q_heads=2,
+                                                 stream=s),
         "read": lambda s: serving.kv_read_q4(*batch, rows=1, stream=s),
         "attention": lambda s: serving.attention_q4(q, *batch, max_q_len=1, stream=s),
     }

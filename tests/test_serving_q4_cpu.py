@@ -92,7 +92,8 @@ def test_attention_arguments(lib):
                    dict(lse=GOOD + 2)):
         assert attention(lib, **change) == -1, change
     # scales of a token are read at once
-    for c in (dict(k_scale=GOOD + 2), dict(v_scale=GOOD + 2), dict(k_scale_token_stride=3), dict(v_scale_page_stride=65)):
+    for c in (dict(k_scale=GOOD + 2), dict(v_scale=GOOD + 2), dict(k_scale_token_stride=3),
+              dict(v_scale_page_stride=65)):
         assert attention(lib, cache(**c)) == -1, c
         assert append(lib, cache(**c), rows=0) == 0
     for c in (dict(head_dim=96), dict(page_size=12), dict(head_dim=256)):
