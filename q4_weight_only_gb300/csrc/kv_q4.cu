@@ -16,9 +16,10 @@
 // d (code - 8), exactly in fp32.
 //
 // Bounds and measurements (40 query heads on 8 key heads of 128, device time):
-// * append: 8191 fp32 rows, 330 MB read and written, take 64 us (a copy's rate:
-//   50).  Every byte moves once; the issue slots are two thirds full, of the
-//   blocks' maxima, quotients and rotations.  A reciprocal and a rounding
+// * append: 8191 fp32 rows, 330 MB read and written, take 60 us (a copy's rate:
+//   50).  Every byte moves once; a row is a chain of its copy, its place, the
+//   rotation and the blocks, of which six CTAs an SM hide one another's waits
+//   (five, without spills: 64 us; seven: 71).  A reciprocal and a rounding
 //   constant make a code in four instructions; a floor and its distance to a
 //   half in each code took 69 us, a division in each 72.
 // * read: the writes, at 0.94 of a copy's rate.  82 thousand rows to bfloat16,
@@ -92,36 +93,43 @@ __device__ __forceinline__ uint32_t codes_of(const float (&w)[8], float d) {
     return codes;
 }
 
-// The largest element of a block so far.
-struct Largest {
-    float size, value;
-    int at;
-    __device__ __forceinline__ void add(float w, int i) {
-        const float a = fabsf(w);
-        const float s = a <= kLargest ? a : INFINITY;  // NaN too
-        if (s > size) size = s, value = w, at = i;
-    }
-};
+// The largest of three, NaN if one is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 
 // A quad of lanes (`mask`) quantises a block, lane j of it elements 4j .. 4j +
 // 3 (u) and 16 + 4j .. (v), to bytes 4j .. 4j + 3 of `codes`.
 __device__ __forceinline__ void quantise_quad(float4 u, float4 v, int j, uint32_t mask, uint8_t *codes,
                                               uint16_t *scale) {
-    Largest m{-1.f, 0.f, 0};
-    m.add(u.x, 4 * j), m.add(u.y, 4 * j + 1), m.add(u.z, 4 * j + 2), m.add(u.w, 4 * j + 3);
-    m.add(v.x, 16 + 4 * j), m.add(v.y, 17 + 4 * j), m.add(v.z, 18 + 4 * j), m.add(v.w, 19 + 4 * j);
+    // the largest element, and the largest of their opposites
+    float up = max3_nan(max3_nan(max3_nan(u.x, u.y, u.z), u.w, v.x), v.y, max3_nan(v.z, v.z, v.w));
+    float down = max3_nan(max3_nan(max3_nan(-u.x, -u.y, -u.z), -u.w, -v.x), -v.y, max3_nan(-v.z, -v.z, -v.w));
 #pragma unroll
     for (int d = 1; d <= 2; d <<= 1) {
-        const float size = __shfl_xor_sync(mask, m.size, d), value = __shfl_xor_sync(mask, m.value, d);
-        const int at = __shfl_xor_sync(mask, m.at, d);
-        if (size > m.size || (size == m.size && at < m.at)) m.size = size, m.value = value, m.at = at;
+        const float a = __shfl_xor_sync(mask, up, d), z = __shfl_xor_sync(mask, down, d);
+        up = max3_nan(up, a, a), down = max3_nan(down, z, z);
     }
     uint32_t w = 0x88888888u;
     uint16_t s = 0;
-    if (m.size == INFINITY) {
+    if (!(up <= kLargest && down <= kLargest)) {
         s = 0x7FFF;  // the block reads back as NaN
-    } else if (m.size > 0.f) {
-        const float d = __fmul_rn(m.value, -0.125f);
+    } else if (up > 0.f || down > 0.f) {
+        float value = up > down ? up : -down;
+        if (up == down) {
+            // elements of both signs: the first of them
+            const float e[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+            int first = 64;  // twice its index, and one more if it is negative
+#pragma unroll
+            for (int i = 7; i >= 0; --i)
+                if (fabsf(e[i]) == up) first = 2 * (4 * j + (i & 3) + (i & 4) * 4) + (e[i] < 0.f);
+#pragma unroll
+            for (int d = 1; d <= 2; d <<= 1) first = min(first, __shfl_xor_sync(mask, first, d));
+            value = first & 1 ? -up : up;
+        }
+        const float d = __fmul_rn(value, -0.125f);
         s = __half_as_ushort(__float2half_rn(d));
         const float e[8] = {u.x, v.x, u.y, v.y, u.z, v.z, u.w, v.w};
         w = codes_of(e, d);
@@ -154,7 +162,7 @@ __device__ __forceinline__ Place place_of(const KvQ4View &c, int row, int ended)
 // (in the piece itself for fp32, beside it for bfloat16), and four lanes then
 // quantise a block.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 5)
+__global__ void __launch_bounds__(kThreads, 6)
     kv_append_q4_kernel(const KvAppendArgs a, const KvQ4View c, int heads, Divisor per_head, Divisor blocks,
                         unsigned int *err) {
     extern __shared__ __align__(128) uint8_t smem[];
