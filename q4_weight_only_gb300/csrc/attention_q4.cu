@@ -169,7 +169,11 @@ constexpr int kThreads = 512, kCopyWarps = 8, kComputeWarps = 8;
 constexpr int kCopyRegs = 88, kComputeRegs = 168;
 constexpr int kTurns = kComputeWarps / (kTile / kStep);  // tiles computed at once
 constexpr int kCopyTurns = kCopyWarps / 2;               // and copied at once
-constexpr int kItems = 4;  // items handed out ahead
+// Items handed out ahead.  Warp 0 looks for its next tile, kCopyTurns on and so
+// up to as many items on, before it copies the one it has: the item that the
+// one it then hands out takes the place of must not need that copy.
+constexpr int kItems = 8;
+static_assert(kItems >= kCopyTurns + 2, "");
 
 template <int D, int NT>
 struct Layout {

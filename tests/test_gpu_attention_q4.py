@@ -206,6 +206,24 @@ def test_long_context_and_many_sequences():
     check(b, *run(b, 4))
 
 
+@pytest.mark.parametrize("q_heads,kv_heads,dim", [(40, 8, 128), (16, 8, 64), (32, 2, 128), (80, 8, 64)])
+@pytest.mark.parametrize("longest,window", [(128, 0), (300, 0), (300, 20), (5, 0)])
+def test_many_short_sequences(q_heads, kv_heads, dim, longest, window):
+    """Many items of one or two key tiles in every share."""
+    n = 140 * 8 // kv_heads
+    b = Batch([1] * n, [1 + (i * 37) % longest for i in range(n)], 16, kv_heads, dim, seed=21).write_tokens()
+    q, out, lse = run(b, q_heads, window=window)
+    check(b, q, out, lse, window)
+
+
+@pytest.mark.parametrize("new,longest", [(7, 120), (20, 130), (33, 200)])
+def test_many_short_drafts(new, longest):
+    b = Batch([new] * 150, [new + (i * 29) % longest for i in range(150)], 16, 8, 128, seed=22).write_tokens()
+    check(b, *run(b, 40))
+    b = Batch([new, 1] * 90, [new + (i * 29) % longest for i in range(180)], 16, 8, 128, seed=23).write_tokens()
+    check(b, *run(b, 40))
+
+
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("window", [0, 90])
 def test_items_of_one_and_two_tiles_in_turn(dim, window):
