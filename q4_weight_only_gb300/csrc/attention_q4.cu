@@ -73,6 +73,17 @@ constexpr int kStep = 32;     // keys of a warp's part of one
 // A nibble that is left where it is, in the low bits of a binary16, is a
 // number below its normal range: code / kCodeUnit, exactly.
 constexpr float kCodeUnit = 16777216.f;
+// What the codes' 8 too many come to in a block, -8 sum q, is held as two
+// binary16 parts in a unit of its own: at most 2^15, and what the two leave out
+// is 2^-23 of it.  In the unit of the codes the second part would mostly be
+// below binary16's normal range, where 2^-25 is lost of it whatever the block
+// holds: beside an element a thousand times the rest, 2^-12 of the other
+// blocks' sum |q k|.  Undoing it costs 8 multiplications a tile of 8 rows in
+// 400 instructions (32 single tokens of 16384: 151.6 -> 153.0 us; sums that
+// start from -8 sum q in fp32 instead of zeros are as good and need no such
+// product, but four registers a block: 154.6, and 69 -> 90 with 16 heads of 128
+// on one).
+constexpr float kLessUnit = 65536.f;
 
 struct Params {
     CacheQ4 cache;
@@ -500,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                sum *= -8.f / kCodeUnit;
+                sum *= -8.f * kLessUnit / kCodeUnit;
                 const __half top_part = __float2half_rn(sum), rest = __float2half_rn(sum - __half2float(top_part));
                 const uint32_t at = j & 1 ? 16 : 0;
                 if (at == 0) less_hi[j / 2] = less_lo[j / 2] = 0;
@@ -546,6 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int n = 0; n < NT; ++n) {
                     sc[h][n][0] = sc[h][n][1] = sc[h][n][2] = sc[h][n][3] = 0.f;
                     mma16816(sc[h][n], e0, e1, 0u, 0u, less[n], 0u);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) sc[h][n][x] *= 1.f / kLessUnit;
                 }
 #pragma unroll
                 for (int j = 0; j < NB; ++j) {
