@@ -535,7 +535,8 @@ int q4_0_kv_read_q4(void *k_out, void *v_out, int out_type, int64_t rows, const 
  * rows * q_heads / kv_heads <= 2^30 (else UNSUPPORTED).
  * Accuracy: scores, softmax statistics and sums in fp32; operands of the
  * products are binary16: a row of q scaled by a power of two, elements of the
- * cache and exponentials rounded once.
+ * cache and exponentials rounded once (exponentials to 2^-11, and no finer than
+ * 2^-32 of the row's largest).
  * Workspace: q4_0_attention_q4_workspace_bytes(...) bytes on the current
  * device, 256-byte aligned, in use until the work on `stream` completes.
  * Returns as q4_0_attention.

@@ -114,8 +114,9 @@ constexpr float kGrow = 8.f;    // log2 of the growth of a row's maximum that mo
 // apart at least: the next power of two in the place of c gives the same
 // p, 1 or nothing, without a rounding.
 constexpr float kHuge = 1 << 30;
-// binary16 holds less: at 2^26 the factor is at most 2^4, so p at most 2^12;
-// a score's own rounding to fp32 is up to 4 in the exponent there.
+// binary16 holds less: below 2^26 the reference is off by at most 4, twice
+// (rounded, and lifted), so p at most 2^15 where it is set, as by growth; a
+// score's own rounding to fp32 is up to 4 in the exponent there.
 constexpr float kHugeQ4 = 1 << 26;
 
 struct Params {
@@ -930,11 +931,15 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                         for (int q = 0; q < 4; ++q)
                             top4[q] = max3(top4[q], __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
                     const float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
+                    // 4 bits: references are kLift below the maximum, p that
+                    // much larger
+                    constexpr float lift = kQ4 ? kLift : 0.f;
                     // (nothing is above an infinite reference)
-                    if (__any_sync(0xffffffffu, fmaf(top, c_row, -mc) > kGrow)) {
+                    if (__any_sync(0xffffffffu, fmaf(top, c_row, -mc) > kGrow + lift)) {
                         const float c = c_of(p.scale_log2);
                         const float c_top = fabsf(top * c) > (kQ4 ? kHugeQ4 : kHuge) ? c_of(p.scale_pow2) : c;
-                        const float mc_new = __fmul_rn(top, c_top);
+                        float mc_new = __fmul_rn(top, c_top);
+                        if (kQ4) mc_new = __fsub_rn(mc_new, lift);
                         const bool above = mc_new > mc;
                         const float f = mc == -INFINITY ? 0.f : above ? ex2(mc - mc_new) : 1.f;
                         l *= f;

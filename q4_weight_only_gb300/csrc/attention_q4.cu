@@ -8,7 +8,7 @@
 // reference follows the running maximum only when a row's maximum grew by more
 // than 2^8 in p: the result does not depend on it, and most steps then skip the
 // correction of O.  The difference s - m is made before the product with c: a
-// certain key has p = 1 exactly.
+// certain key has p = 1 exactly.  p, l and O are held times 2^7 (kLift).
 //
 // Operands of the tensor cores are binary16:
 // * a key's codes, exactly, as the numbers below binary16's normal range that
@@ -19,8 +19,8 @@
 // * a query row times a power of two that brings its largest element to
 //   [2^14, 2^15), undone in c: exact for every element within 2^29 of the
 //   largest, off by at most 2^-39 of that below;
-// * p, at most 2^8, rounded (2^-11, and 2^-25 where it is below 2^-14); l sums p
-//   before the rounding.
+// * p, at most 2^8, times 2^7, rounded (2^-11 of p, and 2^-32 where p is below
+//   2^-21); l sums it before the rounding.
 //
 // Two kernels.  Sequences of at most 16 rows, (token, head of the group) pairs,
 // are this file's: their few rows are the narrow operand of m16n8k16 products
@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float e[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        e[x] = ex2((sc[h][n][x] - base[x & 1]) * cs[n][x & 1]);
+                        e[x] = ex2(fmaf(sc[h][n][x] - base[x & 1], cs[n][x & 1], kLift));
                         l[n][x & 1] += e[x];
                     }
                     pf[h][n][0] = transpose8x8(as_bits(__floats2half2_rn(e[0], e[1])));
@@ -764,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!whole)
                 p.part_mlc[piece + ctid] = mlc;
             else if (p.lse)
-                p.lse[place(ctid)] = (mlc.x * mlc.z + __log2f(mlc.y)) * kLn2;
+                p.lse[place(ctid)] = (mlc.x * mlc.z + (__log2f(mlc.y) - kLift)) * kLn2;
         }
     }
     }
@@ -841,7 +841,7 @@ __global__ void __launch_bounds__(256) attention_q4_join_kernel(const __grid_con
         for (int w = 0; w < 8; ++w) v += sums[w][d];
         store_y(static_cast<float *>(p.out), at * D + d, v * inv, p.out_bf16);
     }
-    if (p.lse && d == 0) p.lse[at] = (m * c + __log2f(l)) * kLn2;
+    if (p.lse && d == 0) p.lse[at] = (m * c + (__log2f(l) - kLift)) * kLn2;
 }
 
 // -------------------------------------------------------------------- host

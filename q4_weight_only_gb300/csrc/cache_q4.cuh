@@ -13,6 +13,13 @@ namespace q4_0 {
 
 namespace {
 
+// log2 of the unit in which a row's p, l and O are held.  p is at most 2^8 (what
+// a reference lets it grow to), so 2^7 of it are 2^15 in binary16, and p is normal
+// there down to 2^-21.  Without it what is below 2^-14 loses 2^-25, and below
+// 2^-25 all of itself: a prompt's rows after 262144 tokens of 2^-25.6 of the
+// first one's weight each, 0.5 % together, then had no weight but the first's.
+constexpr float kLift = 7.f;
+
 // The cache as the attention kernels take it.
 struct CacheQ4 {
     KvQ4View c;
