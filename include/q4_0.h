@@ -85,8 +85,8 @@ size_t q4_0_weight_bytes(int64_t N, int64_t K);
  * index on ties) / -8 in fp32; the stored scale is d rounded to binary16
  * (nearest, ties to even); each code is q = clamp(round(w / d) + 8, 0, 15)
  * with the fp32 d, IEEE division and round-half-away-from-zero; an all-zero
- * block stores d = +0 and codes 8.  Codes match the library's CPU reference
- * bit for bit.
+ * block stores d = +0 and codes 8, and where d underflows to 0 the codes are 8
+ * too.  Codes match the library's CPU reference bit for bit.
  * Alignment: w 16 bytes; wq 2 bytes.
  * Returns Q4_0_OK, Q4_0_ERR_INVALID_ARG or Q4_0_ERR_CUDA.
  */

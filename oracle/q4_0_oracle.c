@@ -20,7 +20,7 @@
  *     the design notes): first index wins a tie on max-|w|; d is formed in
  *     fp32 and w is divided by that fp32 d (correctly rounded IEEE division);
  *     round() is half-away-from-zero; an all-zero block stores d = +0 and
- *     codes 8; the stored scale is fp32 d rounded to binary16, nearest-even.
+ *     codes 8, and so are the codes where d underflows to 0; the stored scale is fp32 d rounded to binary16, nearest-even.
  *   - The matmul is the plain definition y[m,n] = sum_k w[n,k] * x[m,k] with
  *     w decoded exactly into fp64 and x (bf16) widened exactly, summed in fp64
  *     in ascending k.
@@ -163,7 +163,8 @@ static void oracle_quantize_block(const float *w, uint8_t *out) {
         d = (float)oracle_f16_bits_to_f64(dbits); /* mutant: divide by the stored fp16 d */
 #endif
         for (int j = 0; j < ORACLE_QK; ++j) {
-            float r = w[j] / d;
+            /* a d that underflowed to 0 has no quotients: code 8 */
+            float r = d != 0.0f ? w[j] / d : 0.0f;
             int c = (int)oracle_round_half_away(r) + 8;
             if (c < 0) c = 0;
 #if ORACLE_MUTANT == 11

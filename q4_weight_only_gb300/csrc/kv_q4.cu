@@ -10,7 +10,8 @@
 // 32 elements w of a head is then
 //   d = (w of the largest |w|, the first of equals) / -8,
 //   code = clamp(round(w / d) + 8, 0, 15), halves away from zero,
-// with d in fp32 for the codes and rounded to binary16 for the cache: the
+// and 8 where d is 0 (elements of 2^-147 and less in size), with d in fp32 for
+// the codes and rounded to binary16 for the cache: the
 // rules of the weights' quantizer (quantize.cu), element j of a block in the
 // low half of byte j, j + 16 in its high half.  A block reads back as
 // d (code - 8), exactly in fp32.
@@ -66,8 +67,7 @@ __device__ __forceinline__ void turn(float &a, float &b, float cosv, float sinv)
     b = __fadd_rn(__fmul_rn(b, cosv), __fmul_rn(a0, sinv));
 }
 
-// clamp(round(w / d), -8, 7) + 8, halves away from zero (0 / 0 and a d that
-// became 0 give codes that its scale of 0 makes no difference of).
+// clamp(round(w / d), -8, 7) + 8, halves away from zero; d is not 0.
 __device__ __forceinline__ uint32_t code_of(float w, float d) {
     return (uint32_t)(int)(fminf(fmaxf(roundf(__fdiv_rn(w, d)), -8.f), 7.f) + 8.f);
 }
@@ -132,7 +132,7 @@ __device__ __forceinline__ void quantise_quad(float4 u, float4 v, int j, uint32_
         const float d = __fmul_rn(value, -0.125f);
         s = __half_as_ushort(__float2half_rn(d));
         const float e[8] = {u.x, v.x, u.y, v.y, u.z, v.z, u.w, v.w};
-        w = codes_of(e, d);
+        if (d != 0.f) w = codes_of(e, d);
     }
     *reinterpret_cast<uint32_t *>(codes + 4 * j) = w;
     if (j == 0) *scale = s;

@@ -5,7 +5,8 @@
 // one Q4_0 weight format.  This kernel writes that format: per block of 32
 // weights, d = (signed max-|w| element, first index on ties) / -8 in fp32,
 // stored as binary16 (round to nearest even); q = clamp(round(w / d) + 8, 0,
-// 15) with the fp32 d, IEEE division and round-half-away-from-zero; byte
+// 15) with the fp32 d, IEEE division and round-half-away-from-zero, and 8 where
+// d is 0 (weights of 2^-147 and less in size); byte
 // 2 + j holds q[j] in its low nibble and q[j + 16] in its high nibble.
 // Off the hot path (once per weight load); one thread per block.
 //
@@ -50,7 +51,9 @@ __global__ void __launch_bounds__(256) quantize_kernel(const float *__restrict__
         dbits = __half_as_ushort(__float2half_rn(d));
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-            int c = (int)roundf(__fdiv_rn(v[j], d)) + 8;
+            // a d that underflowed to 0 has no quotients
+            const float r = d == 0.0f ? 0.0f : __fdiv_rn(v[j], d);
+            int c = (int)roundf(r) + 8;
             c = c < 0 ? 0 : (c > 15 ? 15 : c);
             q[j] = (uint32_t)c;
         }
