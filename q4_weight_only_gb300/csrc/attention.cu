@@ -54,15 +54,18 @@
 //   the last product and the rows' stores.  With 40 heads on 8, D = 128, they
 //   take 265 us.
 // * One token after 2047 takes 16.7 us against a floor of 1.2: 4.3 launch, 4
-//   join, the rest reads that wait for one another.
+//   join, the rest reads that wait for one another.  (Of a row of such calls,
+//   whose launches overlap, each takes 14.6.)
 //
 // A cache in Q4_0 blocks (attention_q4_wide_kernel; sequences of few rows are
 // attention_q4.cu's).  The same warps, and four more: codes and scales come
 // through a ring of their own, warps 12 to 15 unpack tiles of binary16 from it
 // into the ring that the MMAs read, and the softmax warps turn their rows of Q
-// to binary16.  The copies are a quarter of the bytes; what bounds a tile is
-// the unpacking and what it costs the others:
-// * 8192 tokens after 8192 others take 1.55 ms, 1.33 PFLOP/s; 1.43 with the
+// to binary16.  p is binary16 too, held times 2^7 (kLift) as l and O are.  The
+// copies are a quarter of the bytes; what bounds a tile is the unpacking and
+// what it costs the others:
+// * 8192 tokens after 8192 others take 1.56 ms, 1.33 PFLOP/s (of a row of
+//   replayed calls; one call among others 1.60); 1.43 with the
 //   unpacking left out, 1.36 without the copies too (timing only).  Its warps
 //   work 2240 of a pair of tiles' 3600 cycles, their stores of 64 KB compete
 //   with the MMAs' reads for shared memory, and their code with the softmax's
@@ -74,7 +77,7 @@
 //   copies.  Turning a Q to binary16, and its scores waiting for that, take 5000
 //   cycles an item.
 // * 5 drafted tokens of 16 sequences under a window of 4096: 61 us (bfloat16:
-//   60), 39 without unpacking and copies.
+//   58), 39 without unpacking and copies.
 // * Not faster: rings of 3 unpacked tiles and 6 of codes instead of 4 and 3 (D
 //   = 64: 6 and 12 instead of 8 and 6; prompts 3 % slower, the others level); Q
 //   turned by the unpacking warps (windowed prompts 193 -> 206 us, a prompt of
@@ -229,7 +232,11 @@ struct Layout {
     static constexpr int kSmem = kBars + kStatBytes + 1024;  // + alignment
 };
 
-constexpr int kItems = 4;     // items handed out ahead
+// Items handed out ahead.  A warp that copies looks for the next item's tiles
+// while it holds tiles of this one: the item that the next one takes the place
+// of must not need them.
+constexpr int kItems = 4;
+static_assert(kItems >= 2, "");
 
 constexpr int kMaxQTiles = 4;
 
@@ -1245,7 +1252,9 @@ void fill_params(Params &p, const AttentionArgs &a, const View &c, void *workspa
     p.out = a.out, p.lse = a.lse, p.out_bf16 = a.out_bf16;
     p.max_q_len = a.max_q_len;
     // Where both kinds of item can meet, a key tile of two tiles takes about
-    // 1.7 us and one of a narrow item 1.2.
+    // 1.7 us and one of a narrow item 1.2.  (Read from L2, 1.57 and 1.00, at D =
+    // 64 1.27 and 0.81.  In 4 bits, where both are unpacked whole, the two are
+    // nearer to one another: 1.79 and 1.40, 1.59 and 1.16.)
     const bool mixed = a.max_q_len > p.tokens;
     p.cost[0] = mixed ? 2 : 1, p.cost[1] = mixed ? 3 : 1;
     p.piece_rows = item_rows(p.group, a.max_q_len);

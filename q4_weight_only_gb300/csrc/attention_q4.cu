@@ -13,24 +13,28 @@
 // Operands of the tensor cores are binary16:
 // * a key's codes, exactly, as the numbers below binary16's normal range that
 //   their bits are where they lie; its blocks' scales multiply the blocks' dot
-//   products in fp32, and one more product takes the codes' 8 too many off;
+//   products in fp32, and one more product takes the codes' 8 too many off (as
+//   two binary16 parts, 2^-23 of what they hold);
 // * a value d (code - 8), rounded (2^-11): the format holds elements up to
 //   65504;
 // * a query row times a power of two that brings its largest element to
-//   [2^14, 2^15), undone in c: exact for every element within 2^29 of the
-//   largest, off by at most 2^-39 of that below;
+//   [2^14, 2^15), undone in c: exact for every element within 2^31 of the
+//   largest, off by at most 2^-39 of that below; elements that meet high
+//   nibbles, read as 16 codes, a sixteenth of that: exact within 2^27, off by at
+//   most 2^-35 below;
 // * p, at most 2^8, times 2^7, rounded (2^-11 of p, and 2^-32 where p is below
 //   2^-21); l sums it before the rounding.
 //
-// Two kernels.  Sequences of at most 16 rows, (token, head of the group) pairs,
-// are this file's: their few rows are the narrow operand of m16n8k16 products
-// with the keys and values as the wide one, which warps unpack straight from
-// the codes into their registers.  Nothing unpacked is written anywhere, and
-// a tcgen05 operand in shared memory is not worth it for codes that so few rows
-// use: 64 sequences' next tokens take twice as long there (353 and 700 us).
-// Longer sequences fill tcgen05's tiles of 128 rows and are attention.cu's
-// 4-bit variant: 16 sequences' 5 drafted tokens by 5 heads, 25 rows each, take
-// 61 us there, and 85 as two items of 16 here.
+// Two kernels.  Sequences of few rows, (token, head of the group) pairs, are this
+// file's: at most 8 in a call whose bound is above 16 and whose groups have at
+// most 8 heads, else at most 16 (item_rows).  Their rows are the narrow operand
+// of m16n8k16 products with the keys and values as the wide one, which warps
+// unpack straight from the codes into their registers.  Nothing unpacked is
+// written anywhere, and a tcgen05 operand in shared memory is not worth it for
+// codes that so few rows use: 64 sequences' next tokens take twice as long there
+// (353 and 700 us).  Longer sequences fill tcgen05's tiles of 128 rows and are
+// attention.cu's 4-bit variant: 16 sequences' 5 drafted tokens by 5 heads, 25
+// rows each, take 61 us there, and 85 as two items of 16 here.
 //
 // Layout of work: an item is 8 or 16 rows of one sequence and key head, its
 // cost the key tiles it sees; CTAs, one an SM, take equal shares of all cost,
@@ -43,9 +47,9 @@
 //   alone take 241 us and the arithmetic alone 258: 400 warp instructions for
 //   16 keys and values fill 60 % of the issue slots (logic and integers 49 %
 //   of their pipe, multiply-adds 36 %, tensor 20 %, HBM 50 %).
-// * 16 sequences of 1 to 8 thousand, 98 MB: 41 us (bfloat16: 69), of which 12
+// * 16 sequences of 1 to 8 thousand, 98 MB: 41 us (bfloat16: 68), of which 12
 //   are the launches, the first reads and the join.
-// * One token after 2047: 11.6 us (bfloat16: 14.7).
+// * One token after 2047: 11.7 us (bfloat16: 14.8).
 // * Pages that hold a head's tokens in a row are 12 % faster than pages that
 //   hold a token's heads in a row: a token's scales of one head are 8 bytes,
 //   and a sector of 32 holds four tokens' of the head then (605 against 807 MB
@@ -846,13 +850,17 @@ __global__ void __launch_bounds__(256) attention_q4_join_kernel(const __grid_con
 
 // -------------------------------------------------------------------- host
 
-// Rows (tokens times heads of the group) of the sequences that this kernel
+// The most rows (tokens times heads of the group) of a sequence that this kernel
 // takes; those of longer ones fill tcgen05's tiles (attention.cu).
 constexpr int kMostRows = 16;
 
-// Rows of an item, and the most of a sequence that this kernel takes: one tile
-// of 8 where single tokens need no more and no sequence brings 9 to 16, which
-// two tiles serve best.
+// Rows of an item, and the most of a sequence that this kernel takes: 16 where
+// no sequence can bring more, or one token's heads need it; else one tile of 8,
+// for the single tokens of a mixed batch.  That sends sequences of 9 to 16 rows
+// beside longer ones to tcgen05, whose launch such a call makes anyway.  Two
+// items of 8 for each of them instead: 16 drafts of 2 or 3 tokens by 5 heads
+// after 8192 beside a chunk of 256 156 -> 165 us, without the chunk level (107
+// and 105 to 108), 64 of them after 16384 669 -> 593.
 int item_rows(int group, int max_q_len) {
     const int64_t most = (int64_t)group * max_q_len;
     return most <= 8 || (most > kMostRows && group <= 8) ? 8 : kMostRows;

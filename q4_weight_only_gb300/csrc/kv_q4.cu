@@ -299,8 +299,12 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, float4 a, float4 b) {
 }
 
 // Rows of a CTA, of whose places each warp finds one or two: 16 where there are
-// enough of them to fill the SMs (82 thousand rows take 68 us, with 8 rows 70;
-// 515 rows 3.7 us with 8, with 16 rows 5.3).
+// enough of them to fill the SMs.  With 8 and with 16 rows, to bfloat16, us:
+//   rows           515         4096        16384        32768        65536
+//   8 x 128     3.7, 5.2     6.5, 7.3   17.0, 18.4   30.3, 30.5   56.9, 55.3
+//   4 x 64      2.9, 3.6     4.2, 4.4    9.5, 8.0    18.3, 14.5   34.1, 26.1
+//   32 x 128    7.0, 11.8   18.6, 21.7  55.3, 61.3  104.9, 107.9
+// The two cross between 5 thousand rows (small ones) and 50 thousand.
 constexpr int kReadRows = 8, kMostReadRows = 16, kManyRows = 16384;
 
 // blockIdx.x: `per_cta` rows of the batch.  A thread reads half a block (8
