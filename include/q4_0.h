@@ -537,6 +537,8 @@ int q4_0_kv_read_q4(void *k_out, void *v_out, int out_type, int64_t rows, const 
  * products are binary16: a row of q scaled by a power of two, elements of the
  * cache and exponentials rounded once (exponentials to 2^-11, and no finer than
  * 2^-32 of the row's largest).
+ * Where scale times a row's largest |q| is past 2^116 its lse may be too small
+ * in size.
  * Workspace: q4_0_attention_q4_workspace_bytes(...) bytes on the current
  * device, 256-byte aligned, in use until the work on `stream` completes.
  * Returns as q4_0_attention.

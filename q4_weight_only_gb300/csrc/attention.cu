@@ -865,7 +865,7 @@ __device__ __forceinline__ void attend(const CUtensorMap &qmap, const CUtensorMa
                 }
             }
             // scale * log2 e, and the next power of two, for the row as it is
-            auto c_of = [&](float scale) { return kQ4 ? fminf(scale * bar.q_down[half][row], 3e38f) : scale; };
+            auto c_of = [&](float scale) { return kQ4 ? in_range(scale * bar.q_down[half][row]) : scale; };
             // A row whose maximum grew moves the references of its warp's
             // rows (each its own, one by one, took prompts 1 to 4 % longer).
             // Lanes that are no row of the item must not: they hold other

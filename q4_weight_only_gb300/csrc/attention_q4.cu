@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int up = top > 0.f && top < INFINITY ? min(14 - exponent, 100) : 0;
             const float f = __uint_as_float((uint32_t)(127 + up) << 23);
             const float down = __uint_as_float((uint32_t)(127 - up) << 23);
-            const float row_c = fminf(p.scale_log2 * (down * kCodeUnit), 3e38f);
+            const float row_c = in_range(p.scale_log2 * (down * kCodeUnit));
 #pragma unroll
             for (int x = 0; x < 2; ++x) cs[n][x] = __shfl_sync(0xffffffffu, row_c, (2 * t + x) * 4);
             auto pair = [&](float a, float z, float f) { return pack_f16(a * f, z * f); };

@@ -20,6 +20,12 @@ namespace {
 // first one's weight each, 0.5 % together, then had no weight but the first's.
 constexpr float kLift = 7.f;
 
+// A row's c with what undoes its scaling in it, within fp32's normal range: an
+// infinite one, or one that underflowed to 0, would make NaN of a score that is
+// 0 or masked (0 times infinity).  At the lower end every exponent is 0 either
+// way: scores are below 2^40.
+__device__ __forceinline__ float in_range(float c) { return fmaxf(fminf(c, 3e38f), 0x1p-126f); }
+
 // The cache as the attention kernels take it.
 struct CacheQ4 {
     KvQ4View c;
