@@ -64,8 +64,8 @@
 // to binary16.  p is binary16 too, held times 2^7 (kLift) as l and O are.  The
 // copies are a quarter of the bytes; what bounds a tile is the unpacking and
 // what it costs the others:
-// * 8192 tokens after 8192 others take 1.56 ms, 1.33 PFLOP/s (of a row of
-//   replayed calls; one call among others 1.60); 1.43 with the
+// * 8192 tokens after 8192 others take 1.56 ms, 1.32 PFLOP/s (of a row of
+//   replayed calls; one call among others 1.59); 1.43 with the
 //   unpacking left out, 1.36 without the copies too (timing only).  Its warps
 //   work 2240 of a pair of tiles' 3600 cycles, their stores of 64 KB compete
 //   with the MMAs' reads for shared memory, and their code with the softmax's

@@ -32,8 +32,8 @@ def batch(new, dim, best):
 
 
 @pytest.mark.parametrize("dim", [64, 128])
-@pytest.mark.parametrize("new", [1, 4, 60])
-@pytest.mark.parametrize("size", [10, 18, 20.3, 23, 25, 25.99, 26, 26.01, 27.5, 30])
+@pytest.mark.parametrize("new", [1, 60])
+@pytest.mark.parametrize("size", [10, 20.3, 25.99, 26.01, 30])
 @pytest.mark.parametrize("sign", [1.0, -1.0])
 def test_large_scores(size, new, dim, sign):
     """c s of 2^size (times 7/8 where it is the lesser of two that counts)."""
@@ -59,7 +59,7 @@ def test_large_scores(size, new, dim, sign):
 
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("new", [1, 4, 60])
-@pytest.mark.parametrize("q_size,scale", [(1e-30, 1e-30), (1e-38, 1e-20), (1e-30, 1.0), (1.0, 1e-38), (1.0, 1e-44)])
+@pytest.mark.parametrize("q_size,scale", [(1e-30, 1e-30), (1e-38, 1e-20), (1.0, 1e-44)])
 def test_products_that_underflow(q_size, scale, new, dim):
     """Scores of next to nothing: every key that is seen counts the same, and
     what is not seen does not."""
